@@ -20,11 +20,20 @@ BSG_OUT_BF16 = 0
 BSG_OUT_F32 = 1
 BSG_DGRAD_NN = 2
 BSG_WGRAD_NT_E5M2 = 3
+BSG_OUT_F16 = 2
+BSG_IN_BF16 = 0
+BSG_IN_F16 = 1
+BSG_GRAD_BF16 = 0
+BSG_GRAD_F16 = 1
+BSG_GRAD_F32 = 2
+BSG_MAX_LORA_RANK = 256
 BSG_MAX_GROUPS = 256
 BSG_COLWISE_PAD = 128
 DEV_NEGATIVE_SIZE = 1
 DEV_OVER_CAPACITY = 2
 DEV_BAD_PADDING = 4
+DEV_NONFINITE = 8
+DEV_BAD_ADAPTER = 16
 
 EXPORTS = ("bsg_last_error", "bsg_version", "group_offsets_i32_to_i64", "grouped_quantize_mxfp8",
            "grouped_quantize_mxfp8_rowwise_e5m2",
@@ -37,7 +46,10 @@ EXPORTS = ("bsg_last_error", "bsg_version", "group_offsets_i32_to_i64", "grouped
            "grouped_gemm_nvfp4_rowscaled_ex", "grouped_gemm_nvfp4_rowscaled_wgrad_ex",
            "grouped_gemm_mxfp8_workspace_size", "grouped_gemm_mxfp8_ws",
            "grouped_gemm_nvfp4_workspace_size", "grouped_gemm_nvfp4_rowscaled_ws",
-           "grouped_gemm_nvfp4_pertensor_ws")
+           "grouped_gemm_nvfp4_pertensor_ws",
+           "grouped_gemm_16bit_workspace_size", "grouped_gemm_16bit",
+           "grouped_lora_gemm_16bit_workspace_size", "grouped_lora_gemm_16bit",
+           "grad_clip_plan_fill", "grad_clip_workspace_size", "grad_norm", "clip_grad_norm")
 BSG_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 _lib = None
@@ -119,6 +131,25 @@ def load_library(path=LIB_PATH):
     lib.grouped_gemm_nvfp4_rowscaled_wgrad.restype = I32
     lib.grouped_gemm_nvfp4_rowscaled_wgrad.argtypes = [I64, P, P, P, P, P, P, P, I64, I64, I64, P,
                                                        I32, P, P]
+    SZ = ctypes.c_size_t
+    lib.grouped_gemm_16bit_workspace_size.restype = SZ
+    lib.grouped_gemm_16bit_workspace_size.argtypes = []
+    lib.grouped_gemm_16bit.restype = I32
+    lib.grouped_gemm_16bit.argtypes = [I32, I32, I64, P, I64, P, I64, I64, P, I64, I64, I64, P, P,
+                                       I64, I64, I32, P, SZ, P, P]
+    lib.grouped_lora_gemm_16bit_workspace_size.restype = SZ
+    lib.grouped_lora_gemm_16bit_workspace_size.argtypes = [I64, I64, I64, I64]
+    lib.grouped_lora_gemm_16bit.restype = I32
+    lib.grouped_lora_gemm_16bit.argtypes = [I32, I64, P, I64, P, I64, P, P, I64, I64, P, P, P, I64,
+                                            I64, I64, P, I64, I32, P, SZ, P, P]
+    lib.grad_clip_plan_fill.restype = I32
+    lib.grad_clip_plan_fill.argtypes = [I64, P, P, P, P, P, SZ, P]
+    lib.grad_clip_workspace_size.restype = SZ
+    lib.grad_clip_workspace_size.argtypes = []
+    lib.grad_norm.restype = I32
+    lib.grad_norm.argtypes = [P, I64, P, SZ, P, P, P, P]
+    lib.clip_grad_norm.restype = I32
+    lib.clip_grad_norm.argtypes = [P, I64, ctypes.c_float, P, P, SZ, P, P, P]
     _lib = lib
     return lib
 
@@ -464,13 +495,16 @@ def _mx_gemm_check(mode, G, a, a_scales, b, b_scales, offsets, rows_cap, n, k, o
 
 def gemm_workspace(device=None):
     """A uint8 device tensor of max(grouped_gemm_mxfp8_workspace_size(),
-    grouped_gemm_nvfp4_workspace_size()) bytes (256-byte aligned: torch's caching
-    allocator aligns blocks to 512), for the `workspace` argument of
-    grouped_gemm_mxfp8, grouped_gemm_nvfp4_rowscaled and grouped_gemm_nvfp4_pertensor."""
+    grouped_gemm_nvfp4_workspace_size(), grouped_gemm_16bit_workspace_size()) bytes
+    (256-byte aligned: torch's caching allocator aligns blocks to 512), for the
+    `workspace` argument of grouped_gemm_mxfp8, grouped_gemm_nvfp4_rowscaled,
+    grouped_gemm_nvfp4_pertensor and grouped_gemm_16bit.  Calls that may run at the
+    same time (on different streams) need a workspace each."""
     import torch
     lib = load_library()
     n = max(int(lib.grouped_gemm_mxfp8_workspace_size()),
-            int(lib.grouped_gemm_nvfp4_workspace_size()))
+            int(lib.grouped_gemm_nvfp4_workspace_size()),
+            int(lib.grouped_gemm_16bit_workspace_size()))
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
@@ -691,3 +725,245 @@ def grouped_gemm_nvfp4_rowscaled_wgrad(a, a_scales, a_outer, b, b_scales, b_oute
         G, _ptr(a), _ptr(a_scales), _ptr(a_outer), _ptr(b), _ptr(b_scales), _ptr(b_outer),
         _ptr(padded_offsets), col_rows_cap, n, k, _ptr(out), out_dtype, _ptr(status), _stream(a)))
     return out
+
+
+def _types_16bit(t, name, out_dtype):
+    """(in_dtype, out_dtype code, torch output type) of a 16-bit operand; out_dtype None: its own."""
+    import torch
+    if t.dtype == torch.bfloat16:
+        code, same = BSG_IN_BF16, BSG_OUT_BF16
+    elif t.dtype == torch.float16:
+        code, same = BSG_IN_F16, BSG_OUT_F16
+    else:
+        raise ValueError("%s must be bfloat16 or float16, not %s" % (name, _dtype_name(t.dtype)))
+    if out_dtype is None or out_dtype == same:
+        return code, same, t.dtype
+    if out_dtype == BSG_OUT_F32:
+        return code, out_dtype, torch.float32
+    raise ValueError("out_dtype %r is neither the operands' type nor BSG_OUT_F32" % (out_dtype,))
+
+
+def _strided(t, name, dims, dtype):
+    """Row (and matrix) strides of a tensor whose rows are contiguous: (ld, stride).  A size-1
+    dimension's stride is never used and torch leaves it arbitrary, so a dense one stands in."""
+    if t.dim() != dims:
+        raise ValueError("%s must be %d-D, not %d-D" % (name, dims, t.dim()))
+    if not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, not %s" % (name, _dtype_name(dtype), _dtype_name(t.dtype)))
+    shape, st = t.shape, t.stride()
+    cols, rows = shape[-1], shape[-2]
+    if st[-1] != 1 and cols > 1:
+        raise ValueError("the rows of %s must be contiguous" % name)
+    ld = st[-2] if rows > 1 else max(cols, 1)
+    if dims == 2:
+        return ld, 0
+    return ld, (st[0] if shape[0] > 1 else rows * ld)
+
+
+def _same_device(ref, **others):
+    for name, t in others.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, ref.device))
+
+
+def _out_or_new(out, shape, dtype, ref, name="out"):
+    import torch
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=ref.device)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError("%s is %s; the call writes %s" % (name, tuple(out.shape), tuple(shape)))
+    return out
+
+
+def grouped_gemm_16bit(mode, a, b, offsets, c=None, out=None, out_dtype=None, workspace=None,
+                       status=None):
+    """Grouped products of bf16 or fp16 operands over the row groups of `offsets`:
+
+    BSG_FPROP_TN  a [rows, k], b [G, n, k]  -> [rows, n]: group g's rows times b[g]^T
+    BSG_DGRAD_NN  a [rows, k], b [G, k, n]  -> [rows, n]: group g's rows times b[g]
+    BSG_WGRAD_NT  a [rows, n], b [rows, k]  -> [G, n, k]: a^T b over group g's rows
+
+    c: an addend in the output's type and shape (pass the same tensor as `out` to
+    accumulate).  out_dtype: None (the operands' type) or BSG_OUT_F32.  Rows may be
+    strided (strides multiples of 8 elements).  See include/bsg.h."""
+    lib = load_library()
+    code, od, odt = _types_16bit(a, "a", out_dtype)
+    lda, _ = _strided(a, "a", 2, a.dtype)
+    _req(offsets, "offsets", 16, _i64())
+    G = offsets.numel() - 1
+    rows = a.shape[0]
+    if mode == BSG_WGRAD_NT:
+        ldb, stride_b = _strided(b, "b", 2, a.dtype)
+        n, k = a.shape[1], b.shape[1]
+        if b.shape[0] != rows:
+            raise ValueError("a has %d rows, b has %d" % (rows, b.shape[0]))
+        shape = (G, n, k)
+    elif mode in (BSG_FPROP_TN, BSG_DGRAD_NN):
+        ldb, stride_b = _strided(b, "b", 3, a.dtype)
+        k = a.shape[1]
+        n = b.shape[1] if mode == BSG_FPROP_TN else b.shape[2]
+        if b.shape[0] != G or b.shape[2 if mode == BSG_FPROP_TN else 1] != k:
+            raise ValueError("b is %s; %d groups contracting %d are needed" % (tuple(b.shape), G, k))
+        shape = (rows, n)
+    else:
+        raise ValueError("mode %r has no 16-bit product" % (mode,))
+    out = _out_or_new(out, shape, odt, a)
+    ldo, stride_o = _strided(out, "out", len(shape), odt)
+    if c is not None:
+        if tuple(c.shape) != shape:
+            raise ValueError("c is %s; the output is %s" % (tuple(c.shape), shape))
+        if _strided(c, "c", len(shape), odt) != (ldo, stride_o):
+            raise ValueError("c must have the strides of out")
+    _same_device(a, b=b, offsets=offsets, c=c, out=out, workspace=workspace, status=status)
+    _req(status, "status", 4, optional=True)
+    wbytes = 0
+    if workspace is not None:
+        _req(workspace, "workspace", 0)
+        wbytes = workspace.numel() * workspace.element_size()
+    if n == 0 or k == 0:
+        raise ValueError("n and k must be positive")
+    if out.numel() == 0:
+        return out
+    _check(lib.grouped_gemm_16bit(mode, code, G, _ptr(a) or _ptr(out), lda,
+                                  _ptr(b) or _ptr(out), ldb, stride_b, _ptr(offsets), rows, n, k,
+                                  _ptr(c), _ptr(out), ldo, stride_o, od, _ptr(workspace), wbytes,
+                                  _ptr(status), _stream(a)))
+    return out
+
+
+def grouped_lora_gemm_16bit_workspace(rows_cap, n, k, rank, device=None):
+    """A uint8 device tensor for the `workspace` argument of grouped_lora_gemm_16bit."""
+    import torch
+    nbytes = int(load_library().grouped_lora_gemm_16bit_workspace_size(rows_cap, n, k, rank))
+    if nbytes == 0:
+        raise ValueError("no workspace for rows_cap=%r, n=%r, k=%r, rank=%r" % (rows_cap, n, k, rank))
+    return torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+def grouped_lora_gemm_16bit(x, w, lora_a, lora_b, offsets, adapter, scale, out=None, out_dtype=None,
+                            workspace=None, status=None):
+    """x w^T plus, for the rows of request g (offsets[g] .. offsets[g+1]) with adapter
+    a = adapter[g] >= 0, scale[a] (x lora_a[a]^T) lora_b[a]^T -> [rows, n].
+
+    x [rows, k], w [n, k] (rows may be strided), lora_a [adapters, rank, k] and lora_b
+    [adapters, n, rank] of one 16-bit type; adapter int32 [G], scale float32 [adapters].
+    workspace: grouped_lora_gemm_16bit_workspace(rows, n, k, rank), or None for a new
+    one.  See include/bsg.h."""
+    import torch
+    lib = load_library()
+    code, od, odt = _types_16bit(x, "x", out_dtype)
+    ldx, _ = _strided(x, "x", 2, x.dtype)
+    ldw, _ = _strided(w, "w", 2, x.dtype)
+    (rows, k), n = x.shape, w.shape[0]
+    if lora_a.dim() != 3 or lora_b.dim() != 3:
+        raise ValueError("lora_a and lora_b must be 3-D")
+    count, rank = lora_a.shape[0], lora_a.shape[1]
+    if w.shape[1] != k or lora_a.shape[2] != k or tuple(lora_b.shape) != (count, n, rank):
+        raise ValueError("x %s, w %s, lora_a %s and lora_b %s do not fit" % (
+            tuple(x.shape), tuple(w.shape), tuple(lora_a.shape), tuple(lora_b.shape)))
+    _req(offsets, "offsets", 16, torch.int64)
+    G = offsets.numel() - 1
+    _req(adapter, "adapter", 4 * G, torch.int32)
+    _req(scale, "scale", 4 * count, torch.float32)
+    _req(lora_a, "lora_a", 0, x.dtype)
+    _req(lora_b, "lora_b", 0, x.dtype)
+    _req(status, "status", 4, optional=True)
+    out = _out_or_new(out, (rows, n), odt, x)
+    ldo, _ = _strided(out, "out", 2, odt)
+    if workspace is None:
+        workspace = grouped_lora_gemm_16bit_workspace(rows, n, k, rank, x.device)
+    _req(workspace, "workspace", 0)
+    _same_device(x, w=w, lora_a=lora_a, lora_b=lora_b, offsets=offsets, adapter=adapter, scale=scale,
+                 out=out, workspace=workspace, status=status)
+    if rows == 0:
+        return out
+    _check(lib.grouped_lora_gemm_16bit(code, G, _ptr(x), ldx, _ptr(w), ldw, _ptr(lora_a),
+                                       _ptr(lora_b), count, rank, _ptr(offsets), _ptr(adapter),
+                                       _ptr(scale), rows, n, k, _ptr(out), ldo, od, _ptr(workspace),
+                                       workspace.numel() * workspace.element_size(), _ptr(status),
+                                       _stream(x)))
+    return out
+
+
+class GradClipPlan:
+    """The chunk table of a set of gradients on the device, and the workspace of its calls.
+
+    Valid while the tensors stay where they are; it keeps them alive.  Calls on one plan
+    share its workspace: run them on one stream at a time."""
+
+    def __init__(self, tensors, outs, table, num_chunks, workspace):
+        self.tensors, self.outs = tensors, outs
+        self.table, self.num_chunks, self.workspace = table, num_chunks, workspace
+
+
+def grad_clip_plan(tensors, outs=None, device=None):
+    """Plan for grad_norm and clip_grad_norm over contiguous bf16, fp16 or float32 device
+    tensors (any number, any sizes, aligned to their elements).  outs: where the clipped
+    gradients go (same types and sizes); None clips in place.  device: needed only where
+    there are no tensors."""
+    import torch
+    lib = load_library()
+    tensors = list(tensors)
+    outs = tensors if outs is None else list(outs)
+    if len(outs) != len(tensors):
+        raise ValueError("%d tensors and %d outputs" % (len(tensors), len(outs)))
+    codes = {torch.bfloat16: BSG_GRAD_BF16, torch.float16: BSG_GRAD_F16, torch.float32: BSG_GRAD_F32}
+    for i, (t, o) in enumerate(zip(tensors, outs)):
+        _req(t, "tensor %d" % i, 0, tuple(codes))
+        _req(o, "output %d" % i, 0, t.dtype)
+        if o.numel() != t.numel():
+            raise ValueError("tensor %d has %d elements, its output %d" % (i, t.numel(), o.numel()))
+        _same_device(tensors[0], **{"tensor %d" % i: t, "output %d" % i: o})
+    count = len(tensors)
+    src = (ctypes.c_void_p * max(count, 1))(*[t.data_ptr() for t in tensors])
+    dst = (ctypes.c_void_p * max(count, 1))(*[o.data_ptr() for o in outs])
+    numels = (ctypes.c_int64 * max(count, 1))(*[t.numel() for t in tensors])
+    dtypes = (ctypes.c_int32 * max(count, 1))(*[codes[t.dtype] for t in tensors])
+    chunks = ctypes.c_int64(0)
+    _check(lib.grad_clip_plan_fill(count, src, dst, numels, dtypes, None, 0, ctypes.byref(chunks)))
+    nbytes = 24 * max(chunks.value, 1)
+    table = torch.zeros(nbytes, dtype=torch.uint8)
+    _check(lib.grad_clip_plan_fill(count, src, dst, numels, dtypes,
+                                   ctypes.c_void_p(table.data_ptr()), nbytes, ctypes.byref(chunks)))
+    dev = tensors[0].device if tensors else torch.device(device or "cuda")
+    workspace = torch.empty(int(lib.grad_clip_workspace_size()), dtype=torch.uint8, device=dev)
+    return GradClipPlan(tensors, outs, table.to(dev), chunks.value, workspace)
+
+
+def _grad_outputs(plan, norm, status):
+    import torch
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=plan.table.device)
+    _req(norm, "norm", 4, torch.float32)
+    _req(status, "status", 4, optional=True)
+    _same_device(plan.table, norm=norm, status=status)
+    return norm
+
+
+def grad_norm(plan, norm=None, sumsq=None, status=None):
+    """The 2-norm over all tensors of the plan (float32 scalar tensor).  sumsq: a float64
+    tensor that receives the sum of squares too (for sums over ranks)."""
+    import torch
+    norm = _grad_outputs(plan, norm, status)
+    _req(sumsq, "sumsq", 8, torch.float64, optional=True)
+    _same_device(plan.table, sumsq=sumsq)
+    _check(load_library().grad_norm(_ptr(plan.table), plan.num_chunks, _ptr(plan.workspace),
+                                    plan.workspace.numel(), _ptr(norm), _ptr(sumsq), _ptr(status),
+                                    _stream(plan.table)))
+    return norm
+
+
+def clip_grad_norm(plan, max_norm, sumsq=None, norm=None, status=None):
+    """Scales the plan's tensors by min(1, max_norm / (norm + 1e-6)) into its outputs and
+    returns the norm before it.  sumsq: a float64 tensor holding the sum of squares to go
+    by (e.g. grad_norm's, added over ranks); None computes it."""
+    import torch
+    norm = _grad_outputs(plan, norm, status)
+    _req(sumsq, "sumsq", 8, torch.float64, optional=True)
+    _same_device(plan.table, sumsq=sumsq)
+    _check(load_library().clip_grad_norm(_ptr(plan.table), plan.num_chunks, max_norm, _ptr(sumsq),
+                                         _ptr(plan.workspace), plan.workspace.numel(), _ptr(norm),
+                                         _ptr(status), _stream(plan.table)))
+    return norm

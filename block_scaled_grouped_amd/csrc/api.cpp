@@ -540,4 +540,229 @@ int grouped_gemm_nvfp4_rowscaled_wgrad_ex(int64_t G, const uint8_t* a, const uin
                        col_rows_cap, n, k, out, out_dtype, accumulate == 1, dev_status, stream);
 }
 
+namespace {
+
+constexpr int64_t kMaxRowStride = (int64_t)1 << 20;  // elements: a tile's rows stay in 31 bits
+
+bool row_stride_ok(int64_t ld, int64_t cols) {
+  return ld >= cols && ld % 8 == 0 && ld <= kMaxRowStride;
+}
+
+int check_16bit_types(const char* fn, int in_dtype, int out_dtype) {
+  if (in_dtype != BSG_IN_BF16 && in_dtype != BSG_IN_F16)
+    return fail(BSG_ERR_UNSUPPORTED, "%s: in_dtype %d", fn, in_dtype);
+  const int same = in_dtype == BSG_IN_F16 ? BSG_OUT_F16 : BSG_OUT_BF16;
+  if (out_dtype != same && out_dtype != BSG_OUT_F32)
+    return fail(BSG_ERR_UNSUPPORTED, "%s: out_dtype %d is neither the operands' type nor float32",
+                fn, out_dtype);
+  return BSG_OK;
+}
+
+int check_16bit_workspace(const char* fn, const void* workspace, size_t have, size_t need) {
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(BSG_ERR_ALIGN, "%s: workspace must be 256-byte aligned", fn);
+  if (have < need)
+    return fail(BSG_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, have, need);
+  return BSG_OK;
+}
+
+}  // namespace
+
+size_t grouped_gemm_16bit_workspace_size(void) { return bsg::gemm_16bit_workspace_bytes(); }
+
+int grouped_gemm_16bit(int mode, int in_dtype, int64_t G, const void* a, int64_t lda,
+                       const void* b, int64_t ldb, int64_t stride_b, const int64_t* offsets,
+                       int64_t rows_cap, int64_t n, int64_t k, const void* c, void* out,
+                       int64_t ldo, int64_t stride_o, int out_dtype, void* workspace,
+                       size_t workspace_bytes, uint32_t* dev_status, void* stream) {
+  const char* fn = "grouped_gemm_16bit";
+  if (a == nullptr || b == nullptr || offsets == nullptr || out == nullptr)
+    return fail(BSG_ERR_NULL, "%s: a, b, offsets and out must be non-NULL", fn);
+  if (mode != BSG_FPROP_TN && mode != BSG_WGRAD_NT && mode != BSG_DGRAD_NN)
+    return fail(BSG_ERR_UNSUPPORTED, "%s: mode %d", fn, mode);
+  const int tc = check_16bit_types(fn, in_dtype, out_dtype);
+  if (tc != BSG_OK) return tc;
+  if (G < 1 || G > BSG_MAX_GROUPS)
+    return fail(BSG_ERR_SHAPE, "%s: G=%lld outside [1, %d]", fn, (long long)G, BSG_MAX_GROUPS);
+  if (rows_cap < 0 || rows_cap >= ((int64_t)1 << 31) || n <= 0 || k <= 0 || n % 8 != 0 || k % 8 != 0)
+    return fail(BSG_ERR_SHAPE,
+                "%s: need 0 <= rows_cap < 2^31 and n, k positive multiples of 8 (got %lld, %lld, %lld)",
+                fn, (long long)rows_cap, (long long)n, (long long)k);
+  const bool wgrad = mode == BSG_WGRAD_NT;
+  const int64_t acols = wgrad ? n : k, bcols = mode == BSG_DGRAD_NN ? n : k;
+  const int64_t ocols = wgrad ? k : n;
+  if (!row_stride_ok(lda, acols) || !row_stride_ok(ldb, bcols) || !row_stride_ok(ldo, ocols))
+    return fail(BSG_ERR_SHAPE,
+                "%s: lda=%lld, ldb=%lld, ldo=%lld must be multiples of 8 in [row length, %lld]", fn,
+                (long long)lda, (long long)ldb, (long long)ldo, (long long)kMaxRowStride);
+  const int64_t brows = mode == BSG_DGRAD_NN ? k : n;
+  if (!wgrad && G > 1 && (stride_b % 8 != 0 || stride_b < (brows - 1) * ldb + bcols))
+    return fail(BSG_ERR_SHAPE, "%s: stride_b=%lld overlaps the groups or is no multiple of 8", fn,
+                (long long)stride_b);
+  if (wgrad && G > 1 && (stride_o % 8 != 0 || stride_o < (n - 1) * ldo + k))
+    return fail(BSG_ERR_SHAPE, "%s: stride_o=%lld overlaps the groups or is no multiple of 8", fn,
+                (long long)stride_o);
+  const int64_t tiles = wgrad ? G * ((n + 63) / 64) * ((k + 63) / 64)
+                              : ((rows_cap + 15) / 16 + G) * ((n + 63) / 64);
+  if (n >= kMaxTileBytes || k >= kMaxTileBytes || tiles >= ((int64_t)1 << 31))
+    return fail(BSG_ERR_SHAPE, "%s: too many output tiles", fn);
+  if (!aligned16(a) || !aligned16(b) || !aligned16(out) || !aligned16(c))
+    return fail(BSG_ERR_ALIGN, "%s: a, b, c and out must be 16-byte aligned", fn);
+  if (workspace != nullptr) {
+    const int wc = check_16bit_workspace(fn, workspace, workspace_bytes,
+                                         bsg::gemm_16bit_workspace_bytes());
+    if (wc != BSG_OK) return wc;
+  }
+  return hip_result(bsg::launch_gemm_16bit(mode, in_dtype == BSG_IN_F16, (int)G, a, lda, b, ldb,
+                                           stride_b, offsets, rows_cap, n, k, c, out, ldo, stride_o,
+                                           out_dtype == BSG_OUT_F32, workspace, dev_status,
+                                           (hipStream_t)stream),
+                    fn);
+}
+
+size_t grouped_lora_gemm_16bit_workspace_size(int64_t rows_cap, int64_t n, int64_t k, int64_t rank) {
+  if (rows_cap < 0 || n < 0 || k < 0 || rank < 0 || rank > BSG_MAX_LORA_RANK) return 0;
+  return bsg::lora_gemm_16bit_workspace_bytes(rows_cap, n, k, rank);
+}
+
+int grouped_lora_gemm_16bit(int in_dtype, int64_t G, const void* x, int64_t ldx, const void* w,
+                            int64_t ldw, const void* lora_a, const void* lora_b,
+                            int64_t num_adapters, int64_t rank, const int64_t* offsets,
+                            const int32_t* adapter, const float* scale, int64_t rows_cap,
+                            int64_t n, int64_t k, void* out, int64_t ldo, int out_dtype,
+                            void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                            void* stream) {
+  const char* fn = "grouped_lora_gemm_16bit";
+  if (x == nullptr || w == nullptr || lora_a == nullptr || lora_b == nullptr || offsets == nullptr ||
+      adapter == nullptr || scale == nullptr || out == nullptr || workspace == nullptr)
+    return fail(BSG_ERR_NULL, "%s: every buffer but dev_status must be non-NULL", fn);
+  const int tc = check_16bit_types(fn, in_dtype, out_dtype);
+  if (tc != BSG_OK) return tc;
+  if (G < 1 || G > BSG_MAX_GROUPS)
+    return fail(BSG_ERR_SHAPE, "%s: G=%lld outside [1, %d]", fn, (long long)G, BSG_MAX_GROUPS);
+  if (rows_cap < 0 || rows_cap >= ((int64_t)1 << 31) || n <= 0 || k <= 0 || n % 8 != 0 || k % 8 != 0)
+    return fail(BSG_ERR_SHAPE,
+                "%s: need 0 <= rows_cap < 2^31 and n, k positive multiples of 8 (got %lld, %lld, %lld)",
+                fn, (long long)rows_cap, (long long)n, (long long)k);
+  if (rank < 8 || rank > BSG_MAX_LORA_RANK || rank % 8 != 0)
+    return fail(BSG_ERR_SHAPE, "%s: rank=%lld is no multiple of 8 in [8, %d]", fn, (long long)rank,
+                BSG_MAX_LORA_RANK);
+  if (num_adapters < 1 || num_adapters >= ((int64_t)1 << 31))
+    return fail(BSG_ERR_SHAPE, "%s: num_adapters=%lld", fn, (long long)num_adapters);
+  if (!row_stride_ok(ldx, k) || !row_stride_ok(ldw, k) || !row_stride_ok(ldo, n))
+    return fail(BSG_ERR_SHAPE,
+                "%s: ldx=%lld, ldw=%lld, ldo=%lld must be multiples of 8 in [row length, %lld]", fn,
+                (long long)ldx, (long long)ldw, (long long)ldo, (long long)kMaxRowStride);
+  if (((rows_cap + 15) / 16 + 1) * ((n + 63) / 64) >= ((int64_t)1 << 31))
+    return fail(BSG_ERR_SHAPE, "%s: too many output tiles", fn);
+  if (!aligned16(x) || !aligned16(w) || !aligned16(lora_a) || !aligned16(lora_b) || !aligned16(out))
+    return fail(BSG_ERR_ALIGN, "%s: x, w, lora_a, lora_b and out must be 16-byte aligned", fn);
+  if (!aligned4(adapter) || !aligned4(scale))
+    return fail(BSG_ERR_ALIGN, "%s: adapter and scale must be 4-byte aligned", fn);
+  const int wc = check_16bit_workspace(
+      fn, workspace, workspace_bytes, bsg::lora_gemm_16bit_workspace_bytes(rows_cap, n, k, rank));
+  if (wc != BSG_OK) return wc;
+  return hip_result(
+      bsg::launch_lora_gemm_16bit(in_dtype == BSG_IN_F16, (int)G, x, ldx, w, ldw, lora_a, lora_b,
+                                  num_adapters, rank, offsets, adapter, scale, rows_cap, n, k, out,
+                                  ldo, out_dtype == BSG_OUT_F32, workspace, dev_status,
+                                  (hipStream_t)stream),
+      fn);
+}
+
+int grad_clip_plan_fill(int64_t num_tensors, const void* const* src, void* const* dst,
+                        const int64_t* numels, const int32_t* dtypes, void* plan,
+                        size_t plan_bytes, int64_t* num_chunks) {
+  const char* fn = "grad_clip_plan_fill";
+  if (num_chunks == nullptr || src == nullptr || dst == nullptr || numels == nullptr ||
+      dtypes == nullptr)
+    return fail(BSG_ERR_NULL, "%s: src, dst, numels, dtypes and num_chunks must be non-NULL", fn);
+  if (num_tensors < 0) return fail(BSG_ERR_SHAPE, "%s: num_tensors=%lld", fn, (long long)num_tensors);
+  bsg::GradChunk* out = static_cast<bsg::GradChunk*>(plan);
+  const int64_t room = plan != nullptr ? (int64_t)(plan_bytes / sizeof(bsg::GradChunk)) : 0;
+  int64_t count = 0;
+  for (int64_t i = 0; i < num_tensors; ++i) {
+    if (dtypes[i] != BSG_GRAD_BF16 && dtypes[i] != BSG_GRAD_F16 && dtypes[i] != BSG_GRAD_F32)
+      return fail(BSG_ERR_UNSUPPORTED, "%s: tensor %lld has dtype %d", fn, (long long)i, dtypes[i]);
+    if (numels[i] < 0 || numels[i] >= ((int64_t)1 << 48))
+      return fail(BSG_ERR_SHAPE, "%s: tensor %lld has %lld elements", fn, (long long)i,
+                  (long long)numels[i]);
+    if (numels[i] == 0) continue;
+    if (src[i] == nullptr || dst[i] == nullptr)
+      return fail(BSG_ERR_NULL, "%s: tensor %lld has no data", fn, (long long)i);
+    const uintptr_t esz = dtypes[i] == BSG_GRAD_F32 ? 4 : 2;
+    const uintptr_t s = reinterpret_cast<uintptr_t>(src[i]), d = reinterpret_cast<uintptr_t>(dst[i]);
+    if (s % esz != 0 || d % esz != 0)
+      return fail(BSG_ERR_ALIGN, "%s: tensor %lld is not aligned to its elements", fn, (long long)i);
+    // the first chunk is as much shorter as puts the later ones on 128-byte lines
+    int64_t take = bsg::kGradChunk - (int64_t)((s % 128) / esz);
+    for (int64_t at = 0; at < numels[i];) {
+      const int64_t left = numels[i] - at;
+      if (take > left) take = left;
+      if (plan != nullptr) {
+        if (count >= room)
+          return fail(BSG_ERR_WORKSPACE, "%s: a plan of %zu bytes is too small", fn, plan_bytes);
+        out[count] = bsg::GradChunk{reinterpret_cast<const void*>(s + (uintptr_t)at * esz),
+                                    reinterpret_cast<void*>(d + (uintptr_t)at * esz), (int32_t)take,
+                                    dtypes[i]};
+      }
+      ++count;
+      at += take;
+      take = bsg::kGradChunk;
+    }
+  }
+  *num_chunks = count;
+  return ok();
+}
+
+size_t grad_clip_workspace_size(void) { return sizeof(double) * bsg::kGradMaxBlocks; }
+
+namespace {
+
+int check_grad_call(const char* fn, const void* plan, int64_t num_chunks, const void* workspace,
+                    size_t workspace_bytes) {
+  if (workspace == nullptr || (plan == nullptr && num_chunks != 0))
+    return fail(BSG_ERR_NULL, "%s: plan and workspace must be non-NULL", fn);
+  if (num_chunks < 0) return fail(BSG_ERR_SHAPE, "%s: num_chunks=%lld", fn, (long long)num_chunks);
+  if (((reinterpret_cast<uintptr_t>(plan) | reinterpret_cast<uintptr_t>(workspace)) & 7u) != 0)
+    return fail(BSG_ERR_ALIGN, "%s: plan and workspace must be 8-byte aligned", fn);
+  if (workspace_bytes < grad_clip_workspace_size())
+    return fail(BSG_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes,
+                grad_clip_workspace_size());
+  return BSG_OK;
+}
+
+}  // namespace
+
+int grad_norm(const void* plan, int64_t num_chunks, void* workspace, size_t workspace_bytes,
+              float* norm, double* sumsq, uint32_t* dev_status, void* stream) {
+  const char* fn = "grad_norm";
+  const int cc = check_grad_call(fn, plan, num_chunks, workspace, workspace_bytes);
+  if (cc != BSG_OK) return cc;
+  if (norm == nullptr && sumsq == nullptr)
+    return fail(BSG_ERR_NULL, "%s: no output requested", fn);
+  if (!aligned4(norm) || (reinterpret_cast<uintptr_t>(sumsq) & 7u) != 0)
+    return fail(BSG_ERR_ALIGN, "%s: norm must be 4-byte and sumsq 8-byte aligned", fn);
+  return hip_result(bsg::launch_grad_norm(static_cast<const bsg::GradChunk*>(plan), num_chunks,
+                                          static_cast<double*>(workspace), norm, sumsq, dev_status,
+                                          (hipStream_t)stream),
+                    fn);
+}
+
+int clip_grad_norm(const void* plan, int64_t num_chunks, float max_norm, const double* sumsq,
+                   void* workspace, size_t workspace_bytes, float* norm, uint32_t* dev_status,
+                   void* stream) {
+  const char* fn = "clip_grad_norm";
+  const int cc = check_grad_call(fn, plan, num_chunks, workspace, workspace_bytes);
+  if (cc != BSG_OK) return cc;
+  if (!(max_norm >= 0.0f))
+    return fail(BSG_ERR_SHAPE, "%s: max_norm=%g must be >= 0", fn, (double)max_norm);
+  if (!aligned4(norm) || (reinterpret_cast<uintptr_t>(sumsq) & 7u) != 0)
+    return fail(BSG_ERR_ALIGN, "%s: norm must be 4-byte and sumsq 8-byte aligned", fn);
+  return hip_result(bsg::launch_clip_grad_norm(static_cast<const bsg::GradChunk*>(plan), num_chunks,
+                                               max_norm, sumsq, static_cast<double*>(workspace),
+                                               norm, dev_status, (hipStream_t)stream),
+                    fn);
+}
+
 }  // extern "C"

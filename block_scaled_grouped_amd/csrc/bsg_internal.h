@@ -22,6 +22,8 @@ constexpr int kColPad = 128;
 constexpr uint32_t kDevNegativeSize = 1u;
 constexpr uint32_t kDevOverCapacity = 2u;
 constexpr uint32_t kDevBadPadding = 4u;
+constexpr uint32_t kDevNonFinite = 8u;
+constexpr uint32_t kDevBadAdapter = 16u;
 
 // ---------------------------------------------------------------- device helpers
 
@@ -243,6 +245,42 @@ hipError_t launch_gemm_nvfp4_wgrad(int G, const uint8_t* a, const uint8_t* a_sca
                                    int64_t col_rows_cap, int64_t n, int64_t k, void* out,
                                    int out_f32, uint32_t* status, hipStream_t stream,
                                    bool accumulate = false);
+
+// Bytes of the workspace that lets launch_gemm_16bit split its contractions
+// (on the current device).
+size_t gemm_16bit_workspace_bytes();
+
+hipError_t launch_gemm_16bit(int mode, int f16, int G, const void* a, int64_t lda, const void* b,
+                             int64_t ldb, int64_t stride_b, const int64_t* offsets,
+                             int64_t rows_cap, int64_t n, int64_t k, const void* c, void* out,
+                             int64_t ldo, int64_t stride_o, int out_f32, void* ws, uint32_t* status,
+                             hipStream_t stream);
+
+size_t lora_gemm_16bit_workspace_bytes(int64_t rows_cap, int64_t n, int64_t k, int64_t r);
+
+hipError_t launch_lora_gemm_16bit(int f16, int G, const void* x, int64_t ldx, const void* w,
+                                  int64_t ldw, const void* down, const void* up,
+                                  int64_t num_adapters, int64_t r, const int64_t* offsets,
+                                  const int32_t* adapter, const float* scale, int64_t rows_cap,
+                                  int64_t n, int64_t k, void* out, int64_t ldo, int out_f32,
+                                  void* ws, uint32_t* status, hipStream_t stream);
+
+// One run of consecutive elements of one gradient.
+struct GradChunk {
+  const void* src;
+  void* dst;
+  int32_t n;      // elements, at most kGradChunk
+  int32_t dtype;  // bsg_grad_dtype
+};
+constexpr int kGradChunk = 16384;
+constexpr int kGradMaxBlocks = 2048;
+
+hipError_t launch_grad_norm(const GradChunk* plan, int64_t num_chunks, double* partials,
+                            float* norm, double* sumsq, uint32_t* status, hipStream_t stream);
+
+hipError_t launch_clip_grad_norm(const GradChunk* plan, int64_t num_chunks, float max_norm,
+                                 const double* sumsq, double* partials, float* norm,
+                                 uint32_t* status, hipStream_t stream);
 
 int device_cu_count();
 

@@ -1,0 +1,196 @@
+// Global norm of many gradient tensors, and their clipping by it.
+//
+//   norm = sqrt(sum over all tensors of x^2)
+//   y    = x * min(1, max_norm / (norm + 1e-6))
+//
+// The tensors are cut on the host into chunks (a plan, made once for buffers
+// that stay where they are); a launch walks the chunks whatever tensors they
+// belong to, so the number of tensors costs no launches.
+//
+// Squares and sums are held in 64 bits: a square of a 32-bit value neither
+// overflows nor vanishes there, and the order of the sums is fixed (thread,
+// block, then the blocks' sums in one order), so a norm repeats bit for bit.
+// The multiply-adds are far from the vector units' 64-bit rate.
+#include "bsg_internal.h"
+#include "store_tile.h"
+
+namespace bsg {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// 16 bytes at p, which is aligned to its elements only.
+__device__ __forceinline__ v4i load16(const char* p) {
+  v4i v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+__device__ __forceinline__ void store16(char* p, const v4i& v) { __builtin_memcpy(p, &v, 16); }
+
+// dtype 0: bf16, 1: fp16, 2: float32.
+template <int DT>
+__device__ __forceinline__ float elem(const v4i& v, int e) {
+  if constexpr (DT == 2) return __int_as_float(v[e]);
+  const uint32_t bits = ((uint32_t)v[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+  if constexpr (DT == 1) return (float)__builtin_bit_cast(_Float16, (unsigned short)bits);
+  return bf16_to_f32(bits);
+}
+
+template <int DT>
+__device__ __forceinline__ double chunk_sumsq(const GradChunk& c) {
+  constexpr int per = DT == 2 ? 4 : 8;
+  const char* src = static_cast<const char*>(c.src);
+  const int whole = c.n / per;
+  double s = 0.0;
+  for (int i = threadIdx.x; i < whole; i += kThreads) {
+    const v4i v = load16(src + (int64_t)i * 16);
+#pragma unroll
+    for (int e = 0; e < per; ++e) {
+      const double x = (double)elem<DT>(v, e);
+      s += x * x;
+    }
+  }
+  const int tail = whole * per + threadIdx.x;
+  if (tail < c.n) {
+    v4i v = v4i{0, 0, 0, 0};
+    __builtin_memcpy(&v, src + (int64_t)tail * (16 / per), 16 / per);
+    const double x = (double)elem<DT>(v, 0);
+    s += x * x;
+  }
+  return s;
+}
+
+__device__ __forceinline__ double block_sum(double s) {
+  __shared__ double part[kThreads / 64];
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+  __syncthreads();
+  double t = 0.0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 64; ++i) t += part[i];
+  return t;
+}
+
+__global__ __launch_bounds__(kThreads) void grad_sumsq_kernel(const GradChunk* __restrict__ plan,
+                                                              int64_t num_chunks,
+                                                              double* __restrict__ partials) {
+  double s = 0.0;
+  for (int64_t i = blockIdx.x; i < num_chunks; i += gridDim.x) {
+    const GradChunk c = plan[i];
+    if (c.dtype == 2) s += chunk_sumsq<2>(c);
+    else if (c.dtype == 1) s += chunk_sumsq<1>(c);
+    else s += chunk_sumsq<0>(c);
+  }
+  s = block_sum(s);
+  if (threadIdx.x == 0) partials[blockIdx.x] = s;
+}
+
+__device__ __forceinline__ double sum_partials(const double* __restrict__ partials, int count) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < count; i += kThreads) s += partials[i];
+  return block_sum(s);
+}
+
+__device__ __forceinline__ void write_norm(double sumsq, float* norm, double* out_sumsq,
+                                           uint32_t* status) {
+  const float n = (float)sqrt(sumsq);
+  if (norm != nullptr) *norm = n;
+  if (out_sumsq != nullptr) *out_sumsq = sumsq;
+  if (!(sumsq < __builtin_inf())) dev_status_or(status, kDevNonFinite);
+}
+
+__global__ __launch_bounds__(kThreads) void grad_norm_kernel(const double* __restrict__ partials,
+                                                             int count, float* norm,
+                                                             double* out_sumsq, uint32_t* status) {
+  const double s = sum_partials(partials, count);
+  if (threadIdx.x == 0) write_norm(s, norm, out_sumsq, status);
+}
+
+template <int DT>
+__device__ __forceinline__ void chunk_scale(const GradChunk& c, float f) {
+  constexpr int per = DT == 2 ? 4 : 8;
+  const char* src = static_cast<const char*>(c.src);
+  char* dst = static_cast<char*>(c.dst);
+  const int whole = c.n / per;
+  for (int i = threadIdx.x; i < whole; i += kThreads) {
+    const v4i v = load16(src + (int64_t)i * 16);
+    v4i y;
+    if constexpr (DT == 2) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = __float_as_int(elem<2>(v, e) * f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        y[e] = (int)pack16<DT == 1>(elem<DT>(v, 2 * e) * f, elem<DT>(v, 2 * e + 1) * f);
+    }
+    store16(dst + (int64_t)i * 16, y);
+  }
+  const int tail = whole * per + threadIdx.x;
+  if (tail < c.n) {
+    v4i v = v4i{0, 0, 0, 0};
+    __builtin_memcpy(&v, src + (int64_t)tail * (16 / per), 16 / per);
+    const float x = elem<DT>(v, 0) * f;
+    if constexpr (DT == 2) {
+      *reinterpret_cast<float*>(dst + (int64_t)tail * 4) = x;
+    } else {
+      const uint16_t b = (uint16_t)(pack16<DT == 1>(x, x) & 0xffffu);
+      *reinterpret_cast<uint16_t*>(dst + (int64_t)tail * 2) = b;
+    }
+  }
+}
+
+// Every block adds the partial sums again, in the same order (2048 of them at
+// most, from the L2): cheaper than a third launch between the two passes.
+__global__ __launch_bounds__(kThreads) void grad_scale_kernel(
+    const GradChunk* __restrict__ plan, int64_t num_chunks, const double* __restrict__ partials,
+    int count, float max_norm, float* norm, uint32_t* status) {
+  const double sumsq = sum_partials(partials, count);
+  if (blockIdx.x == 0 && threadIdx.x == 0) write_norm(sumsq, norm, nullptr, status);
+  double f = (double)max_norm / (sqrt(sumsq) + 1e-6);
+  if (f > 1.0) f = 1.0;  // a NaN stays one
+  const float factor = (float)f;
+  // the second pass begins with what the first one read last
+  for (int64_t i = num_chunks - 1 - blockIdx.x; i >= 0; i -= gridDim.x) {
+    const GradChunk c = plan[i];
+    if (factor == 1.0f && c.dst == c.src) continue;
+    if (c.dtype == 2) chunk_scale<2>(c, factor);
+    else if (c.dtype == 1) chunk_scale<1>(c, factor);
+    else chunk_scale<0>(c, factor);
+  }
+}
+
+int blocks_for(int64_t num_chunks) {
+  int64_t b = 8 * (int64_t)device_cu_count();
+  if (b > kGradMaxBlocks) b = kGradMaxBlocks;
+  if (b > num_chunks) b = num_chunks;
+  return (int)(b > 0 ? b : 1);
+}
+
+}  // namespace
+
+hipError_t launch_grad_norm(const GradChunk* plan, int64_t num_chunks, double* partials,
+                            float* norm, double* sumsq, uint32_t* status, hipStream_t stream) {
+  const int blocks = blocks_for(num_chunks);
+  hipLaunchKernelGGL(grad_sumsq_kernel, dim3(blocks), dim3(kThreads), 0, stream, plan, num_chunks,
+                     partials);
+  hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(kThreads), 0, stream, partials, blocks, norm,
+                     sumsq, status);
+  return hipGetLastError();
+}
+
+hipError_t launch_clip_grad_norm(const GradChunk* plan, int64_t num_chunks, float max_norm,
+                                 const double* sumsq, double* partials, float* norm,
+                                 uint32_t* status, hipStream_t stream) {
+  const int blocks = blocks_for(num_chunks);
+  if (sumsq == nullptr)
+    hipLaunchKernelGGL(grad_sumsq_kernel, dim3(blocks), dim3(kThreads), 0, stream, plan, num_chunks,
+                       partials);
+  hipLaunchKernelGGL(grad_scale_kernel, dim3(blocks), dim3(kThreads), 0, stream, plan, num_chunks,
+                     sumsq != nullptr ? sumsq : partials, sumsq != nullptr ? 1 : blocks, max_norm,
+                     norm, status);
+  return hipGetLastError();
+}
+
+}  // namespace bsg

@@ -48,6 +48,8 @@ typedef enum {
 #define BSG_DEV_OVER_CAPACITY 2u   /* offsets ran past the buffer capacity; clamped */
 #define BSG_DEV_BAD_PADDING   4u   /* padded offsets not multiples of 128 or smaller than
                                       the live sizes; that group was skipped */
+#define BSG_DEV_NONFINITE     8u   /* a global gradient norm is infinite or NaN */
+#define BSG_DEV_BAD_ADAPTER   16u  /* an adapter index >= num_adapters was treated as none */
 
 typedef enum {
   BSG_FPROP_TN = 0,
@@ -55,10 +57,13 @@ typedef enum {
   BSG_DGRAD_NN = 2,
   BSG_WGRAD_NT_E5M2 = 3
 } bsg_gemm_mode;
-typedef enum { BSG_OUT_BF16 = 0, BSG_OUT_F32 = 1 } bsg_out_dtype;
+typedef enum { BSG_OUT_BF16 = 0, BSG_OUT_F32 = 1, BSG_OUT_F16 = 2 } bsg_out_dtype; /* F16: 16-bit GEMMs */
+typedef enum { BSG_IN_BF16 = 0, BSG_IN_F16 = 1 } bsg_in_dtype;
+typedef enum { BSG_GRAD_BF16 = 0, BSG_GRAD_F16 = 1, BSG_GRAD_F32 = 2 } bsg_grad_dtype;
 
 #define BSG_MAX_GROUPS 256
 #define BSG_COLWISE_PAD 128
+#define BSG_MAX_LORA_RANK 256
 
 /* Thread-local message of the last failing call on this thread ("" if none). */
 const char* bsg_last_error(void);
@@ -586,6 +591,118 @@ int grouped_gemm_nvfp4_rowscaled_wgrad_ex(int64_t G, const uint8_t* a, const uin
                                           const int64_t* padded_offsets, int64_t col_rows_cap,
                                           int64_t n, int64_t k, void* out, int out_dtype,
                                           int accumulate, uint32_t* dev_status, void* stream);
+
+/*
+ * grouped_gemm_16bit
+ *
+ * The grouped products of grouped_gemm_mxfp8 for operands that stay in 16 bits
+ * (bf16 or fp16), one launch over all groups, FP32 accumulation, for the layers
+ * a low-precision recipe leaves unquantized.  No padded or transposed copies:
+ * every mode reads the row-major tensors as they are.
+ *
+ * mode BSG_FPROP_TN:  Y[r, j] = C[r, j] + sum_i A[r, i] * B[g, j, i]
+ *   a [rows_cap, k], b [G, n, k], out [rows_cap, n]; r in [offsets[g], offsets[g+1])
+ * mode BSG_DGRAD_NN:  Y[r, j] = C[r, j] + sum_i A[r, i] * B[g, i, j]
+ *   a [rows_cap, k], b [G, k, n], out [rows_cap, n]
+ * mode BSG_WGRAD_NT:  Y[g, i, j] = C[g, i, j] + sum_t A[t, i] * B[t, j]
+ *   a [rows_cap, n], b [rows_cap, k], out [G, n, k]; t over group g's rows
+ *   (a group without rows gets C, or zeros)
+ *
+ *   in_dtype    BSG_IN_BF16 or BSG_IN_F16: both operands.
+ *   lda, ldb    elements between consecutive rows of a and b (>= the row length,
+ *               multiples of 8, at most 2^20); stride_b: elements between
+ *               consecutive groups' matrices of b (FPROP, DGRAD; a multiple of 8).
+ *   offsets     [G+1] int64 live row offsets; rows outside [offsets[0], offsets[G])
+ *               are neither read nor written.
+ *   n, k        multiples of 8, > 0.
+ *   c           the addend, in out's type and layout, or NULL (none).  It may be
+ *               out itself: Y accumulates (e.g. into FP32 main gradients).
+ *   out         element type out_dtype: the 16-bit type of the operands or
+ *               BSG_OUT_F32; the sum with C is rounded to it once.  ldo elements
+ *               between rows (a multiple of 8), stride_o between groups (WGRAD).
+ *   workspace   grouped_gemm_16bit_workspace_size() bytes, 256-byte aligned, or
+ *               NULL.  With it, products with few output tiles are split along the
+ *               contraction and summed in a fixed order by a second kernel.
+ * Results do not depend on the order in which workgroups run.
+ * Errors: BSG_ERR_NULL, BSG_ERR_SHAPE, BSG_ERR_UNSUPPORTED (mode, types),
+ * BSG_ERR_ALIGN (a, b, c, out 16-byte), BSG_ERR_WORKSPACE.
+ */
+size_t grouped_gemm_16bit_workspace_size(void);
+int grouped_gemm_16bit(int mode, int in_dtype, int64_t G, const void* a, int64_t lda,
+                       const void* b, int64_t ldb, int64_t stride_b, const int64_t* offsets,
+                       int64_t rows_cap, int64_t n, int64_t k, const void* c, void* out,
+                       int64_t ldo, int64_t stride_o, int out_dtype, void* workspace,
+                       size_t workspace_bytes, uint32_t* dev_status, void* stream);
+
+/*
+ * grouped_lora_gemm_16bit
+ *
+ * A projection shared by all rows beside the low-rank adapters of many requests:
+ *   Y[r, :] = X[r, :] W^T + scale[a] * (X[r, :] A_a^T) B_a^T,   a = adapter[g]
+ * for the rows r in [offsets[g], offsets[g+1]) of request g; a request whose
+ * adapter is negative gets the projection alone.  Prompts and single tokens mix
+ * freely.  What one adapter holds never reaches a row of another request.
+ *
+ *   x           [rows_cap, k], ldx; rows outside [offsets[0], offsets[G]) are not
+ *               written.  w [n, k], ldw.  Element type in_dtype throughout.
+ *   lora_a      [num_adapters, rank, k], lora_b [num_adapters, n, rank], contiguous.
+ *   rank        a multiple of 8 in [8, BSG_MAX_LORA_RANK] (pad smaller ranks with
+ *               zeros).
+ *   adapter     [G] int32, scale [num_adapters] float32, device.
+ *   out         [rows_cap, n], ldo; the operands' type or BSG_OUT_F32, rounded once.
+ *               X A^T is accumulated in FP32, scaled, and kept as two 16-bit values
+ *               (their sum holds 16 or more bits of it) for the second product.
+ *   workspace   grouped_lora_gemm_16bit_workspace_size(rows_cap, n, k, rank) bytes,
+ *               256-byte aligned.
+ * Constraints on n, k and strides and errors as grouped_gemm_16bit.
+ * The gradients of the adapters are products of grouped_gemm_16bit.
+ */
+size_t grouped_lora_gemm_16bit_workspace_size(int64_t rows_cap, int64_t n, int64_t k, int64_t rank);
+int grouped_lora_gemm_16bit(int in_dtype, int64_t G, const void* x, int64_t ldx, const void* w,
+                            int64_t ldw, const void* lora_a, const void* lora_b,
+                            int64_t num_adapters, int64_t rank, const int64_t* offsets,
+                            const int32_t* adapter, const float* scale, int64_t rows_cap,
+                            int64_t n, int64_t k, void* out, int64_t ldo, int out_dtype,
+                            void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                            void* stream);
+
+/*
+ * Global gradient norm and clipping over many tensors.
+ *
+ * grad_clip_plan_fill cuts num_tensors tensors into the chunks that one launch
+ * walks, on the host: no device is touched.
+ *   src, dst    [host] arrays of num_tensors device pointers, aligned to their
+ *               elements; dst[i] receives the clipped src[i] and may equal it.
+ *               Other overlaps are not allowed.
+ *   numels      [host] elements (>= 0); dtypes [host] bsg_grad_dtype.
+ *   plan        [host] buffer of plan_bytes, or NULL to ask for the size only.
+ *   num_chunks  [host] output; the plan takes 24 bytes per chunk.
+ * The caller copies the plan to the device (8-byte aligned) and keeps it while
+ * the tensors stay where they are.
+ *
+ * grad_norm:      norm[0] = sqrt(sum x^2) (float32, optional), sumsq[0] = sum x^2
+ *                 (float64, optional; add the ranks' values for a sharded model).
+ * clip_grad_norm: dst = src * min(1, max_norm / (norm + 1e-6)), rounded once to
+ *                 the tensor's type; norm[0] (optional) the norm before clipping.
+ *                 sumsq: a float64 on the device to take for the sum of squares
+ *                 (NULL: this call computes it).  In place and within max_norm,
+ *                 nothing is written.
+ * Sums are float64, in a fixed order.  A norm that is not finite sets
+ * BSG_DEV_NONFINITE; the formula then gives zeros and NaN.
+ *   workspace   grad_clip_workspace_size() bytes, 8-byte aligned.
+ *   max_norm    >= 0 (infinity: no clipping).
+ * Errors: BSG_ERR_NULL, BSG_ERR_SHAPE (counts, max_norm), BSG_ERR_UNSUPPORTED
+ * (dtype), BSG_ERR_ALIGN, BSG_ERR_WORKSPACE (plan or workspace too small).
+ */
+int grad_clip_plan_fill(int64_t num_tensors, const void* const* src, void* const* dst,
+                        const int64_t* numels, const int32_t* dtypes, void* plan,
+                        size_t plan_bytes, int64_t* num_chunks);
+size_t grad_clip_workspace_size(void);
+int grad_norm(const void* plan, int64_t num_chunks, void* workspace, size_t workspace_bytes,
+              float* norm, double* sumsq, uint32_t* dev_status, void* stream);
+int clip_grad_norm(const void* plan, int64_t num_chunks, float max_norm, const double* sumsq,
+                   void* workspace, size_t workspace_bytes, float* norm, uint32_t* dev_status,
+                   void* stream);
 
 #ifdef __cplusplus
 }
