@@ -727,9 +727,12 @@ def grouped_gemm_nvfp4_rowscaled_wgrad(a, a_scales, a_outer, b, b_scales, b_oute
     return out
 
 
-def _types_16bit(t, name, out_dtype):
-    """(in_dtype, out_dtype code, torch output type) of a 16-bit operand; out_dtype None: its own."""
+def _types_16bit(t, name, out_dtype, like=None):
+    """(in_dtype, out_dtype code, torch output type) of a 16-bit operand; out_dtype None: its own
+    or, where there is one, that of `like` (an addend or an output)."""
     import torch
+    if out_dtype is None and like is not None and like.dtype == torch.float32:
+        out_dtype = BSG_OUT_F32
     if t.dtype == torch.bfloat16:
         code, same = BSG_IN_BF16, BSG_OUT_BF16
     elif t.dtype == torch.float16:
@@ -786,10 +789,11 @@ def grouped_gemm_16bit(mode, a, b, offsets, c=None, out=None, out_dtype=None, wo
     BSG_WGRAD_NT  a [rows, n], b [rows, k]  -> [G, n, k]: a^T b over group g's rows
 
     c: an addend in the output's type and shape (pass the same tensor as `out` to
-    accumulate).  out_dtype: None (the operands' type) or BSG_OUT_F32.  Rows may be
-    strided (strides multiples of 8 elements).  See include/bsg.h."""
+    accumulate).  out_dtype: the operands' type or BSG_OUT_F32; None takes that of `out`
+    or `c` where given, else the operands'.  Rows may be strided (strides multiples of 8
+    elements).  See include/bsg.h."""
     lib = load_library()
-    code, od, odt = _types_16bit(a, "a", out_dtype)
+    code, od, odt = _types_16bit(a, "a", out_dtype, out if out is not None else c)
     lda, _ = _strided(a, "a", 2, a.dtype)
     _req(offsets, "offsets", 16, _i64())
     G = offsets.numel() - 1
@@ -853,7 +857,7 @@ def grouped_lora_gemm_16bit(x, w, lora_a, lora_b, offsets, adapter, scale, out=N
     one.  See include/bsg.h."""
     import torch
     lib = load_library()
-    code, od, odt = _types_16bit(x, "x", out_dtype)
+    code, od, odt = _types_16bit(x, "x", out_dtype, out)
     ldx, _ = _strided(x, "x", 2, x.dtype)
     ldw, _ = _strided(w, "w", 2, x.dtype)
     (rows, k), n = x.shape, w.shape[0]

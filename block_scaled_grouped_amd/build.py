@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(HERE, "libbsg.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 KERNEL_SOURCES = ["offsets.hip", "quantize_mxfp8.hip", "quantize_nvfp4.hip", "gemm_mxfp8.hip",
-                  "gemm_nvfp4.hip", "gemm_16bit.hip", "grad_clip.hip"]
+                  "gemm_nvfp4.hip", "gemm_16bit.hip",
+                  "gemm_16bit_large.hip", "gemm_16bit_small.hip", "grad_clip.hip"]
 HOST_SOURCES = ["api.cpp"]
 
 # Packed-fp32 VALU ops are turned off for all device code.

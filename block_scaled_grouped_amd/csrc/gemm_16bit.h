@@ -1,0 +1,673 @@
+// Parts shared by the kernels of the 16-bit grouped products (bf16 or fp16
+// operands, FP32 accumulation):
+//
+//   FPROP_TN:  Y[r, :]  = C[r, :] + A[r, :] B_g^T      r in group g
+//   DGRAD_NN:  Y[r, :]  = C[r, :] + A[r, :] B_g        r in group g
+//   WGRAD_NT:  Y_g      = C_g + A_g^T B_g              over the group's rows
+//
+// and, beside a projection shared by all rows, the low-rank product of each
+// row's own adapter (LORA): Y[r, :] = A[r, :] B^T + low[r, :] U_a^T.
+//
+// Every output tile is one contraction of an A tile and a B tile.  An operand
+// lies in memory either with the contraction innermost ("rows": both operands
+// of FPROP, A of DGRAD) or with its rows innermost ("columns": B of DGRAD, both
+// of WGRAD).  Both kinds are copied to LDS as they lie, 64 contraction indexes a
+// stage, in whole lines; the transposition that the matrix instruction needs of
+// the second kind is done by the LDS reads (ds_read_b64_tr_b16), so no operand
+// is transposed in memory and none passes through the vector units.
+//
+// LDS layout of an operand tile of BR rows (both kinds take 128 BR bytes):
+//   rows:    row r at 128 r; 16-byte chunk c (8 contraction indexes) in slot
+//            c ^ ((r / 2) % 8), so that 16 lanes reading one chunk of 16
+//            consecutive rows hit all 64 banks.
+//   columns: contraction index k at 2 BR k; chunk c (8 rows) in slot
+//            c ^ swz(k), so that the four 64-byte pieces that 32 lanes of a
+//            transposing read take from four consecutive k hit all 64 banks.
+//
+// Matrix instruction: v_mfma_f32_32x32x16, lane (r, h) = (l % 32, l / 32) holds
+// contraction indexes 8 h .. 8 h + 7 of row r.  B is its first operand and A
+// its second, so lane (r, h) ends with output row r, columns 8 q + 4 h + [0, 4)
+// in registers 4 q .. 4 q + 3 of a 32 x 32 block.
+#ifndef BSG_GEMM_16BIT_H
+#define BSG_GEMM_16BIT_H
+
+#include <utility>
+
+#include "bsg_internal.h"
+#include "lds_dma.h"
+#include "store_tile.h"
+
+namespace bsg {
+namespace g16 {
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4i lds_v4i;
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+
+constexpr int kStageK = 64;       // contraction indexes per LDS stage
+constexpr int kThreads = 256;
+constexpr int kSuperM = 4, kSuperN = 8;  // tile block one XCD works on
+
+enum Mode { kFprop = 0, kWgrad = 1, kDgrad = 2, kLora = 3 };
+template <int MODE> constexpr bool kColsA = MODE == kWgrad;
+template <int MODE> constexpr bool kColsB = MODE == kWgrad || MODE == kDgrad;
+
+template <typename F, int... Is>
+__device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, Is...>) {
+  (f(std::integral_constant<int, Is>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_impl(f, std::make_integer_sequence<int, N>{});
+}
+
+struct Args {
+  const uint16_t* a;
+  const uint16_t* b;
+  const int64_t* offsets;
+  const char* c;
+  char* out;
+  int64_t lda, ldb, stride_b, ldo, stride_o;  // elements
+  int64_t rows_cap, n, k;
+  uint32_t* status;
+  char* ws;  // split workspace or null: no split
+  int G, out_f32;
+  // LORA
+  const uint16_t* low;     // [rows_cap, 2 r]: high and low halves of the scaled X A^T
+  const uint16_t* up;      // [adapters, n, r]
+  const int32_t* adapter;  // [G], negative: none
+  int num_adapters, r;
+};
+
+struct Sched {
+  int64_t off[kMaxGroups + 1];
+  int32_t cnt[kMaxGroups];
+  int32_t pre[kMaxGroups + 1];
+};
+
+struct Tile {
+  const uint16_t* a;  // first element of the operand tiles
+  const uint16_t* b;
+  int64_t lda, ldb;
+  int a_rows, b_rows;  // live rows (those past them read as zeros)
+  int kl;              // contraction length
+  int64_t out_off;     // bytes from out (and c) to the tile's first element
+  int64_t row0;        // LORA: first row
+  int64_t col0;        // LORA: first column
+};
+
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uni64(int64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(v & 0xffffffff));
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes,
+                                           0x00020000);
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t lds_offset(T* shared_ptr) {
+  return (uint32_t)(size_t)(__attribute__((address_space(3))) T*)(shared_ptr);
+}
+
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+
+// Vector-memory operations complete in issue order: waits until only the N most
+// recent are outstanding and for this wave's LDS accesses, then joins the barrier.
+template <int N>
+__device__ __forceinline__ void wait_and_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// ---------------------------------------------------------------- tiles
+
+// Loads the offsets and counts tiles; returns their number.  Every thread calls it.
+template <int MODE, int BM, int BN>
+__device__ __forceinline__ int count_tiles(const Args& p, Sched& sm) {
+  const int tid = threadIdx.x;
+  load_offsets_clamped(p.offsets, p.G, p.rows_cap, sm.off, blockIdx.x == 0 ? p.status : nullptr);
+  const int64_t ntn = (p.n + BN - 1) / BN;
+  if constexpr (MODE == kLora) {
+    // all rows of all requests are one run of rows of the shared projection
+    __syncthreads();
+    const int64_t m = sm.off[p.G] - sm.off[0];
+    const int total = (int)(((m > 0 ? m : 0) + BM - 1) / BM * ntn);
+    return uni(total);
+  } else {
+    for (int g = tid; g < p.G; g += kThreads)
+      sm.cnt[g] = (int32_t)(MODE == kWgrad ? ((p.n + BM - 1) / BM) * ((p.k + BN - 1) / BN)
+                                           : ((group_extent(sm.off, g) + BM - 1) / BM) * ntn);
+    __syncthreads();
+    wave0_exclusive_scan(sm.cnt, p.G, sm.pre);
+    __syncthreads();
+    return uni(sm.pre[p.G]);
+  }
+}
+
+template <int MODE, int BM, int BN>
+__device__ __forceinline__ Tile find_tile(const Args& p, const Sched& sm, int tile) {
+  const int esz = p.out_f32 ? 4 : 2;
+  Tile t;
+  int mt, nt;
+  if constexpr (MODE == kWgrad) {
+    const int g = uni(find_group(sm.pre, p.G, tile));
+    super_tile<kSuperM, kSuperN>(tile - uni(sm.pre[g]), (int)((p.n + BM - 1) / BM),
+                                 (int)((p.k + BN - 1) / BN), mt, nt);
+    const int64_t i0 = (int64_t)mt * BM, j0 = (int64_t)nt * BN;
+    const int64_t t0 = uni64(sm.off[g]);
+    t.a = p.a + t0 * p.lda + i0;
+    t.b = p.b + t0 * p.ldb + j0;
+    const int64_t rv = p.n - i0, cv = p.k - j0;
+    t.a_rows = (int)(rv < BM ? rv : BM);
+    t.b_rows = (int)(cv < BN ? cv : BN);
+    t.kl = uni((int)group_extent(sm.off, g));
+    t.out_off = (g * p.stride_o + i0 * p.ldo + j0) * esz;
+    t.row0 = t.col0 = 0;
+  } else {
+    const int g = MODE == kLora ? 0 : uni(find_group(sm.pre, p.G, tile));
+    const int64_t first = uni64(sm.off[g]);
+    const int64_t m = MODE == kLora ? uni64(sm.off[p.G]) - first : uni64(group_extent(sm.off, g));
+    super_tile<kSuperM, kSuperN>(MODE == kLora ? tile : tile - uni(sm.pre[g]),
+                                 (int)((m + BM - 1) / BM), (int)((p.n + BN - 1) / BN), mt, nt);
+    const int64_t r0 = (int64_t)mt * BM, n0 = (int64_t)nt * BN;
+    t.a = p.a + (first + r0) * p.lda;
+    t.b = p.b + (MODE == kLora ? 0 : g * p.stride_b) + (MODE == kDgrad ? n0 : n0 * p.ldb);
+    const int64_t rv = m - r0, cv = p.n - n0;
+    t.a_rows = (int)(rv < BM ? rv : BM);
+    t.b_rows = (int)(cv < BN ? cv : BN);
+    t.kl = (int)p.k;
+    t.out_off = ((first + r0) * p.ldo + n0) * esz;
+    t.row0 = first + r0;
+    t.col0 = n0;
+  }
+  t.lda = p.lda;
+  t.ldb = p.ldb;
+  return t;
+}
+
+// ---------------------------------------------------------------- global -> LDS
+
+template <int BR>
+__device__ __forceinline__ int swz(int k) {
+  if constexpr (BR >= 128) return 4 * (k & 3);
+  else if constexpr (BR == 64) return 4 * ((k >> 1) & 1);
+  else return 0;
+}
+
+// One wave's share of the copies of an operand tile of BR rows: pieces w, w + 4,
+// .. of the tile's BR / 8 pieces of 1 KiB (a wave's pieces have one swizzle).
+//   rows:    piece p is rows 8 p .. 8 p + 7, lane l row 8 p + l / 8, slot l % 8
+//   columns: piece p is 512 / BR contraction indexes, lane l index l / (BR / 8)
+//            of them, slot l % (BR / 8)
+// What lies past the tile's rows or the contraction is copied as zeros: by the
+// descriptor's range, or by an offset past every range.
+template <bool COLS, int BR>
+struct Side {
+  static constexpr int kPieces = BR / 32;  // per wave
+  uint64_t base;
+  int range;  // rows: bytes of the whole tile
+  int ld2;    // bytes between memory rows
+  int off;    // this lane's offset in piece w, stage 0
+  int kc;     // rows: contraction index of this lane's chunk in a stage
+  int step;   // bytes from one of the wave's pieces to the next
+  int kl;
+
+  // linear: lanes read consecutive chunks (for copies through registers);
+  // otherwise each lane reads the chunk that belongs in its LDS slot.
+  __device__ __forceinline__ void init(const uint16_t* src, int64_t ld, int rows, int contraction,
+                                       int w, int lane, bool linear) {
+    base = (uint64_t)uni64((int64_t)reinterpret_cast<uint64_t>(src));
+    ld2 = uni((int)(ld * 2));
+    kl = uni(contraction);
+    if constexpr (!COLS) {
+      const int row = 8 * w + (lane >> 3);
+      const int c = (lane & 7) ^ (linear ? 0 : (row >> 1) & 7);
+      range = uni(rows) * ld2;
+      off = row * ld2 + c * 16;
+      kc = c * 8;
+      step = 32 * ld2;
+    } else {
+      constexpr int cpr = BR / 8, rpp = 512 / BR;
+      const int k = rpp * w + lane / cpr;
+      const int c = (lane % cpr) ^ (linear ? 0 : swz<BR>(k));
+      range = 0;
+      kc = 0;
+      off = c * 8 < rows ? k * ld2 + c * 16 : kDmaOutOfRange;
+      step = 4 * rpp * ld2;
+    }
+  }
+
+  // this lane's offset in the tile's LDS of piece w when it read linearly
+  __device__ __forceinline__ static int slot(int w, int lane) {
+    if constexpr (!COLS) {
+      const int row = 8 * w + (lane >> 3);
+      return row * 128 + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
+    } else {
+      constexpr int cpr = BR / 8, rpp = 512 / BR;
+      const int k = rpp * w + lane / cpr;
+      return k * (BR * 2) + (((lane % cpr) ^ swz<BR>(k)) << 4);
+    }
+  }
+
+  // Base address and range of stage kt (nothing is in range when it is not live).
+  __device__ __forceinline__ uint64_t stage_base(int kt) const {
+    return COLS ? base + (uint64_t)kt * (uint64_t)(kStageK * (int64_t)ld2) : base;
+  }
+  __device__ __forceinline__ int stage_range(int kt, bool live) const {
+    if (!live) return 0;
+    if constexpr (!COLS) return range;
+    const int left = kl - kt * kStageK;
+    return (left < kStageK ? left : kStageK) * ld2;
+  }
+  __device__ __forceinline__ int piece_off(int i, int kt) const {
+    if constexpr (COLS) return off + i * step;
+    return kc < kl - kt * kStageK ? off + i * step + kt * (2 * kStageK) : kDmaOutOfRange;
+  }
+};
+
+__device__ __forceinline__ v4i rsrc_words(uint64_t base, int range) {
+  return v4i{(int)(uint32_t)base, (int)(uint32_t)(base >> 32), range, 0x00020000};
+}
+
+// ---------------------------------------------------------------- LDS -> registers
+
+// Offsets of a lane's fragment reads: one register a k16 step (rows; the 32-row
+// steps are immediates) or a 32-row block (columns; the k16 steps are).
+template <bool COLS, int BR, int NB>
+struct FragOff {
+  static constexpr int kRegs = COLS ? NB : 4;
+  int o[kRegs];
+  __device__ __forceinline__ void init(int row0, int lane) {
+    if constexpr (!COLS) {
+      const int r = lane & 31, h = lane >> 5;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        o[t] = (row0 + r) * 128 + (((2 * t + h) ^ ((r >> 1) & 7)) << 4);
+    } else {
+      const int h = lane >> 5, kk = (lane & 15) >> 2;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const int c = (row0 >> 3) + 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+        o[i] = (8 * h + kk) * (BR * 2) + ((c ^ swz<BR>(kk)) << 4) + 8 * (lane & 1);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kRegs; ++t) asm volatile("" : "+v"(o[t]));
+  }
+  // Rows 32 I + lane % 32, contraction indexes 16 T + 8 (lane / 32) + [0, 8).
+  template <int I, int T>
+  __device__ __forceinline__ v4i read(uint32_t tile) const {
+    if constexpr (!COLS) {
+      return *reinterpret_cast<const lds_v4i*>((size_t)(tile + o[T] + I * 4096));
+    } else {
+      const uint32_t at = tile + o[I] + T * 32 * BR;
+      const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(size_t)at);
+      const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(size_t)(at + 8 * BR));
+      const v2i l = __builtin_bit_cast(v2i, lo), u = __builtin_bit_cast(v2i, hi);
+      return v4i{l[0], l[1], u[0], u[1]};
+    }
+  }
+};
+
+template <bool F16>
+__device__ __forceinline__ v16f mfma16(const v4i& x, const v4i& y, const v16f& acc) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, x),
+                                                  __builtin_bit_cast(v8h, y), acc, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, x),
+                                                   __builtin_bit_cast(v8bf, y), acc, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------- adapters
+
+// Adapter of request g, or -1.
+__device__ __forceinline__ int adapter_of(const Args& p, int g) {
+  const int a = p.adapter[g];
+  return a < p.num_adapters ? a : -1;
+}
+
+// Request of a row in [off[0], off[G]).
+__device__ __forceinline__ int request_of(const int64_t* off, int G, int64_t row) {
+  int lo = 0, hi = G - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (off[mid] <= row) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Adds each row's own low-rank product to a wave's accumulators: for every
+// adapter that occurs in a 32-row block one product of the block's low rows (both
+// halves) with the adapter's rows of `up`, kept for its own rows only.  So what
+// an adapter holds (infinities, NaN) never reaches a row of another request, and
+// the cost follows the adapters that meet in 32 rows, not the requests.  The
+// operands come straight from the L2: 2 r / 16 matrix instructions a block and
+// adapter are few against the projection's k / 16.
+// ids: adapter of each of the tile's rows (-1: none).  A split tile's parts
+// share the adapters out: the c-th of a block goes to part c % nparts.
+template <bool F16, int MI, int NJ>
+__device__ __forceinline__ void add_low_rank(const Args& p, const Tile& t, const int* ids, int wrow,
+                                             int wcol, int lane, int part, int nparts,
+                                             v16f (&acc)[MI][NJ]) {
+  const int r = lane & 31, h = lane >> 5, rank = p.r;
+  const uint16_t* urow[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    int col = wcol + 32 * j + r;
+    if (col >= t.b_rows) col = t.b_rows - 1;  // such columns are not stored
+    urow[j] = p.up + (t.col0 + col) * rank + 8 * h;
+  }
+  static_for<MI>([&](auto ic) {
+    constexpr int i = decltype(ic)::value;
+    const int row = wrow + 32 * i + r;
+    const int id = ids[row];
+    const int lrow = row < t.a_rows ? row : t.a_rows - 1;
+    const uint16_t* low = p.low + (t.row0 + lrow) * 2 * rank + 8 * h;
+    uint32_t todo = (uint32_t)__ballot(id >= 0);
+    int turn = 0;
+    while (todo != 0) {
+      const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+      todo &= ~(uint32_t)__ballot(id == a);
+      if (nparts > 1) {
+        const bool mine = turn == part;
+        turn = turn + 1 == nparts ? 0 : turn + 1;
+        if (!mine) continue;
+      }
+      const int64_t ua = (int64_t)a * p.n * rank;
+      // one block at a time: the large form's accumulators leave no room for more
+      static_for<NJ>([&](auto jc) {
+        constexpr int j = decltype(jc)::value;
+        v16f one = v16f{};
+#pragma unroll 2
+        for (int k = 0; k < rank; k += 16) {
+          v4i l0 = v4i{0, 0, 0, 0}, l1 = l0, u = l0;
+          if (k + 8 * h < rank) {  // a rank of 8 (mod 16) ends within the step
+            l0 = *reinterpret_cast<const v4i*>(low + k);
+            l1 = *reinterpret_cast<const v4i*>(low + rank + k);
+            u = *reinterpret_cast<const v4i*>(urow[j] + ua + k);
+          }
+          one = mfma16<F16>(u, l0, one);
+          one = mfma16<F16>(u, l1, one);
+        }
+        fence();
+        v16f y = acc[i][j];
+        asm volatile("" : "+v"(y));
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = id == a ? y[e] + one[e] : y[e];
+        acc[i][j] = y;
+        asm volatile("" : "+a"(acc[i][j]));
+        fence();
+      });
+    }
+  });
+}
+
+// Fills ids[0..BM) for a tile; the caller places a barrier after it.
+template <int BM>
+__device__ __forceinline__ void tile_adapters(const Args& p, const Sched& sm, const Tile& t,
+                                              int* ids) {
+  for (int i = threadIdx.x; i < BM; i += kThreads)
+    ids[i] = i < t.a_rows ? adapter_of(p, request_of(sm.off, p.G, t.row0 + i)) : -1;
+}
+
+// ---------------------------------------------------------------- epilogue
+
+// One 32 x 32 block with C added in float32 before the one rounding.
+template <bool F32, bool F16>
+__device__ __forceinline__ void store_block_c(const v16f& acc, __amdgpu_buffer_rsrc_t ro,
+                                              __amdgpu_buffer_rsrc_t rc, int ldo, int row, int col0,
+                                              int out_cols) {
+  constexpr int esz = F32 ? 4 : 2;
+  int off[4];
+  float c[16];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int col = col0 + 8 * q;
+    off[q] = col < out_cols ? (row * ldo + col) * esz : (int)kDropped;
+    if constexpr (F32) {
+      const v4i v = __builtin_amdgcn_raw_buffer_load_b128(rc, off[q], 0, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[4 * q + e] = __int_as_float(v[e]);
+    } else {
+      const v2i v = __builtin_amdgcn_raw_buffer_load_b64(rc, off[q], 0, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t bits = ((uint32_t)v[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+        c[4 * q + e] = F16 ? (float)__builtin_bit_cast(_Float16, (unsigned short)bits)
+                           : bf16_to_f32(bits);
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = acc[4 * q + e] + c[4 * q + e];
+    if constexpr (F32) {
+      __builtin_amdgcn_raw_buffer_store_b128(
+          (v4i){__float_as_int(y[0]), __float_as_int(y[1]), __float_as_int(y[2]),
+                __float_as_int(y[3])},
+          ro, off[q], 0, 0);
+    } else {
+      __builtin_amdgcn_raw_buffer_store_b64(
+          (v2i){(int)pack16<F16>(y[0], y[1]), (int)pack16<F16>(y[2], y[3])}, ro, off[q], 0, 0);
+    }
+  }
+}
+
+// Where a tile's output goes: its first element, live rows and columns.
+struct OutTile {
+  char* out;
+  const char* c;  // or null
+  int ldo, rows, cols;
+};
+
+// A wave's MI x NJ blocks, the first at (row, col) of the tile, one at a time:
+// each block's accumulators are copied out right before its loads and stores.
+template <bool F16, int MI, int NJ>
+__device__ __forceinline__ void store_blocks(const v16f (&acc)[MI][NJ], const OutTile& o,
+                                             int out_f32, int wrow, int wcol, int lane) {
+  const int esz = out_f32 ? 4 : 2;
+  int ldo = o.ldo;
+  asm volatile("" : "+s"(ldo));  // keeps all the store offsets from being hoisted
+  const __amdgpu_buffer_rsrc_t ro = make_rsrc(o.out, (int64_t)o.rows * o.ldo * esz);
+  const int h = lane >> 5, row = wrow + (lane & 31), col = wcol + 4 * h;
+  const __amdgpu_buffer_rsrc_t rc =
+      make_rsrc(o.c, o.c != nullptr ? (int64_t)o.rows * o.ldo * esz : 0);
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      fence();
+      v16f y = acc[i][j];
+      asm volatile("" : "+v"(y));
+      const int ri = row + 32 * i, cj = col + 32 * j;
+      if (o.c != nullptr) {
+        if (out_f32) store_block_c<true, F16>(y, ro, rc, ldo, ri, cj, o.cols);
+        else store_block_c<false, F16>(y, ro, rc, ldo, ri, cj, o.cols);
+      } else {
+        if (out_f32) store_block<true, true>(y, ro, ldo, ri, cj, h, o.cols);
+        else store_block<true, false, F16>(y, ro, ldo, ri, cj, h, o.cols);
+      }
+      fence();
+    }
+}
+
+// ---------------------------------------------------------------- split contractions
+
+// With T tiles on a grid of P workgroups the last round holds L = T mod P tiles
+// (all of them when T < P).  Given a workspace, each of those is split along the
+// contraction into S <= min(P / L, kSplitMax) parts of whole stages; workgroup
+// L s' + s of that round takes part s of its tile s' and writes its float32
+// accumulators to the workspace, and a second kernel on the same stream adds each
+// tile's parts in the order s = 0, 1, .. and stores the tile, so the result does
+// not depend on which part ended first.
+//
+// Workspace: header (L, S), a record for each split tile, then the parts.
+constexpr int kSplitMax = 16;
+constexpr int64_t kWsHeader = 16384;
+constexpr int kMaxSplitTiles = (int)((kWsHeader - 64) / 32);
+
+struct SplitRecord {
+  int64_t out_off;
+  int32_t rows, cols, pad0, pad1;
+  int64_t pad2;
+};
+static_assert(sizeof(SplitRecord) == 32, "records fill the header");
+
+// Parts of a contraction of `stages` stages when `left` tiles are on `grid`
+// workgroups; a part keeps at least `least` stages.
+__host__ __device__ __forceinline__ int split_parts(int grid, int left, int stages, int least) {
+  if (left <= 0 || left > kMaxSplitTiles) return 1;
+  int s = grid / left;
+  if (s > kSplitMax) s = kSplitMax;
+  if (s > stages / least) s = stages / least;
+  return s < 2 ? 1 : s;
+}
+
+struct Work {
+  int tile, part, nparts;  // part < 0: a whole tile
+};
+
+// The work of a workgroup in a round; tile < 0: none left.
+__device__ __forceinline__ Work take_work(int round, int slot, int total, int nsplit) {
+  const int grid = (int)gridDim.x;
+  const int full = total / grid, left = total - full * grid;
+  Work k;
+  k.part = -1;
+  k.nparts = 1;
+  if (nsplit > 1 && round == full) {
+    const bool mine = slot < left * nsplit;
+    k.tile = mine ? full * grid + slot / nsplit : -1;
+    k.part = slot % nsplit;
+    k.nparts = nsplit;
+    return k;
+  }
+  k.tile = round * grid + slot;
+  if (k.tile >= total) k.tile = -1;
+  return k;
+}
+
+__device__ __forceinline__ void write_split_header(char* ws, int total, int nsplit) {
+  if (ws != nullptr && blockIdx.x == 0 && threadIdx.x == 0) {
+    int32_t* hdr = reinterpret_cast<int32_t*>(ws);
+    hdr[0] = nsplit > 1 ? total % (int)gridDim.x : 0;
+    hdr[1] = nsplit;
+  }
+}
+
+__device__ __forceinline__ void write_split_record(char* ws, int slot, int nsplit, const Tile& t) {
+  if (threadIdx.x == 0) {
+    SplitRecord* rec = reinterpret_cast<SplitRecord*>(ws + 64) + slot / nsplit;
+    rec->out_off = t.out_off;
+    rec->rows = t.a_rows;
+    rec->cols = t.b_rows;
+  }
+}
+
+// Narrows a tile to its part of the contraction.
+template <int MODE>
+__device__ __forceinline__ void narrow_tile(Tile& t, int part, int nsplit) {
+  const int stages = (t.kl + kStageK - 1) / kStageK;
+  const int k0 = (int)((int64_t)stages * part / nsplit) * kStageK;
+  int k1 = (int)((int64_t)stages * (part + 1) / nsplit) * kStageK;
+  if (k1 > t.kl) k1 = t.kl;
+  t.a += kColsA<MODE> ? (int64_t)k0 * t.lda : k0;
+  t.b += kColsB<MODE> ? (int64_t)k0 * t.ldb : k0;
+  t.kl = k1 - k0;
+}
+
+// A wave's accumulators as blocks of 1024 floats, [quarter][lane][4]; rows past
+// the live ones are left out.
+template <int MI, int NJ>
+__device__ __forceinline__ void store_part(float* __restrict__ part, const v16f (&acc)[MI][NJ],
+                                           int w, int lane, int wrow, int rows) {
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      float* dst = part + ((w * MI + i) * NJ + j) * 1024 + 4 * lane;
+      fence();
+      v16f y = acc[i][j];
+      asm volatile("" : "+v"(y));
+      if (wrow + 32 * i + (lane & 31) < rows) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<v4f*>(dst + 256 * q) =
+              v4f{y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]};
+      }
+      fence();
+    }
+}
+
+// The second step of a split: wave by wave one 32 x 32 block of a split tile.
+template <bool F16, int BM, int BN, int WN, int MI, int NJ>
+__global__ __launch_bounds__(kThreads) void split_reduce_kernel(const char* __restrict__ ws,
+                                                                char* out, const char* c,
+                                                                int64_t ldo, int out_f32) {
+  constexpr int kUnits = BM * BN / 1024;
+  const int32_t* hdr = reinterpret_cast<const int32_t*>(ws);
+  const int nl = hdr[0], nsplit = hdr[1];
+  if (nl <= 0) return;
+  const SplitRecord* recs = reinterpret_cast<const SplitRecord*>(ws + 64);
+  const float* parts = reinterpret_cast<const float*>(ws + kWsHeader);
+  const int lane = threadIdx.x & 63;
+  const int stride = (int)gridDim.x * (kThreads / 64);
+  for (int it = uni((int)blockIdx.x * (kThreads / 64) + (int)(threadIdx.x >> 6)); it < nl * kUnits;
+       it += stride) {
+    const int l = it / kUnits, u = it % kUnits;
+    const int w = u / (MI * NJ), i = u / NJ % MI, j = u % NJ;
+    const SplitRecord rec = recs[l];
+    const int wrow = (w / WN) * (32 * MI) + 32 * i, wcol = (w % WN) * (32 * NJ) + 32 * j;
+    if (wrow >= rec.rows || wcol >= rec.cols) continue;
+    v16f y[1][1];
+    y[0][0] = v16f{};
+    if (wrow + (lane & 31) < rec.rows) {
+      const float* src = parts + (int64_t)l * nsplit * (BM * BN) + u * 1024 + 4 * lane;
+#pragma unroll 4
+      for (int s = 0; s < nsplit; ++s) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const v4f v = *reinterpret_cast<const v4f*>(src + (int64_t)s * (BM * BN) + 256 * q);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[0][0][4 * q + e] += v[e];
+        }
+      }
+    }
+    OutTile o;
+    o.out = out + rec.out_off;
+    o.c = c != nullptr ? c + rec.out_off : nullptr;
+    o.ldo = (int)ldo;
+    o.rows = rec.rows;
+    o.cols = rec.cols;
+    store_blocks<F16, 1, 1>(y, o, out_f32, wrow, wcol, lane);
+  }
+}
+
+__device__ __forceinline__ OutTile out_tile(const Args& p, const Tile& t) {
+  OutTile o;
+  o.out = p.out + t.out_off;
+  o.c = p.c != nullptr ? p.c + t.out_off : nullptr;
+  o.ldo = (int)p.ldo;
+  o.rows = t.a_rows;
+  o.cols = t.b_rows;
+  return o;
+}
+
+// ---------------------------------------------------------------- launchers
+
+hipError_t launch_large(int mode, int f16, const Args& p, hipStream_t stream);
+hipError_t launch_small(int mode, int f16, int bm, const Args& p, hipStream_t stream);
+size_t large_workspace_bytes();
+size_t small_workspace_bytes();
+
+}  // namespace g16
+}  // namespace bsg
+
+#endif  // BSG_GEMM_16BIT_H
