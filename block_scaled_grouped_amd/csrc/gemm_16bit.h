@@ -21,13 +21,16 @@
 //            c ^ ((r / 2) % 8), so that 16 lanes reading one chunk of 16
 //            consecutive rows hit all 64 banks.
 //   columns: contraction index k at 2 BR k; chunk c (8 rows) in slot
-//            c ^ swz(k), so that the four 64-byte pieces that 32 lanes of a
-//            transposing read take from four consecutive k hit all 64 banks.
+//            c ^ swz(k), so that the eight 32-byte pieces that 32 lanes of a
+//            transposing read take (k = 0 .. 3 and 8 .. 11 of a step) hit all 64
+//            banks.
 //
-// Matrix instruction: v_mfma_f32_32x32x16, lane (r, h) = (l % 32, l / 32) holds
-// contraction indexes 8 h .. 8 h + 7 of row r.  B is its first operand and A
-// its second, so lane (r, h) ends with output row r, columns 8 q + 4 h + [0, 4)
-// in registers 4 q .. 4 q + 3 of a 32 x 32 block.
+// Matrix instruction: v_mfma_f32_16x16x32, lane (r, q) = (l % 16, l / 16) holds
+// contraction indexes 8 q .. 8 q + 7 of row r.  B is its first operand and A its
+// second, so lane (r, q) ends with output row r, columns 4 q + [0, 4) of a
+// 16 x 16 block.  On this chip products of random operands are limited by power:
+// a loop of these instructions alone runs at 2.06 PFLOP/s (2.04 GHz), one of
+// v_mfma_f32_32x32x16 at 1.78 (1.73 GHz), and both at 2.45 on zeros.
 #ifndef BSG_GEMM_16BIT_H
 #define BSG_GEMM_16BIT_H
 
@@ -194,120 +197,142 @@ __device__ __forceinline__ Tile find_tile(const Args& p, const Sched& sm, int ti
 
 template <int BR>
 __device__ __forceinline__ int swz(int k) {
-  if constexpr (BR >= 128) return 4 * (k & 3);
-  else if constexpr (BR == 64) return 4 * ((k >> 1) & 1);
-  else return 0;
+  const int low = BR >= 128 ? 4 * (k & 3) : BR == 64 ? 4 * ((k >> 1) & 1) : 0;
+  return low + 2 * ((k >> 3) & 1);
+}
+
+// Global -> LDS copy of 16 bytes a lane (1 KiB at at + IMM): as in lds_dma.h, but m0
+// is written and left (nothing else reads it), and something stands between its
+// writing and the load, which has to be one wait state later: MASKED picks the
+// lane's offset there (past every range for lanes outside of `mask`).
+template <int IMM, bool MASKED>
+__device__ __forceinline__ void copy16(const v4i& rsrc, uint32_t at, int voff, uint64_t mask) {
+  if constexpr (MASKED) {
+    int o;
+    asm volatile(
+        "s_add_u32 m0, %1, %2\n\t"
+        "v_cndmask_b32 %0, %3, %4, %5\n\t"
+        "buffer_load_dwordx4 %0, %6, 0 offen lds"
+        : "=&v"(o)
+        : "s"(at), "n"(IMM), "v"(kDmaOutOfRange), "v"(voff), "s"(mask), "s"(rsrc)
+        : "memory", "scc");
+  } else {
+    asm volatile(
+        "s_add_u32 m0, %0, %1\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %2, %3, 0 offen lds"
+        :
+        : "s"(at), "n"(IMM), "v"(voff), "s"(rsrc)
+        : "memory", "scc");
+  }
 }
 
 // One wave's share of the copies of an operand tile of BR rows: pieces w, w + 4,
-// .. of the tile's BR / 8 pieces of 1 KiB (a wave's pieces have one swizzle).
+// .. of the tile's BR / 8 pieces of 1 KiB.
 //   rows:    piece p is rows 8 p .. 8 p + 7, lane l row 8 p + l / 8, slot l % 8
 //   columns: piece p is 512 / BR contraction indexes, lane l index l / (BR / 8)
 //            of them, slot l % (BR / 8)
-// What lies past the tile's rows or the contraction is copied as zeros: by the
-// descriptor's range, or by an offset past every range.
+// A stage's descriptor begins at the stage, so a lane's offsets are the same in
+// every stage.  What lies past the tile's rows or the contraction is copied as
+// zeros: by the descriptor's range, by a column's offset past every range, or (rows,
+// a last stage that is not whole) by the stage's lane mask.
 template <bool COLS, int BR>
 struct Side {
   static constexpr int kPieces = BR / 32;  // per wave
   uint64_t base;
   int range;  // rows: bytes of the whole tile
   int ld2;    // bytes between memory rows
-  int off;    // this lane's offset in piece w, stage 0
-  int kc;     // rows: contraction index of this lane's chunk in a stage
-  int step;   // bytes from one of the wave's pieces to the next
   int kl;
+  uint64_t last;  // rows: lanes whose chunk lies within the contraction in the last stage
+  int off[kPieces];
 
-  // linear: lanes read consecutive chunks (for copies through registers);
-  // otherwise each lane reads the chunk that belongs in its LDS slot.
   __device__ __forceinline__ void init(const uint16_t* src, int64_t ld, int rows, int contraction,
-                                       int w, int lane, bool linear) {
+                                       int w, int lane) {
     base = (uint64_t)uni64((int64_t)reinterpret_cast<uint64_t>(src));
     ld2 = uni((int)(ld * 2));
     kl = uni(contraction);
     if constexpr (!COLS) {
       const int row = 8 * w + (lane >> 3);
-      const int c = (lane & 7) ^ (linear ? 0 : (row >> 1) & 7);
+      const int c = (lane & 7) ^ ((row >> 1) & 7);
       range = uni(rows) * ld2;
-      off = row * ld2 + c * 16;
-      kc = c * 8;
-      step = 32 * ld2;
+      last = __ballot(c * 8 < kl - (kl - 1) / kStageK * kStageK);
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) off[i] = (row + 32 * i) * ld2 + c * 16;
     } else {
       constexpr int cpr = BR / 8, rpp = 512 / BR;
-      const int k = rpp * w + lane / cpr;
-      const int c = (lane % cpr) ^ (linear ? 0 : swz<BR>(k));
       range = 0;
-      kc = 0;
-      off = c * 8 < rows ? k * ld2 + c * 16 : kDmaOutOfRange;
-      step = 4 * rpp * ld2;
+      last = 0;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int k = rpp * (w + 4 * i) + lane / cpr;
+        const int c = (lane % cpr) ^ swz<BR>(k);
+        off[i] = c * 8 < rows ? k * ld2 + c * 16 : kDmaOutOfRange;
+      }
     }
   }
 
-  // this lane's offset in the tile's LDS of piece w when it read linearly
-  __device__ __forceinline__ static int slot(int w, int lane) {
-    if constexpr (!COLS) {
-      const int row = 8 * w + (lane >> 3);
-      return row * 128 + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
-    } else {
-      constexpr int cpr = BR / 8, rpp = 512 / BR;
-      const int k = rpp * w + lane / cpr;
-      return k * (BR * 2) + (((lane % cpr) ^ swz<BR>(k)) << 4);
-    }
+  // Lanes whose chunk lies within the contraction in stage kt of `stages`.
+  __device__ __forceinline__ uint64_t mask(int kt, int stages) const {
+    return kt == stages - 1 ? last : ~0ull;
   }
 
-  // Base address and range of stage kt (nothing is in range when it is not live).
-  __device__ __forceinline__ uint64_t stage_base(int kt) const {
-    return COLS ? base + (uint64_t)kt * (uint64_t)(kStageK * (int64_t)ld2) : base;
-  }
-  __device__ __forceinline__ int stage_range(int kt, bool live) const {
-    if (!live) return 0;
-    if constexpr (!COLS) return range;
+  // Descriptor of stage kt (nothing is in range when it is not live).
+  __device__ __forceinline__ v4i rsrc(int kt, bool live) const {
+    const int64_t at = (int64_t)kt * (COLS ? kStageK * (int64_t)ld2 : 2 * kStageK);
     const int left = kl - kt * kStageK;
-    return (left < kStageK ? left : kStageK) * ld2;
+    const int bytes =
+        !live ? 0 : COLS ? (left < kStageK ? left : kStageK) * ld2 : range - kt * 2 * kStageK;
+    const uint64_t p = base + (uint64_t)at;
+    return v4i{(int)(uint32_t)p, (int)(uint32_t)(p >> 32), bytes, 0x00020000};
   }
-  __device__ __forceinline__ int piece_off(int i, int kt) const {
-    if constexpr (COLS) return off + i * step;
-    return kc < kl - kt * kStageK ? off + i * step + kt * (2 * kStageK) : kDmaOutOfRange;
+
+  template <int I, int IMM>
+  __device__ __forceinline__ void copy(const v4i& rs, uint32_t at, uint64_t m) const {
+    copy16<IMM, !COLS>(rs, at, off[I], m);
   }
 };
 
-__device__ __forceinline__ v4i rsrc_words(uint64_t base, int range) {
-  return v4i{(int)(uint32_t)base, (int)(uint32_t)(base >> 32), range, 0x00020000};
-}
-
 // ---------------------------------------------------------------- LDS -> registers
 
-// Offsets of a lane's fragment reads: one register a k16 step (rows; the 32-row
-// steps are immediates) or a 32-row block (columns; the k16 steps are).
+// Offsets of a lane's fragment reads: one register a half stage of 32 indexes
+// (rows; the 16-row steps are immediates) or a 16-row block (columns; the half
+// stages are).
 template <bool COLS, int BR, int NB>
 struct FragOff {
-  static constexpr int kRegs = COLS ? NB : 4;
+  static constexpr int kRegs = COLS ? NB : 2;
   int o[kRegs];
-  __device__ __forceinline__ void init(int row0, int lane) {
+  // tile: the operand's LDS; row0: the wave's first row
+  __device__ __forceinline__ void init(uint32_t tile, int row0, int lane) {
+    const int r = lane & 15, q = lane >> 4;
     if constexpr (!COLS) {
-      const int r = lane & 31, h = lane >> 5;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-        o[t] = (row0 + r) * 128 + (((2 * t + h) ^ ((r >> 1) & 7)) << 4);
+      for (int s = 0; s < 2; ++s)
+        o[s] = (int)tile + (row0 + r) * 128 + (((4 * s + q) ^ ((r >> 1) & 7)) << 4);
     } else {
-      const int h = lane >> 5, kk = (lane & 15) >> 2;
+      const int k = 8 * q + (r >> 2);
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
-        const int c = (row0 >> 3) + 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-        o[i] = (8 * h + kk) * (BR * 2) + ((c ^ swz<BR>(kk)) << 4) + 8 * (lane & 1);
+        const int c = (row0 >> 3) + 2 * i + ((lane & 3) >> 1);
+        o[i] = (int)tile + k * (BR * 2) + ((c ^ swz<BR>(k)) << 4) + 8 * (lane & 1);
       }
     }
 #pragma unroll
     for (int t = 0; t < kRegs; ++t) asm volatile("" : "+v"(o[t]));
   }
-  // Rows 32 I + lane % 32, contraction indexes 16 T + 8 (lane / 32) + [0, 8).
-  template <int I, int T>
-  __device__ __forceinline__ v4i read(uint32_t tile) const {
+  template <int T>
+  __device__ __forceinline__ void move(int bytes) {
+    o[T] += bytes;
+  }
+  // Rows 16 I + lane % 16, contraction indexes 32 S + 8 (lane / 16) + [0, 8).
+  // at: bytes from the tile given to init.
+  template <int I, int S>
+  __device__ __forceinline__ v4i read(uint32_t at = 0) const {
     if constexpr (!COLS) {
-      return *reinterpret_cast<const lds_v4i*>((size_t)(tile + o[T] + I * 4096));
+      return *reinterpret_cast<const lds_v4i*>((size_t)(uint32_t)(o[S] + at + I * 2048));
     } else {
-      const uint32_t at = tile + o[I] + T * 32 * BR;
-      const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(size_t)at);
-      const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(size_t)(at + 8 * BR));
+      const uint32_t p = o[I] + at + S * 64 * BR;
+      const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(size_t)p);
+      const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(size_t)(p + 8 * BR));
       const v2i l = __builtin_bit_cast(v2i, lo), u = __builtin_bit_cast(v2i, hi);
       return v4i{l[0], l[1], u[0], u[1]};
     }
@@ -315,12 +340,12 @@ struct FragOff {
 };
 
 template <bool F16>
-__device__ __forceinline__ v16f mfma16(const v4i& x, const v4i& y, const v16f& acc) {
+__device__ __forceinline__ v4f mfma16(const v4i& x, const v4i& y, const v4f& acc) {
   if constexpr (F16)
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, x),
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x),
                                                   __builtin_bit_cast(v8h, y), acc, 0, 0, 0);
   else
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, x),
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x),
                                                    __builtin_bit_cast(v8bf, y), acc, 0, 0, 0);
 }
 
@@ -343,33 +368,27 @@ __device__ __forceinline__ int request_of(const int64_t* off, int G, int64_t row
 }
 
 // Adds each row's own low-rank product to a wave's accumulators: for every
-// adapter that occurs in a 32-row block one product of the block's low rows (both
+// adapter that occurs in a 16-row block one product of the block's low rows (both
 // halves) with the adapter's rows of `up`, kept for its own rows only.  So what
 // an adapter holds (infinities, NaN) never reaches a row of another request, and
-// the cost follows the adapters that meet in 32 rows, not the requests.  The
-// operands come straight from the L2: 2 r / 16 matrix instructions a block and
-// adapter are few against the projection's k / 16.
+// the cost follows the adapters that meet in 16 rows, not the requests.  The
+// operands come straight from the L2: 2 r / 32 matrix instructions a block and
+// adapter are few against the projection's k / 32.
 // ids: adapter of each of the tile's rows (-1: none).  A split tile's parts
 // share the adapters out: the c-th of a block goes to part c % nparts.
 template <bool F16, int MI, int NJ>
 __device__ __forceinline__ void add_low_rank(const Args& p, const Tile& t, const int* ids, int wrow,
                                              int wcol, int lane, int part, int nparts,
-                                             v16f (&acc)[MI][NJ]) {
-  const int r = lane & 31, h = lane >> 5, rank = p.r;
-  const uint16_t* urow[NJ];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    int col = wcol + 32 * j + r;
-    if (col >= t.b_rows) col = t.b_rows - 1;  // such columns are not stored
-    urow[j] = p.up + (t.col0 + col) * rank + 8 * h;
-  }
+                                             v4f (&acc)[MI][NJ]) {
+  const int r = lane & 15, q = lane >> 4, rank = p.r;
+  const uint16_t* up = p.up + t.col0 * rank + 8 * q;
   static_for<MI>([&](auto ic) {
     constexpr int i = decltype(ic)::value;
-    const int row = wrow + 32 * i + r;
+    const int row = wrow + 16 * i + r;
     const int id = ids[row];
     const int lrow = row < t.a_rows ? row : t.a_rows - 1;
-    const uint16_t* low = p.low + (t.row0 + lrow) * 2 * rank + 8 * h;
-    uint32_t todo = (uint32_t)__ballot(id >= 0);
+    const uint16_t* low = p.low + (t.row0 + lrow) * 2 * rank + 8 * q;
+    uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xffffu;
     int turn = 0;
     while (todo != 0) {
       const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
@@ -379,29 +398,41 @@ __device__ __forceinline__ void add_low_rank(const Args& p, const Tile& t, const
         turn = turn + 1 == nparts ? 0 : turn + 1;
         if (!mine) continue;
       }
-      const int64_t ua = (int64_t)a * p.n * rank;
-      // one block at a time: the large form's accumulators leave no room for more
-      static_for<NJ>([&](auto jc) {
-        constexpr int j = decltype(jc)::value;
-        v16f one = v16f{};
-#pragma unroll 2
-        for (int k = 0; k < rank; k += 16) {
-          v4i l0 = v4i{0, 0, 0, 0}, l1 = l0, u = l0;
-          if (k + 8 * h < rank) {  // a rank of 8 (mod 16) ends within the step
+      const uint16_t* ua = up + (int64_t)a * p.n * rank;
+      // a few blocks at a time: the large form's accumulators leave no room for more
+      constexpr int kGroup = NJ < 4 ? NJ : 4;
+      static_for<NJ / kGroup>([&](auto jc) {
+        constexpr int j0 = decltype(jc)::value * kGroup;
+        v4f one[kGroup];
+        const uint16_t* urow[kGroup];
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) {
+          one[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+          int col = wcol + 16 * (j0 + j) + r;
+          if (col >= t.b_rows) col = t.b_rows - 1;  // such columns are not stored
+          urow[j] = ua + (int64_t)col * rank;
+        }
+        for (int k = 0; k < rank; k += 32) {
+          v4i l0 = v4i{0, 0, 0, 0}, l1 = l0, u[kGroup];
+#pragma unroll
+          for (int j = 0; j < kGroup; ++j) u[j] = l0;
+          if (k + 8 * q < rank) {  // the rank may end within the step
             l0 = *reinterpret_cast<const v4i*>(low + k);
             l1 = *reinterpret_cast<const v4i*>(low + rank + k);
-            u = *reinterpret_cast<const v4i*>(urow[j] + ua + k);
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) u[j] = *reinterpret_cast<const v4i*>(urow[j] + k);
           }
-          one = mfma16<F16>(u, l0, one);
-          one = mfma16<F16>(u, l1, one);
+#pragma unroll
+          for (int j = 0; j < kGroup; ++j) one[j] = mfma16<F16>(u[j], l0, one[j]);
+#pragma unroll
+          for (int j = 0; j < kGroup; ++j) one[j] = mfma16<F16>(u[j], l1, one[j]);
         }
         fence();
-        v16f y = acc[i][j];
-        asm volatile("" : "+v"(y));
 #pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] = id == a ? y[e] + one[e] : y[e];
-        acc[i][j] = y;
-        asm volatile("" : "+a"(acc[i][j]));
+        for (int j = 0; j < kGroup; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[i][j0 + j][e] = id == a ? acc[i][j0 + j][e] + one[j][e] : acc[i][j0 + j][e];
         fence();
       });
     }
@@ -418,49 +449,6 @@ __device__ __forceinline__ void tile_adapters(const Args& p, const Sched& sm, co
 
 // ---------------------------------------------------------------- epilogue
 
-// One 32 x 32 block with C added in float32 before the one rounding.
-template <bool F32, bool F16>
-__device__ __forceinline__ void store_block_c(const v16f& acc, __amdgpu_buffer_rsrc_t ro,
-                                              __amdgpu_buffer_rsrc_t rc, int ldo, int row, int col0,
-                                              int out_cols) {
-  constexpr int esz = F32 ? 4 : 2;
-  int off[4];
-  float c[16];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int col = col0 + 8 * q;
-    off[q] = col < out_cols ? (row * ldo + col) * esz : (int)kDropped;
-    if constexpr (F32) {
-      const v4i v = __builtin_amdgcn_raw_buffer_load_b128(rc, off[q], 0, 0);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) c[4 * q + e] = __int_as_float(v[e]);
-    } else {
-      const v2i v = __builtin_amdgcn_raw_buffer_load_b64(rc, off[q], 0, 0);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t bits = ((uint32_t)v[e >> 1] >> (16 * (e & 1))) & 0xffffu;
-        c[4 * q + e] = F16 ? (float)__builtin_bit_cast(_Float16, (unsigned short)bits)
-                           : bf16_to_f32(bits);
-      }
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    float y[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = acc[4 * q + e] + c[4 * q + e];
-    if constexpr (F32) {
-      __builtin_amdgcn_raw_buffer_store_b128(
-          (v4i){__float_as_int(y[0]), __float_as_int(y[1]), __float_as_int(y[2]),
-                __float_as_int(y[3])},
-          ro, off[q], 0, 0);
-    } else {
-      __builtin_amdgcn_raw_buffer_store_b64(
-          (v2i){(int)pack16<F16>(y[0], y[1]), (int)pack16<F16>(y[2], y[3])}, ro, off[q], 0, 0);
-    }
-  }
-}
-
 // Where a tile's output goes: its first element, live rows and columns.
 struct OutTile {
   char* out;
@@ -468,33 +456,88 @@ struct OutTile {
   int ldo, rows, cols;
 };
 
-// A wave's MI x NJ blocks, the first at (row, col) of the tile, one at a time:
-// each block's accumulators are copied out right before its loads and stores.
+// Two neighbouring 16 x 16 blocks of accumulators, the first at column col0: this
+// lane's row `row`, columns col0 + 16 b + 4 q + [0, 4).  Rows past the live ones
+// are dropped by the descriptors' range, columns past out_cols by an offset past
+// every range.  C is added in float32 before the one rounding.
+//   float32: a store is 16 bytes a lane, 64-byte runs of 16 rows.
+//   16-bit:  lanes trade halves of the two blocks (v_permlane16_swap), after which
+//            lane (r, q) holds columns 8 (q / 2) + [0, 8) of block q % 2: 16 bytes
+//            a lane, and again 64-byte runs of 16 rows.
+template <bool F32, bool F16>
+__device__ __forceinline__ void store_pair(v4f y0, v4f y1, __amdgpu_buffer_rsrc_t ro,
+                                           __amdgpu_buffer_rsrc_t rc, bool add, int ldo, int row,
+                                           int col0, int q, int out_cols) {
+  constexpr int esz = F32 ? 4 : 2;
+  int off[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int col = col0 + 16 * b + 4 * q;
+    off[b] = col < out_cols ? (row * ldo + col) * esz : (int)kDropped;
+  }
+  if (add) {
+    float c[8];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if constexpr (F32) {
+        const v4i v = __builtin_amdgcn_raw_buffer_load_b128(rc, off[b], 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[4 * b + e] = __int_as_float(v[e]);
+      } else {
+        const v2i v = __builtin_amdgcn_raw_buffer_load_b64(rc, off[b], 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t bits = ((uint32_t)v[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+          c[4 * b + e] = F16 ? (float)__builtin_bit_cast(_Float16, (unsigned short)bits)
+                             : bf16_to_f32(bits);
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      y0[e] += c[e];
+      y1[e] += c[4 + e];
+    }
+  }
+  if constexpr (F32) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, y0), ro, off[0], 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, y1), ro, off[1], 0, 0);
+  } else {
+    const auto lo = __builtin_amdgcn_permlane16_swap((int)pack16<F16>(y0[0], y0[1]),
+                                                     (int)pack16<F16>(y1[0], y1[1]), false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap((int)pack16<F16>(y0[2], y0[3]),
+                                                     (int)pack16<F16>(y1[2], y1[3]), false, false);
+    const int col = col0 + 16 * (q & 1) + 8 * (q >> 1);
+    const int at = col < out_cols ? (row * ldo + col) * 2 : (int)kDropped;
+    __builtin_amdgcn_raw_buffer_store_b128(
+        (v4i){(int)lo[0], (int)hi[0], (int)lo[1], (int)hi[1]}, ro, at, 0, 0);
+  }
+}
+
+// A wave's MI x NJ blocks, the first at (wrow, wcol) of the tile, two at a time:
+// the accumulators are copied out right before their loads and stores.
 template <bool F16, int MI, int NJ>
-__device__ __forceinline__ void store_blocks(const v16f (&acc)[MI][NJ], const OutTile& o,
+__device__ __forceinline__ void store_blocks(const v4f (&acc)[MI][NJ], const OutTile& o,
                                              int out_f32, int wrow, int wcol, int lane) {
+  static_assert(NJ % 2 == 0, "blocks are stored in pairs");
   const int esz = out_f32 ? 4 : 2;
   int ldo = o.ldo;
   asm volatile("" : "+s"(ldo));  // keeps all the store offsets from being hoisted
   const __amdgpu_buffer_rsrc_t ro = make_rsrc(o.out, (int64_t)o.rows * o.ldo * esz);
-  const int h = lane >> 5, row = wrow + (lane & 31), col = wcol + 4 * h;
-  const __amdgpu_buffer_rsrc_t rc =
-      make_rsrc(o.c, o.c != nullptr ? (int64_t)o.rows * o.ldo * esz : 0);
+  const bool add = o.c != nullptr;
+  const __amdgpu_buffer_rsrc_t rc = make_rsrc(o.c, add ? (int64_t)o.rows * o.ldo * esz : 0);
+  const int q = lane >> 4, row = wrow + (lane & 15);
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
+    for (int j = 0; j < NJ; j += 2) {
       fence();
-      v16f y = acc[i][j];
-      asm volatile("" : "+v"(y));
-      const int ri = row + 32 * i, cj = col + 32 * j;
-      if (o.c != nullptr) {
-        if (out_f32) store_block_c<true, F16>(y, ro, rc, ldo, ri, cj, o.cols);
-        else store_block_c<false, F16>(y, ro, rc, ldo, ri, cj, o.cols);
-      } else {
-        if (out_f32) store_block<true, true>(y, ro, ldo, ri, cj, h, o.cols);
-        else store_block<true, false, F16>(y, ro, ldo, ri, cj, h, o.cols);
-      }
+      v4f y0 = acc[i][j], y1 = acc[i][j + 1];
+      asm volatile("" : "+v"(y0), "+v"(y1));
+      if (out_f32)
+        store_pair<true, F16>(y0, y1, ro, rc, add, ldo, row + 16 * i, wcol + 16 * j, q, o.cols);
+      else
+        store_pair<false, F16>(y0, y1, ro, rc, add, ldo, row + 16 * i, wcol + 16 * j, q, o.cols);
       fence();
     }
 }
@@ -583,35 +626,30 @@ __device__ __forceinline__ void narrow_tile(Tile& t, int part, int nsplit) {
   t.kl = k1 - k0;
 }
 
-// A wave's accumulators as blocks of 1024 floats, [quarter][lane][4]; rows past
-// the live ones are left out.
+// A wave's accumulators as blocks of 256 floats, [lane][4]; rows past the live
+// ones are left out.
 template <int MI, int NJ>
-__device__ __forceinline__ void store_part(float* __restrict__ part, const v16f (&acc)[MI][NJ],
+__device__ __forceinline__ void store_part(float* __restrict__ part, const v4f (&acc)[MI][NJ],
                                            int w, int lane, int wrow, int rows) {
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      float* dst = part + ((w * MI + i) * NJ + j) * 1024 + 4 * lane;
       fence();
-      v16f y = acc[i][j];
+      v4f y = acc[i][j];
       asm volatile("" : "+v"(y));
-      if (wrow + 32 * i + (lane & 31) < rows) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<v4f*>(dst + 256 * q) =
-              v4f{y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]};
-      }
+      if (wrow + 16 * i + (lane & 15) < rows)
+        *reinterpret_cast<v4f*>(part + ((w * MI + i) * NJ + j) * 256 + 4 * lane) = y;
       fence();
     }
 }
 
-// The second step of a split: wave by wave one 32 x 32 block of a split tile.
+// The second step of a split: wave by wave one pair of blocks of a split tile.
 template <bool F16, int BM, int BN, int WN, int MI, int NJ>
 __global__ __launch_bounds__(kThreads) void split_reduce_kernel(const char* __restrict__ ws,
                                                                 char* out, const char* c,
                                                                 int64_t ldo, int out_f32) {
-  constexpr int kUnits = BM * BN / 1024;
+  constexpr int kUnits = BM * BN / 512;
   const int32_t* hdr = reinterpret_cast<const int32_t*>(ws);
   const int nl = hdr[0], nsplit = hdr[1];
   if (nl <= 0) return;
@@ -622,21 +660,21 @@ __global__ __launch_bounds__(kThreads) void split_reduce_kernel(const char* __re
   for (int it = uni((int)blockIdx.x * (kThreads / 64) + (int)(threadIdx.x >> 6)); it < nl * kUnits;
        it += stride) {
     const int l = it / kUnits, u = it % kUnits;
-    const int w = u / (MI * NJ), i = u / NJ % MI, j = u % NJ;
+    const int w = u / (MI * NJ / 2), i = u / (NJ / 2) % MI, j = u % (NJ / 2) * 2;
     const SplitRecord rec = recs[l];
-    const int wrow = (w / WN) * (32 * MI) + 32 * i, wcol = (w % WN) * (32 * NJ) + 32 * j;
+    const int wrow = (w / WN) * (16 * MI) + 16 * i, wcol = (w % WN) * (16 * NJ) + 16 * j;
     if (wrow >= rec.rows || wcol >= rec.cols) continue;
-    v16f y[1][1];
-    y[0][0] = v16f{};
-    if (wrow + (lane & 31) < rec.rows) {
-      const float* src = parts + (int64_t)l * nsplit * (BM * BN) + u * 1024 + 4 * lane;
-#pragma unroll 4
+    v4f y[1][2];
+    y[0][0] = y[0][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    if (wrow + (lane & 15) < rec.rows) {
+      const float* src = parts + (int64_t)l * nsplit * (BM * BN) + u * 512 + 4 * lane;
+#pragma unroll 8
       for (int s = 0; s < nsplit; ++s) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const v4f v = *reinterpret_cast<const v4f*>(src + (int64_t)s * (BM * BN) + 256 * q);
+        for (int b = 0; b < 2; ++b) {
+          const v4f v = *reinterpret_cast<const v4f*>(src + (int64_t)s * (BM * BN) + 256 * b);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[0][0][4 * q + e] += v[e];
+          for (int e = 0; e < 4; ++e) y[0][b][e] += v[e];
         }
       }
     }
@@ -646,7 +684,7 @@ __global__ __launch_bounds__(kThreads) void split_reduce_kernel(const char* __re
     o.ldo = (int)ldo;
     o.rows = rec.rows;
     o.cols = rec.cols;
-    store_blocks<F16, 1, 1>(y, o, out_f32, wrow, wcol, lane);
+    store_blocks<F16, 1, 2>(y, o, out_f32, wrow, wcol, lane);
   }
 }
 

@@ -27,6 +27,16 @@ __device__ __forceinline__ void split16(float s, uint32_t& top, uint32_t& rest) 
   rest = pack16<F16>(left, left) & 0xffffu;
 }
 
+template <bool F16>
+__device__ __forceinline__ v16f mfma32(const v4i& x, const v4i& y, const v16f& acc) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, x),
+                                                  __builtin_bit_cast(v8h, y), acc, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, x),
+                                                   __builtin_bit_cast(v8bf, y), acc, 0, 0, 0);
+}
+
 // low[t, 0..r) + low[t, r..2r) = scale_a X[t, :] A_a^T.
 //
 // A workgroup of eight waves takes 32 consecutive rows, 64 rank columns and one
@@ -91,8 +101,8 @@ __global__ __launch_bounds__(kLowThreads) void lora_low_kernel(Args p, const uin
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          acc[0] = mfma16<F16>(f0[c], fx[c], acc[0]);
-          if (two) acc[1] = mfma16<F16>(f1[c], fx[c], acc[1]);
+          acc[0] = mfma32<F16>(f0[c], fx[c], acc[0]);
+          if (two) acc[1] = mfma32<F16>(f1[c], fx[c], acc[1]);
         }
       }
 #pragma unroll

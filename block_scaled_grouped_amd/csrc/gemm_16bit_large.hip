@@ -1,6 +1,6 @@
 // 16-bit grouped products, large form: 256 x 256 output tiles, one persistent
 // workgroup of four wavefronts on each compute unit, each wave 128 x 128 of the
-// output as 4 x 4 blocks of 32 x 32 (256 accumulator registers a lane).
+// output as 8 x 8 blocks of 16 x 16 (256 accumulator registers a lane).
 //
 // A stage is 64 contraction indexes (32 KiB an operand); two LDS buffers.  While
 // stage s is consumed from one, stage s + 1 lands in the other, and the copies of
@@ -19,146 +19,143 @@ namespace {
 
 constexpr int BM = 256, BN = 256;
 constexpr int kTileBytes = 256 * 128;
-constexpr int kBufBytes = 2 * kTileBytes;
-constexpr int kPieces = 8;          // per wave, operand and stage
-constexpr int kBarrierSlot = 4;     // matrix instruction of a stage's second half that
-                                    // the barrier follows
+constexpr int kBufBytes = 2 * kTileBytes;  // A's tile, then B's
+// Places in a stage's 128 matrix instructions: where its buffer is free for the
+// next copies, where the next stage has to be there, and the copies between.
+constexpr int kFreeSlot = 36;
+constexpr int kReadySlot = 72;
+constexpr int kCopySlot = 38, kCopyStep = 4;
+constexpr int kCopies = 16;  // per wave and stage: 8 of A, 8 of B
+constexpr int kCopiesBeforeReady = (kReadySlot - kCopySlot + kCopyStep - 1) / kCopyStep;
+static_assert(kCopySlot + (kCopies - 1) * kCopyStep < 128 && kReadySlot + 32 <= 128 &&
+                  kReadySlot - kFreeSlot >= 34,
+              "schedule");
 constexpr int64_t kPartBytes = (int64_t)BM * BN * 4;
 
-typedef v4i Half[2][4];  // fragments of 32 contraction indexes: [k16 step][block]
+typedef v4i Half[8];  // an operand's fragments of 32 contraction indexes
 
+// This wave's copies of a stage.
 template <int MODE>
 struct Copies {
   Side<kColsA<MODE>, BM> a;
   Side<kColsB<MODE>, BN> b;
-  int bslot;  // this lane's LDS offset of a piece of B
-  uint32_t lds;
-  int w;
+  uint32_t lds;   // of the buffer that is being copied to
+  int stages;
+  v4i ra, rb;     // descriptors and lanes of the stage that is being copied
+  uint64_t ma, mb;
+
+  __device__ __forceinline__ void begin(int kt) {
+    const bool live = kt < stages;
+    ra = a.rsrc(kt, live);
+    rb = b.rsrc(kt, live);
+    ma = a.mask(kt, stages);
+    mb = b.mask(kt, stages);
+  }
+  template <int P>
+  __device__ __forceinline__ void copy() const {
+    if constexpr (P < 8) a.template copy<P, P * 4096>(ra, lds, ma);
+    else b.template copy<P - 8, kTileBytes + (P - 8) * 4096>(rb, lds, mb);
+  }
 };
 
-__device__ __forceinline__ uint32_t buf_a(uint32_t lds, int s) { return lds + s * kBufBytes; }
-__device__ __forceinline__ uint32_t buf_b(uint32_t lds, int s) {
-  return lds + s * kBufBytes + kTileBytes;
-}
-
-template <int P, int MODE>
-__device__ __forceinline__ void copy_a(const Copies<MODE>& c, v4i rsrc, int s, int kt) {
-  dma16(rsrc, buf_a(c.lds, s) + c.w * 1024 + P * 4096, c.a.piece_off(P, kt));
-}
-
-template <int Q, int MODE>
-__device__ __forceinline__ void load_b(const Copies<MODE>& c, __amdgpu_buffer_rsrc_t rsrc, int kt,
-                                       v4i (&stage)[kPieces]) {
-  stage[Q] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, c.b.piece_off(Q, kt), 0, 0);
-}
-
-template <int Q, int MODE>
-__device__ __forceinline__ void store_b(const Copies<MODE>& c, int s, const v4i (&stage)[kPieces]) {
-  *reinterpret_cast<lds_v4i*>((size_t)(buf_b(c.lds, s) + c.bslot + Q * 4096)) = stage[Q];
-}
-
-template <int MODE>
-__device__ __forceinline__ v4i a_rsrc(const Copies<MODE>& c, int kt, int stages) {
-  return rsrc_words(c.a.stage_base(kt), c.a.stage_range(kt, kt < stages));
-}
-template <int MODE>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t b_rsrc(const Copies<MODE>& c, int kt, int stages) {
-  return make_rsrc(reinterpret_cast<const void*>(c.b.stage_base(kt)),
-                   c.b.stage_range(kt, kt < stages));
-}
-
 // Fragment Q of the 16 of half S of a stage, in the order the matrix instructions
-// first use them: for each k16 step A0, B0, B1, B2, B3, A1, A2, A3.
+// first use them: A0, B0 .. B7, A1 .. A7.
 template <int MODE, int S, int Q>
-__device__ __forceinline__ void read_frag(uint32_t lds, int s,
-                                          const FragOff<kColsA<MODE>, BM, 4>& fa,
-                                          const FragOff<kColsB<MODE>, BN, 4>& fb, Half& a, Half& b) {
-  constexpr int u = Q >> 3, k = Q & 7, T = 2 * S + u;
-  if constexpr (k == 0 || k >= 5) {
-    constexpr int i = k == 0 ? 0 : k - 4;
-    a[u][i] = fa.template read<i, T>(buf_a(lds, s));
+__device__ __forceinline__ void read_frag(const FragOff<kColsA<MODE>, BM, 8>& fa,
+                                          const FragOff<kColsB<MODE>, BN, 8>& fb, Half& a, Half& b) {
+  if constexpr (Q == 0 || Q >= 9) {
+    constexpr int i = Q == 0 ? 0 : Q - 8;
+    a[i] = fa.template read<i, S>();
   } else {
-    b[u][k - 1] = fb.template read<k - 1, T>(buf_b(lds, s));
+    b[Q - 1] = fb.template read<Q - 1, S>();
   }
 }
 
+// The instruction itself, its accumulator tied to its own registers: left to
+// the intrinsic, the register allocator moves a good part of the 256 accumulators
+// around in every stage.  Its operands come from LDS reads (for whose arrival the
+// compiler waits), never from a vector instruction right before it, and an
+// accumulator is used again 64 instructions later, so it needs no wait states here;
+// mfma_drain() ends a run of them.
 template <bool F16, int M>
-__device__ __forceinline__ void mfma(const Half& a, const Half& b, v16f (&acc)[4][4]) {
-  constexpr int u = M >> 4, i = (M >> 2) & 3, j = M & 3;
-  acc[i][j] = mfma16<F16>(b[u][j], a[u][i], acc[i][j]);
-  // the intrinsic has no side effects, so passes may sink it past the fences; an
-  // opaque use of its result keeps it in place
-  asm volatile("" : "+a"(acc[i][j]));
+__device__ __forceinline__ void mfma(const Half& a, const Half& b, v4f (&acc)[8][8]) {
+  if constexpr (F16)
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0"
+                 : "+a"(acc[M >> 3][M & 7])
+                 : "v"(b[M & 7]), "v"(a[M >> 3]));
+  else
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0"
+                 : "+a"(acc[M >> 3][M & 7])
+                 : "v"(b[M & 7]), "v"(a[M >> 3]));
 }
+
+// Wait states before the accumulators of a run are read by vector instructions.
+__device__ __forceinline__ void mfma_drain() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
 // One tile's contraction.
 template <int MODE, bool F16>
 __device__ __forceinline__ void contract(uint32_t lds, const Tile& t, int w, int lane,
-                                         v16f (&acc)[4][4]) {
+                                         v4f (&acc)[8][8]) {
   const int stages = uni((t.kl + kStageK - 1) / kStageK);
   if (stages == 0) return;
   Copies<MODE> c;
-  c.a.init(t.a, t.lda, t.a_rows, t.kl, w, lane, false);
-  c.b.init(t.b, t.ldb, t.b_rows, t.kl, w, lane, true);
-  c.bslot = Side<kColsB<MODE>, BN>::slot(w, lane);
-  c.lds = lds;
-  c.w = w;
-  FragOff<kColsA<MODE>, BM, 4> fa;
-  FragOff<kColsB<MODE>, BN, 4> fb;
-  fa.init((w >> 1) * 128, lane);
-  fb.init((w & 1) * 128, lane);
-
-  // stage 0 into buffer 0; stage 1's A into buffer 1 and its B into registers
-  v4i stage[kPieces];
-  {
-    const __amdgpu_buffer_rsrc_t r = b_rsrc(c, 0, stages);
-    static_for<kPieces>([&](auto q) { load_b<decltype(q)::value>(c, r, 0, stage); });
-    const v4i ra = a_rsrc(c, 0, stages);
-    static_for<kPieces>([&](auto q) { copy_a<decltype(q)::value>(c, ra, 0, 0); });
-    static_for<kPieces>([&](auto q) { store_b<decltype(q)::value>(c, 0, stage); });
-    const v4i ra1 = a_rsrc(c, 1, stages);
-    static_for<kPieces>([&](auto q) { copy_a<decltype(q)::value>(c, ra1, 1, 1); });
-    const __amdgpu_buffer_rsrc_t r1 = b_rsrc(c, 1, stages);
-    static_for<kPieces>([&](auto q) { load_b<decltype(q)::value>(c, r1, 1, stage); });
-  }
-  wait_and_barrier<2 * kPieces>();
+  c.a.init(t.a, t.lda, t.a_rows, t.kl, w, lane);
+  c.b.init(t.b, t.ldb, t.b_rows, t.kl, w, lane);
+  c.lds = uni(lds + w * 1024);
+  c.stages = stages;
+  using FragsA = FragOff<kColsA<MODE>, BM, 8>;
+  using FragsB = FragOff<kColsB<MODE>, BN, 8>;
+  FragsA fa;
+  FragsB fb;
+  fa.init(lds, (w >> 1) * 128, lane);
+  fb.init(lds + kTileBytes, (w & 1) * 128, lane);
+  c.begin(0);
+  static_for<kCopies>([&](auto q) { c.template copy<decltype(q)::value>(); });
+  c.lds += kBufBytes;
+  c.begin(1);
+  static_for<kCopies>([&](auto q) { c.template copy<decltype(q)::value>(); });
+  c.lds -= kBufBytes;
+  wait_and_barrier<kCopies>();
   Half a0, b0, a1, b1;
-  static_for<16>([&](auto q) { read_frag<MODE, 0, decltype(q)::value>(lds, 0, fa, fb, a0, b0); });
+  static_for<16>([&](auto q) { read_frag<MODE, 0, decltype(q)::value>(fa, fb, a0, b0); });
+  int other = kBufBytes;  // bytes to the other buffer
   for (int kt = 0; kt < stages; ++kt) {
-    const int s = kt & 1;
-    const __amdgpu_buffer_rsrc_t rb = b_rsrc(c, kt + 2, stages);
-    const v4i ra = a_rsrc(c, kt + 2, stages);
-    // first half: the second half's fragments (same buffer), then, one register at
-    // a time, stage kt + 1's B into the other buffer and the loads of stage kt + 2's
-    static_for<32>([&](auto mc) {
+    c.begin(kt + 2);
+    fence();
+    static_for<128>([&](auto mc) {
       constexpr int m = decltype(mc)::value;
-      mfma<F16, m>(a0, b0, acc);
+      if constexpr (m < 64) mfma<F16, m>(a0, b0, acc);
+      else mfma<F16, m - 64>(a1, b1, acc);
       fence();
-      if constexpr (m < 16) {
-        read_frag<MODE, 1, m>(lds, s, fa, fb, a1, b1);
-      } else if constexpr (m % 2 == 0) {
-        constexpr int q = (m - 16) / 2;
-        store_b<q>(c, s ^ 1, stage);
-        load_b<q>(c, rb, kt + 2, stage);
+      // the second half's fragments
+      if constexpr (m < 32 && m % 2 == 0) read_frag<MODE, 1, m / 2>(fa, fb, a1, b1);
+      // every wave has read this buffer
+      if constexpr (m == kFreeSlot) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      // the reads move to the other buffer
+      if constexpr (m > kFreeSlot && m % 2 == 1) {
+        constexpr int q = (m - kFreeSlot) / 2;
+        if constexpr (q < FragsA::kRegs) fa.template move<q>(other);
+        else if constexpr (q < FragsA::kRegs + FragsB::kRegs)
+          fb.template move<q - FragsA::kRegs>(other);
       }
+      // the other buffer holds the next stage for every wave
+      if constexpr (m == kReadySlot)
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kCopiesBeforeReady) : "memory");
+      // the next stage's first half's fragments
+      if constexpr (m >= kReadySlot && m < kReadySlot + 32 && m % 2 == 0)
+        read_frag<MODE, 0, (m - kReadySlot) / 2>(fa, fb, a0, b0);
+      // the stage after next into this buffer
+      if constexpr (m >= kCopySlot && (m - kCopySlot) % kCopyStep == 0 &&
+                    (m - kCopySlot) / kCopyStep < kCopies)
+        c.template copy<(m - kCopySlot) / kCopyStep>();
       fence();
     });
-    // second half: after the barrier the other buffer holds stage kt + 1 for every
-    // wave and this one is free: A of stage kt + 2 into it, and the first fragments
-    // of stage kt + 1
-    static_for<32>([&](auto mc) {
-      constexpr int m = decltype(mc)::value;
-      mfma<F16, m>(a1, b1, acc);
-      fence();
-      if constexpr (m == kBarrierSlot) wait_and_barrier<kPieces>();
-      if constexpr (m >= kBarrierSlot) {
-        constexpr int q = m - kBarrierSlot;
-        if constexpr (q < 16) read_frag<MODE, 0, q>(lds, s ^ 1, fa, fb, a0, b0);
-        if constexpr (q % 3 == 1 && q / 3 < kPieces) copy_a<q / 3>(c, ra, s, kt + 2);
-      }
-      fence();
-    });
+    c.lds += other;
+    other = -other;
   }
+  fence();
+  mfma_drain();
+  fence();
 }
 
 template <int MODE, bool F16>
@@ -187,26 +184,26 @@ __global__ __launch_bounds__(kThreads) void large_kernel(Args p) {
     asm volatile("" : "+v"(tid));
     const int lane = tid & 63, w = uni(tid >> 6);
     const int wrow = (w >> 1) * 128, wcol = (w & 1) * 128;
-    v16f acc[4][4];
+    v4f acc[8][8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = v16f{};
+      for (int j = 0; j < 8; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     if constexpr (MODE == kLora) tile_adapters<BM>(p, sm, t, ids);
     contract<MODE, F16>(lds, t, w, lane, acc);
     // every copy has landed and no wave still reads a buffer before the next
     // tile's first copies
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     if constexpr (MODE == kLora) {
-      add_low_rank<F16, 4, 4>(p, t, ids, wrow, wcol, lane, uni(work.part), work.nparts, acc);
+      add_low_rank<F16, 8, 8>(p, t, ids, wrow, wcol, lane, uni(work.part), work.nparts, acc);
       __syncthreads();  // ids are read before the next tile's
     }
     if (work.part >= 0) {
       write_split_record(p.ws, slot, nsplit, t);
-      store_part<4, 4>(reinterpret_cast<float*>(p.ws + kWsHeader + (int64_t)slot * kPartBytes), acc,
+      store_part<8, 8>(reinterpret_cast<float*>(p.ws + kWsHeader + (int64_t)slot * kPartBytes), acc,
                        w, lane, wrow, t.a_rows);
     } else {
-      store_blocks<F16, 4, 4>(acc, out_tile(p, t), p.out_f32, wrow, wcol, lane);
+      store_blocks<F16, 8, 8>(acc, out_tile(p, t), p.out_f32, wrow, wcol, lane);
     }
   }
 }
@@ -224,7 +221,7 @@ hipError_t launch(const Args& p, hipStream_t stream) {
   hipLaunchKernelGGL((large_kernel<MODE, F16>), dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || parts < 2) return e;
-  hipLaunchKernelGGL((split_reduce_kernel<F16, BM, BN, 2, 4, 4>), dim3((unsigned)cus),
+  hipLaunchKernelGGL((split_reduce_kernel<F16, BM, BN, 2, 8, 8>), dim3((unsigned)cus),
                      dim3(kThreads), 0, stream, p.ws, p.out, p.c, p.ldo, p.out_f32);
   return hipGetLastError();
 }

@@ -17,8 +17,8 @@ constexpr int BN = 128;
 
 // Waves of a BM x 128 tile: 2 x 2 (each BM / 2 x 64), or 1 x 4 (each 32 x 32).
 template <int BM> constexpr int kWavesN = BM == 32 ? 4 : 2;
-template <int BM> constexpr int kMI = BM == 128 ? 2 : 1;
-template <int BM> constexpr int kNJ = BM == 32 ? 1 : 2;
+template <int BM> constexpr int kMI = BM == 128 ? 4 : 2;  // 16-row blocks
+template <int BM> constexpr int kNJ = BM == 32 ? 2 : 4;   // 16-column blocks
 template <int BM> constexpr int kStages = BM == 128 ? 2 : 3;  // of (BM + 128) * 128 bytes
 template <int BM> constexpr int64_t kPartBytes = (int64_t)BM * BN * 4;
 constexpr int kWgPerCu = 2;
@@ -30,37 +30,39 @@ struct Ring {
   Side<kColsA<MODE>, BM> a;
   Side<kColsB<MODE>, BN> b;
   uint32_t lds;
-  int w, stages;
+  int stages;
 
+  // Copies stage kt into buffer s.
   __device__ __forceinline__ void copy(int kt, int s) const {
     const bool live = kt < stages;
-    const uint32_t at = lds + s * kStageBytes + w * 1024;
-    const v4i ra = rsrc_words(a.stage_base(kt), a.stage_range(kt, live));
+    const uint32_t at = lds + s * kStageBytes;
+    const v4i ra = a.rsrc(kt, live), rb = b.rsrc(kt, live);
+    const uint64_t ma = a.mask(kt, stages), mb = b.mask(kt, stages);
     static_for<BM / 32>([&](auto i) {
-      dma16(ra, at + decltype(i)::value * 4096, a.piece_off(decltype(i)::value, kt));
+      constexpr int I = decltype(i)::value;
+      a.template copy<I, I * 4096>(ra, at, ma);
     });
-    const v4i rb = rsrc_words(b.stage_base(kt), b.stage_range(kt, live));
     static_for<BN / 32>([&](auto i) {
-      dma16(rb, at + BM * 128 + decltype(i)::value * 4096, b.piece_off(decltype(i)::value, kt));
+      constexpr int I = decltype(i)::value;
+      b.template copy<I, BM * 128 + I * 4096>(rb, at, mb);
     });
   }
 };
 
 template <int MODE, bool F16, int BM>
 __device__ __forceinline__ void contract(uint32_t lds, const Tile& t, int w, int lane,
-                                         v16f (&acc)[kMI<BM>][kNJ<BM>]) {
+                                         v4f (&acc)[kMI<BM>][kNJ<BM>]) {
   constexpr int MI = kMI<BM>, NJ = kNJ<BM>, NS = kStages<BM>;
   Ring<MODE, BM> ring;
   ring.stages = uni((t.kl + kStageK - 1) / kStageK);
   if (ring.stages == 0) return;
-  ring.a.init(t.a, t.lda, t.a_rows, t.kl, w, lane, false);
-  ring.b.init(t.b, t.ldb, t.b_rows, t.kl, w, lane, false);
-  ring.lds = lds;
-  ring.w = w;
+  ring.a.init(t.a, t.lda, t.a_rows, t.kl, w, lane);
+  ring.b.init(t.b, t.ldb, t.b_rows, t.kl, w, lane);
+  ring.lds = uni(lds + w * 1024);
   FragOff<kColsA<MODE>, BM, MI> fa;
   FragOff<kColsB<MODE>, BN, NJ> fb;
-  fa.init((w / kWavesN<BM>) * (32 * MI), lane);
-  fb.init((w % kWavesN<BM>) * (32 * NJ), lane);
+  fa.init(lds, (w / kWavesN<BM>) * (16 * MI), lane);
+  fb.init(lds + BM * 128, (w % kWavesN<BM>) * (16 * NJ), lane);
   static_for<NS - 1>([&](auto s) { ring.copy(decltype(s)::value, decltype(s)::value); });
   int s = 0;
   for (int kt = 0; kt < ring.stages; ++kt) {
@@ -69,15 +71,15 @@ __device__ __forceinline__ void contract(uint32_t lds, const Tile& t, int w, int
     wait_and_barrier<(NS - 2) * Ring<MODE, BM>::kCopies>();
     const int next = s == 0 ? NS - 1 : s - 1;
     ring.copy(kt + NS - 1, next);
-    const uint32_t ta = lds + s * Ring<MODE, BM>::kStageBytes, tb = ta + BM * 128;
-    static_for<4>([&](auto tc) {
+    const uint32_t at = s * Ring<MODE, BM>::kStageBytes;
+    static_for<2>([&](auto tc) {
       constexpr int T = decltype(tc)::value;
       v4i a[MI], b[NJ];
       static_for<MI>([&](auto i) {
-        a[decltype(i)::value] = fa.template read<decltype(i)::value, T>(ta);
+        a[decltype(i)::value] = fa.template read<decltype(i)::value, T>(at);
       });
       static_for<NJ>([&](auto j) {
-        b[decltype(j)::value] = fb.template read<decltype(j)::value, T>(tb);
+        b[decltype(j)::value] = fb.template read<decltype(j)::value, T>(at);
       });
 #pragma unroll
       for (int i = 0; i < MI; ++i)
@@ -112,12 +114,12 @@ __global__ __launch_bounds__(kThreads, kWgPerCu) void small_kernel(Args p) {
     int tid = threadIdx.x;
     asm volatile("" : "+v"(tid));
     const int lane = tid & 63, w = uni(tid >> 6);
-    const int wrow = (w / kWavesN<BM>) * (32 * MI), wcol = (w % kWavesN<BM>) * (32 * NJ);
-    v16f acc[MI][NJ];
+    const int wrow = (w / kWavesN<BM>) * (16 * MI), wcol = (w % kWavesN<BM>) * (16 * NJ);
+    v4f acc[MI][NJ];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = v16f{};
+      for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     if constexpr (MODE == kLora) tile_adapters<BM>(p, sm, t, ids);
     contract<MODE, F16, BM>(lds, t, w, lane, acc);
     // every copy has landed and no wave still reads the ring before the next
