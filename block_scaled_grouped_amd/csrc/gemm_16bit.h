@@ -201,30 +201,28 @@ __device__ __forceinline__ int swz(int k) {
   return low + 2 * ((k >> 3) & 1);
 }
 
-// Global -> LDS copy of 16 bytes a lane (1 KiB at at + IMM): as in lds_dma.h, but m0
-// is written and left (nothing else reads it), and something stands between its
-// writing and the load, which has to be one wait state later: MASKED picks the
-// lane's offset there (past every range for lanes outside of `mask`).
+// A global -> LDS copy of 16 bytes a lane (1 KiB at `at` + IMM) in two steps, so that
+// other instructions can stand between them: the load has to be a wait state later
+// than the writing of m0, which nothing else reads.  MASKED: the lane's offset is
+// past every range for lanes outside of `mask`.
 template <int IMM, bool MASKED>
-__device__ __forceinline__ void copy16(const v4i& rsrc, uint32_t at, int voff, uint64_t mask) {
+__device__ __forceinline__ int copy16_begin(uint32_t at, int voff, uint64_t mask) {
   if constexpr (MASKED) {
     int o;
     asm volatile(
         "s_add_u32 m0, %1, %2\n\t"
-        "v_cndmask_b32 %0, %3, %4, %5\n\t"
-        "buffer_load_dwordx4 %0, %6, 0 offen lds"
-        : "=&v"(o)
-        : "s"(at), "n"(IMM), "v"(kDmaOutOfRange), "v"(voff), "s"(mask), "s"(rsrc)
+        "v_cndmask_b32 %0, %3, %4, %5"
+        : "=v"(o)
+        : "s"(at), "n"(IMM), "v"(kDmaOutOfRange), "v"(voff), "s"(mask)
         : "memory", "scc");
+    return o;
   } else {
-    asm volatile(
-        "s_add_u32 m0, %0, %1\n\t"
-        "s_nop 0\n\t"
-        "buffer_load_dwordx4 %2, %3, 0 offen lds"
-        :
-        : "s"(at), "n"(IMM), "v"(voff), "s"(rsrc)
-        : "memory", "scc");
+    asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0" : : "s"(at), "n"(IMM) : "memory", "scc");
+    return voff;
   }
+}
+__device__ __forceinline__ void copy16_end(const v4i& rsrc, int voff) {
+  asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(rsrc) : "memory");
 }
 
 // One wave's share of the copies of an operand tile of BR rows: pieces w, w + 4,
@@ -287,8 +285,12 @@ struct Side {
   }
 
   template <int I, int IMM>
+  __device__ __forceinline__ int copy_begin(uint32_t at, uint64_t m) const {
+    return copy16_begin<IMM, !COLS>(at, off[I], m);
+  }
+  template <int I, int IMM>
   __device__ __forceinline__ void copy(const v4i& rs, uint32_t at, uint64_t m) const {
-    copy16<IMM, !COLS>(rs, at, off[I], m);
+    copy16_end(rs, copy_begin<I, IMM>(at, m));
   }
 };
 

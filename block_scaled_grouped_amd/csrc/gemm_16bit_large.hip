@@ -23,8 +23,8 @@ constexpr int kBufBytes = 2 * kTileBytes;  // A's tile, then B's
 // Places in a stage's 128 matrix instructions: where its buffer is free for the
 // next copies, where the next stage has to be there, and the copies between.
 constexpr int kFreeSlot = 36;
-constexpr int kReadySlot = 72;
-constexpr int kCopySlot = 38, kCopyStep = 4;
+constexpr int kReadySlot = 96;
+constexpr int kCopySlot = 37, kCopyStep = 6;
 constexpr int kCopies = 16;  // per wave and stage: 8 of A, 8 of B
 constexpr int kCopiesBeforeReady = (kReadySlot - kCopySlot + kCopyStep - 1) / kCopyStep;
 static_assert(kCopySlot + (kCopies - 1) * kCopyStep < 128 && kReadySlot + 32 <= 128 &&
@@ -52,9 +52,13 @@ struct Copies {
     mb = b.mask(kt, stages);
   }
   template <int P>
-  __device__ __forceinline__ void copy() const {
-    if constexpr (P < 8) a.template copy<P, P * 4096>(ra, lds, ma);
-    else b.template copy<P - 8, kTileBytes + (P - 8) * 4096>(rb, lds, mb);
+  __device__ __forceinline__ int copy_begin() const {
+    if constexpr (P < 8) return a.template copy_begin<P, P * 4096>(lds, ma);
+    else return b.template copy_begin<P - 8, kTileBytes + (P - 8) * 4096>(lds, mb);
+  }
+  template <int P>
+  __device__ __forceinline__ void copy_end(int off) const {
+    copy16_end(P < 8 ? ra : rb, off);
   }
 };
 
@@ -110,10 +114,16 @@ __device__ __forceinline__ void contract(uint32_t lds, const Tile& t, int w, int
   fa.init(lds, (w >> 1) * 128, lane);
   fb.init(lds + kTileBytes, (w & 1) * 128, lane);
   c.begin(0);
-  static_for<kCopies>([&](auto q) { c.template copy<decltype(q)::value>(); });
+  static_for<kCopies>([&](auto q) {
+    constexpr int P = decltype(q)::value;
+    c.template copy_end<P>(c.template copy_begin<P>());
+  });
   c.lds += kBufBytes;
   c.begin(1);
-  static_for<kCopies>([&](auto q) { c.template copy<decltype(q)::value>(); });
+  static_for<kCopies>([&](auto q) {
+    constexpr int P = decltype(q)::value;
+    c.template copy_end<P>(c.template copy_begin<P>());
+  });
   c.lds -= kBufBytes;
   wait_and_barrier<kCopies>();
   Half a0, b0, a1, b1;
@@ -121,6 +131,7 @@ __device__ __forceinline__ void contract(uint32_t lds, const Tile& t, int w, int
   int other = kBufBytes;  // bytes to the other buffer
   for (int kt = 0; kt < stages; ++kt) {
     c.begin(kt + 2);
+    int voff = 0;
     fence();
     static_for<128>([&](auto mc) {
       constexpr int m = decltype(mc)::value;
@@ -145,9 +156,11 @@ __device__ __forceinline__ void contract(uint32_t lds, const Tile& t, int w, int
       if constexpr (m >= kReadySlot && m < kReadySlot + 32 && m % 2 == 0)
         read_frag<MODE, 0, (m - kReadySlot) / 2>(fa, fb, a0, b0);
       // the stage after next into this buffer
-      if constexpr (m >= kCopySlot && (m - kCopySlot) % kCopyStep == 0 &&
-                    (m - kCopySlot) / kCopyStep < kCopies)
-        c.template copy<(m - kCopySlot) / kCopyStep>();
+      constexpr int cb = m + 1 - kCopySlot, ce = m - kCopySlot;
+      if constexpr (ce >= 0 && ce % kCopyStep == 0 && ce / kCopyStep < kCopies)
+        c.template copy_end<ce / kCopyStep>(voff);
+      if constexpr (cb >= 0 && cb % kCopyStep == 0 && cb / kCopyStep < kCopies)
+        voff = c.template copy_begin<cb / kCopyStep>();
       fence();
     });
     c.lds += other;
