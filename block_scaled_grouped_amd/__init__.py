@@ -160,12 +160,12 @@ def _check(rc):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr() or None
 
 
 def _stream(t):
     import torch
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _need_cuda(*ts):
@@ -196,7 +196,7 @@ def _req(t, name, nbytes, dtype=None, optional=False):
                 name, " or ".join(_dtype_name(d) for d in allowed), _dtype_name(t.dtype)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    have = t.numel() * t.element_size()
+    have = t.nbytes
     if have < nbytes:
         raise ValueError("%s holds %d bytes; the call touches %d" % (name, have, int(nbytes)))
 
@@ -609,7 +609,7 @@ def grouped_gemm_nvfp4_rowscaled(a, a_scales, a_outer, offsets, k, b, b_scales, 
             G, _ptr(a), _ptr(a_scales), _ptr(a_outer), _ptr(offsets), rows_cap, k, _ptr(b),
             _ptr(b_scales), _ptr(b_outer), ctypes.cast(host_n, ctypes.c_void_p), _ptr(out), ld_out,
             out_dtype, 1 if accumulate else 0, _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _ptr(status), _stream(a)))
+            workspace.nbytes, _ptr(status), _stream(a)))
         return out
     if accumulate:
         _check(lib.grouped_gemm_nvfp4_rowscaled_ex(
@@ -679,7 +679,7 @@ def grouped_gemm_nvfp4_pertensor(a, a_scales, a_amax, offsets, k, b, b_scales, b
         _check(lib.grouped_gemm_nvfp4_pertensor_ws(
             G, _ptr(a), _ptr(a_scales), _ptr(a_amax), _ptr(offsets), rows_cap, k, _ptr(b),
             _ptr(b_scales), _ptr(b_amax), ctypes.cast(host_n, ctypes.c_void_p), _ptr(out), ld_out,
-            out_dtype, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
+            out_dtype, _ptr(workspace), workspace.nbytes, _ptr(status),
             _stream(a)))
         return out
     _check(lib.grouped_gemm_nvfp4_pertensor(G, _ptr(a), _ptr(a_scales), _ptr(a_amax),
@@ -755,26 +755,30 @@ def _strided(t, name, dims, dtype):
         raise ValueError("%s must be a device tensor" % name)
     if t.dtype != dtype:
         raise ValueError("%s must be %s, not %s" % (name, _dtype_name(dtype), _dtype_name(t.dtype)))
-    shape, st = t.shape, t.stride()
-    cols, rows = shape[-1], shape[-2]
-    if st[-1] != 1 and cols > 1:
+    st = t.stride()
+    if dims == 2:
+        (rows, cols), (ld, one) = t.shape, st
+    else:
+        (groups, rows, cols), (stride, ld, one) = t.shape, st
+    if one != 1 and cols > 1:
         raise ValueError("the rows of %s must be contiguous" % name)
-    ld = st[-2] if rows > 1 else max(cols, 1)
+    if rows <= 1:
+        ld = max(cols, 1)
     if dims == 2:
         return ld, 0
-    return ld, (st[0] if shape[0] > 1 else rows * ld)
+    return ld, (stride if groups > 1 else rows * ld)
 
 
 def _same_device(ref, **others):
+    index = ref.get_device()
     for name, t in others.items():
-        if t is not None and t.device != ref.device:
+        if t is not None and t.get_device() != index:
             raise ValueError("%s is on %s, not on %s" % (name, t.device, ref.device))
 
 
 def _out_or_new(out, shape, dtype, ref, name="out"):
-    import torch
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=ref.device)
+        return ref.new_empty(shape, dtype=dtype)
     if tuple(out.shape) != tuple(shape):
         raise ValueError("%s is %s; the call writes %s" % (name, tuple(out.shape), tuple(shape)))
     return out
@@ -825,7 +829,7 @@ def grouped_gemm_16bit(mode, a, b, offsets, c=None, out=None, out_dtype=None, wo
     wbytes = 0
     if workspace is not None:
         _req(workspace, "workspace", 0)
-        wbytes = workspace.numel() * workspace.element_size()
+        wbytes = workspace.nbytes
     if n == 0 or k == 0:
         raise ValueError("n and k must be positive")
     if out.numel() == 0:
@@ -886,7 +890,7 @@ def grouped_lora_gemm_16bit(x, w, lora_a, lora_b, offsets, adapter, scale, out=N
     _check(lib.grouped_lora_gemm_16bit(code, G, _ptr(x), ldx, _ptr(w), ldw, _ptr(lora_a),
                                        _ptr(lora_b), count, rank, _ptr(offsets), _ptr(adapter),
                                        _ptr(scale), rows, n, k, _ptr(out), ldo, od, _ptr(workspace),
-                                       workspace.numel() * workspace.element_size(), _ptr(status),
+                                       workspace.nbytes, _ptr(status),
                                        _stream(x)))
     return out
 

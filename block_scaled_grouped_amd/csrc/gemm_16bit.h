@@ -370,75 +370,106 @@ __device__ __forceinline__ int request_of(const int64_t* off, int G, int64_t row
 }
 
 // Adds each row's own low-rank product to a wave's accumulators: for every
-// adapter that occurs in a 16-row block one product of the block's low rows (both
-// halves) with the adapter's rows of `up`, kept for its own rows only.  So what
-// an adapter holds (infinities, NaN) never reaches a row of another request, and
-// the cost follows the adapters that meet in 16 rows, not the requests.  The
-// operands come straight from the L2: 2 r / 32 matrix instructions a block and
-// adapter are few against the projection's k / 32.
-// ids: adapter of each of the tile's rows (-1: none).  A split tile's parts
-// share the adapters out: the c-th of a block goes to part c % nparts.
+// adapter that occurs in the wave's rows one product of the rows' low values (both
+// halves) with the adapter's rows of `up`, kept for its own rows only.  So what an
+// adapter holds (infinities, NaN) never reaches a row of another request, and the
+// cost follows the adapters that meet in the wave's rows, not the requests.  The
+// operands come straight from the L2, 64 rank columns at a time: `up` is loaded
+// once an adapter, and the low values of up to four 16-row blocks together, so
+// that a load's latency is paid per adapter and not per block.
+// ids: adapter of each of the tile's rows (-1: none).  A split tile's parts share
+// the adapters out: the c-th of a wave goes to part c % nparts.
 template <bool F16, int MI, int NJ>
 __device__ __forceinline__ void add_low_rank(const Args& p, const Tile& t, const int* ids, int wrow,
                                              int wcol, int lane, int part, int nparts,
                                              v4f (&acc)[MI][NJ]) {
+  constexpr int kRows = 16 * MI, kI = MI < 4 ? MI : 4, kJ = NJ < 4 ? NJ : 4;
   const int r = lane & 15, q = lane >> 4, rank = p.r;
-  const uint16_t* up = p.up + t.col0 * rank + 8 * q;
-  static_for<MI>([&](auto ic) {
-    constexpr int i = decltype(ic)::value;
-    const int row = wrow + 16 * i + r;
-    const int id = ids[row];
-    const int lrow = row < t.a_rows ? row : t.a_rows - 1;
-    const uint16_t* low = p.low + (t.row0 + lrow) * 2 * rank + 8 * q;
-    uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xffffu;
-    int turn = 0;
-    while (todo != 0) {
-      const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
-      todo &= ~(uint32_t)__ballot(id == a);
-      if (nparts > 1) {
-        const bool mine = turn == part;
-        turn = turn + 1 == nparts ? 0 : turn + 1;
-        if (!mine) continue;
-      }
-      const uint16_t* ua = up + (int64_t)a * p.n * rank;
-      // a few blocks at a time: the large form's accumulators leave no room for more
-      constexpr int kGroup = NJ < 4 ? NJ : 4;
-      static_for<NJ / kGroup>([&](auto jc) {
-        constexpr int j0 = decltype(jc)::value * kGroup;
-        v4f one[kGroup];
-        const uint16_t* urow[kGroup];
+  const v4i zero = v4i{0, 0, 0, 0};
+  // rows lane and 64 + lane of the wave's
+  const int id0 = lane < kRows ? ids[wrow + lane] : -1;
+  const int id1 = 64 + lane < kRows ? ids[wrow + 64 + lane] : -1;
+  uint64_t todo0 = __ballot(id0 >= 0), todo1 = __ballot(id1 >= 0);
+  const uint16_t* low = p.low + (t.row0 + wrow) * 2 * rank + 8 * q;
+  const int last_row = t.a_rows - 1 - wrow;
+  int turn = 0;
+  while ((todo0 | todo1) != 0) {
+    const int a = todo0 != 0 ? __builtin_amdgcn_readlane(id0, __builtin_ctzll(todo0))
+                             : __builtin_amdgcn_readlane(id1, __builtin_ctzll(todo1));
+    const uint64_t own0 = __ballot(id0 == a), own1 = __ballot(id1 == a);
+    todo0 &= ~own0;
+    todo1 &= ~own1;
+    if (nparts > 1) {
+      const bool mine = turn == part;
+      turn = turn + 1 == nparts ? 0 : turn + 1;
+      if (!mine) continue;
+    }
+    const uint16_t* ua = p.up + ((int64_t)a * p.n + t.col0) * rank + 8 * q;
+    for (int k = 0; k < rank; k += 64) {
+      const bool in0 = k + 8 * q < rank, in1 = k + 32 + 8 * q < rank;  // the rank may end within
+      static_for<NJ / kJ>([&](auto hc) {
+        constexpr int jh = decltype(hc)::value * kJ;
+        fence();
+        v4i u[2][kJ];
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
-          one[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-          int col = wcol + 16 * (j0 + j) + r;
+        for (int j = 0; j < kJ; ++j) {
+          int col = wcol + 16 * (jh + j) + r;
           if (col >= t.b_rows) col = t.b_rows - 1;  // such columns are not stored
-          urow[j] = ua + (int64_t)col * rank;
+          const uint16_t* src = ua + (int64_t)col * rank + k;
+          u[0][j] = in0 ? *reinterpret_cast<const v4i*>(src) : zero;
+          u[1][j] = in1 ? *reinterpret_cast<const v4i*>(src + 32) : zero;
         }
-        for (int k = 0; k < rank; k += 32) {
-          v4i l0 = v4i{0, 0, 0, 0}, l1 = l0, u[kGroup];
+        static_for<MI / kI>([&](auto gc) {
+          constexpr int i0 = decltype(gc)::value * kI;
+          const uint64_t own = i0 < 4 ? own0 : own1;
+          if (own == 0) return;
+          v4i l[kI][2][2];  // [block][half][32 rank columns]
 #pragma unroll
-          for (int j = 0; j < kGroup; ++j) u[j] = l0;
-          if (k + 8 * q < rank) {  // the rank may end within the step
-            l0 = *reinterpret_cast<const v4i*>(low + k);
-            l1 = *reinterpret_cast<const v4i*>(low + rank + k);
+          for (int i = 0; i < kI; ++i) {
+            int row = 16 * (i0 + i) + r;
+            if (row > last_row) row = last_row;
+            const uint16_t* src = low + (int64_t)row * 2 * rank + k;
 #pragma unroll
-            for (int j = 0; j < kGroup; ++j) u[j] = *reinterpret_cast<const v4i*>(urow[j] + k);
+            for (int half = 0; half < 2; ++half) {
+              l[i][half][0] = in0 ? *reinterpret_cast<const v4i*>(src + half * rank) : zero;
+              l[i][half][1] = in1 ? *reinterpret_cast<const v4i*>(src + half * rank + 32) : zero;
+            }
           }
+          static_for<kI>([&](auto ic) {
+            constexpr int i = decltype(ic)::value;
+            const uint32_t rows = (uint32_t)(own >> (16 * i)) & 0xffffu;
+            if (rows == 0) return;
+            const bool mine = (rows >> r & 1) != 0;
+            static_for<kJ / 2>([&](auto jc) {
+              constexpr int j0 = decltype(jc)::value * 2, ja = jh + j0;
+              fence();
+              v4f one[2];
 #pragma unroll
-          for (int j = 0; j < kGroup; ++j) one[j] = mfma16<F16>(u[j], l0, one[j]);
+              for (int j = 0; j < 2; ++j) one[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int j = 0; j < kGroup; ++j) one[j] = mfma16<F16>(u[j], l1, one[j]);
-        }
-        fence();
+              for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j)
+                for (int half = 0; half < 2; ++half)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[i][j0 + j][e] = id == a ? acc[i][j0 + j][e] + one[j][e] : acc[i][j0 + j][e];
-        fence();
+                  for (int j = 0; j < 2; ++j)
+                    one[j] = mfma16<F16>(u[c][j0 + j], l[i][half][c], one[j]);
+              // opaque copies: the accumulators stay where they are between the adapters
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                v4f y = acc[i0 + i][ja + j];
+                asm volatile("" : "+v"(y));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = mine ? y[e] + one[j][e] : y[e];
+                acc[i0 + i][ja + j] = y;
+                if constexpr (MI * NJ == 64) asm volatile("" : "+a"(acc[i0 + i][ja + j]));
+              }
+              fence();
+            });
+          });
+        });
       });
     }
-  });
+  }
 }
 
 // Fills ids[0..BM) for a tile; the caller places a barrier after it.

@@ -27,34 +27,24 @@ __device__ __forceinline__ void split16(float s, uint32_t& top, uint32_t& rest) 
   rest = pack16<F16>(left, left) & 0xffffu;
 }
 
-template <bool F16>
-__device__ __forceinline__ v16f mfma32(const v4i& x, const v4i& y, const v16f& acc) {
-  if constexpr (F16)
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, x),
-                                                  __builtin_bit_cast(v8h, y), acc, 0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, x),
-                                                   __builtin_bit_cast(v8bf, y), acc, 0, 0, 0);
-}
-
 // low[t, 0..r) + low[t, r..2r) = scale_a X[t, :] A_a^T.
 //
 // A workgroup of eight waves takes 32 consecutive rows, 64 rank columns and one
 // of the adapters that occur in those rows; the waves take turns at the
-// contraction's runs of 64 and their sums are added through LDS in one order.
-// Rows of another adapter are computed too and not written: a matrix instruction
-// takes 32 rows anyway.  Operands come straight from memory, a lane 64 bytes of
-// its row's 128-byte line a run (the k16 steps contract the line's chunks in the
-// order (c, 4 + c), the same for both operands).
+// contraction's runs of 64 (a 128-byte line of a row) and their sums are added
+// through LDS in one order.  Rows of another adapter are computed too and not
+// written.  Operands come straight from memory: X is read once an adapter and 64
+// rank columns, and nothing is shared between waves that LDS could serve.
 constexpr int kLowThreads = 512;
 constexpr int kLowWaves = kLowThreads / 64;
+constexpr int kLowRows = 32;
 
-template <bool F16>
+template <bool F16, int NB>  // 16 NB <= 64 rank columns a workgroup
 __global__ __launch_bounds__(kLowThreads) void lora_low_kernel(Args p, const uint16_t* down,
                                                                const float* scale, uint16_t* low,
                                                                int turns) {
   __shared__ int64_t off[kMaxGroups + 1];
-  __shared__ __attribute__((aligned(16))) float sums[kLowWaves][2][4][64][4];
+  __shared__ __attribute__((aligned(16))) v4f sums[kLowWaves][2][NB][64];
   load_offsets_clamped(p.offsets, p.G, p.rows_cap, off, nullptr);
   __syncthreads();
   if (blockIdx.x == 0)
@@ -62,79 +52,121 @@ __global__ __launch_bounds__(kLowThreads) void lora_low_kernel(Args p, const uin
       if (p.adapter[g] >= p.num_adapters) dev_status_or(p.status, kDevBadAdapter);
   const int64_t first = uni64(off[0]), last = uni64(off[p.G]);
   const int lane = threadIdx.x & 63, w = uni((int)(threadIdx.x >> 6));
-  const int r = lane & 31, h = lane >> 5, rank = p.r, k = (int)p.k;
-  const int rank_blocks = (rank + 63) / 64;
-  const int64_t items = (last - first + 31) / 32 * rank_blocks * turns;
+  const int r = lane & 15, q = lane >> 4, rank = p.r, k = (int)p.k;
+  const int rank_blocks = (rank + 16 * NB - 1) / (16 * NB);
+  const int64_t items = (last - first + kLowRows - 1) / kLowRows * rank_blocks * turns;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int turn0 = uni((int)(it % turns));
-    const int j0 = uni((int)(it / turns % rank_blocks)) * 64;
-    const int64_t row = first + it / turns / rank_blocks * 32 + r;
-    const int id = row < last ? adapter_of(p, request_of(off, p.G, row)) : -1;
-    const uint16_t* x = p.a + (row < last ? row : last - 1) * p.lda + 32 * h;
-    const bool two = rank - j0 > 32;
+    const int j0 = uni((int)(it / turns % rank_blocks)) * (16 * NB);
+    const int64_t row0 = first + it / turns / rank_blocks * kLowRows;
+    // lane l: adapter of row l % 32
+    const int64_t mine_row = row0 + (lane & 31);
+    const int id = mine_row < last ? adapter_of(p, request_of(off, p.G, mine_row)) : -1;
+    const uint16_t* x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t row = row0 + 16 * i + r;
+      x[i] = p.a + (row < last ? row : last - 1) * p.lda + 8 * q;
+    }
     uint32_t todo = (uint32_t)__ballot(id >= 0);
     int turn = 0;
     while (todo != 0) {
       const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
-      todo &= ~(uint32_t)__ballot(id == a);
+      const uint32_t own = (uint32_t)__ballot(id == a);
+      todo &= ~own;
       const bool mine = turn == turn0;
       turn = turn + 1 == turns ? 0 : turn + 1;
       if (!mine) continue;
-      const uint16_t* d[2];
+      const uint16_t* d[NB];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        int j = j0 + 32 * b + r;
+      for (int b = 0; b < NB; ++b) {
+        int j = j0 + 16 * b + r;
         if (j >= rank) j = rank - 1;  // such columns are not written
-        d[b] = down + ((int64_t)a * rank + j) * p.k + 32 * h;
+        d[b] = down + ((int64_t)a * rank + j) * p.k + 8 * q;
       }
-      v16f acc[2] = {v16f{}, v16f{}};
-#pragma unroll 2
-      for (int k0 = 64 * w; k0 < k; k0 += 64 * kLowWaves) {
-        v4i fx[4], f0[4], f1[4];
+      v4f acc[2][NB];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const bool in = k0 + 32 * h + 8 * c < k;
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[i][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      // kRuns of the wave's runs are loaded before the first is used
+      constexpr int kRuns = NB == 4 ? 2 : 4;
+      for (int k0 = 64 * w; k0 < k; k0 += 64 * kLowWaves * kRuns) {
+        v4i fx[2 * kRuns][2], fd[2 * kRuns][NB];
+#pragma unroll
+        for (int c = 0; c < 2 * kRuns; ++c) {
+          const int at = k0 + (c >> 1) * 64 * kLowWaves + 32 * (c & 1);
+          const bool in = at + 8 * q < k;
           const v4i zero = v4i{0, 0, 0, 0};
-          fx[c] = in ? *reinterpret_cast<const v4i*>(x + k0 + 8 * c) : zero;
-          f0[c] = in ? *reinterpret_cast<const v4i*>(d[0] + k0 + 8 * c) : zero;
-          f1[c] = in && two ? *reinterpret_cast<const v4i*>(d[1] + k0 + 8 * c) : zero;
-        }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          acc[0] = mfma32<F16>(f0[c], fx[c], acc[0]);
-          if (two) acc[1] = mfma32<F16>(f1[c], fx[c], acc[1]);
+          for (int i = 0; i < 2; ++i)
+            fx[c][i] = in ? *reinterpret_cast<const v4i*>(x[i] + at) : zero;
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            fd[c][b] = in ? *reinterpret_cast<const v4i*>(d[b] + at) : zero;
         }
+        fence();
+#pragma unroll
+        for (int c = 0; c < 2 * kRuns; ++c)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) acc[i][b] = mfma16<F16>(fd[c][b], fx[c][i], acc[i][b]);
       }
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<v4f*>(sums[w][b][q][lane]) =
-              v4f{acc[b][4 * q], acc[b][4 * q + 1], acc[b][4 * q + 2], acc[b][4 * q + 3]};
+        for (int b = 0; b < NB; ++b) sums[w][i][b][lane] = acc[i][b];
       __syncthreads();
-      // wave w adds quarter w % 4 of column block w / 4
-      v4f s = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      // wave w adds block (w / NB, w % NB)
+      if (w < 2 * NB) {
+        const int i = w / NB, b = w % NB;
+        v4f s = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int v = 0; v < kLowWaves; ++v) {
-        const v4f t = *reinterpret_cast<const v4f*>(sums[v][w >> 2][w & 3][lane]);
+        for (int v = 0; v < kLowWaves; ++v) {
+          const v4f t = sums[v][i][b][lane];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] += t[e];
-      }
-      const int j = j0 + 32 * (w >> 2) + 8 * (w & 3) + 4 * h;
-      if (id == a && j < rank) {
-        const float f = scale[a];
-        uint32_t top[4], rest[4];
+          for (int e = 0; e < 4; ++e) s[e] += t[e];
+        }
+        const int j = j0 + 16 * b + 4 * q;
+        if ((own >> (16 * i + r) & 1) != 0 && j < rank) {
+          const float f = scale[a];
+          uint32_t top[4], rest[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split16<F16>(s[e] * f, top[e], rest[e]);
-        uint16_t* dst = low + row * 2 * rank + j;
-        *reinterpret_cast<v2i*>(dst) =
-            v2i{(int)(top[0] | top[1] << 16), (int)(top[2] | top[3] << 16)};
-        *reinterpret_cast<v2i*>(dst + rank) =
-            v2i{(int)(rest[0] | rest[1] << 16), (int)(rest[2] | rest[3] << 16)};
+          for (int e = 0; e < 4; ++e) split16<F16>(s[e] * f, top[e], rest[e]);
+          uint16_t* dst = low + (row0 + 16 * i + r) * 2 * rank + j;
+          *reinterpret_cast<v2i*>(dst) =
+              v2i{(int)(top[0] | top[1] << 16), (int)(top[2] | top[3] << 16)};
+          *reinterpret_cast<v2i*>(dst + rank) =
+              v2i{(int)(rest[0] | rest[1] << 16), (int)(rest[2] | rest[3] << 16)};
+        }
       }
       __syncthreads();
     }
   }
+}
+
+template <bool F16>
+hipError_t launch_low(const Args& p, const uint16_t* down, const float* scale, uint16_t* low,
+                      hipStream_t stream) {
+  const int nb = p.r <= 16 ? 1 : p.r <= 32 ? 2 : 4;
+  // as many workgroups share a block's adapters as fill the compute units
+  const int64_t blocks = (p.rows_cap + kLowRows - 1) / kLowRows * ((p.r + 16 * nb - 1) / (16 * nb));
+  const int64_t cap = 2 * (int64_t)device_cu_count();
+  int64_t turns = cap / blocks;
+  turns = turns < 1 ? 1 : turns > kLowRows ? kLowRows : turns;
+  const int64_t most = p.rows_cap < p.G ? p.rows_cap : p.G;  // adapters that can meet in a block
+  if (turns > most) turns = most;
+  const int64_t grid = blocks * turns < cap ? blocks * turns : cap;
+  const dim3 gd((unsigned)grid), bd(kLowThreads);
+  const int tn = (int)turns;
+  if (nb == 1)
+    hipLaunchKernelGGL((lora_low_kernel<F16, 1>), gd, bd, 0, stream, p, down, scale, low, tn);
+  else if (nb == 2)
+    hipLaunchKernelGGL((lora_low_kernel<F16, 2>), gd, bd, 0, stream, p, down, scale, low, tn);
+  else
+    hipLaunchKernelGGL((lora_low_kernel<F16, 4>), gd, bd, 0, stream, p, down, scale, low, tn);
+  return hipGetLastError();
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -209,20 +241,8 @@ hipError_t launch_lora_gemm_16bit(int f16, int G, const void* x, int64_t ldx, co
   p.num_adapters = (int)num_adapters;
   p.r = (int)r;
   const uint16_t* d = static_cast<const uint16_t*>(down);
-  // as many workgroups share a block's adapters as fill the compute units
-  const int64_t blocks = (rows_cap + 31) / 32 * ((r + 63) / 64);
-  const int64_t cap = 2 * (int64_t)device_cu_count();
-  int64_t turns = cap / blocks;
-  turns = turns < 1 ? 1 : turns > 32 ? 32 : turns;
-  const int64_t most = rows_cap < G ? rows_cap : G;  // adapters that can meet in a block
-  if (turns > most) turns = most;
-  const int64_t grid = blocks * turns < cap ? blocks * turns : cap;
-  const dim3 gd((unsigned)grid), bd(kLowThreads);
-  if (f16)
-    hipLaunchKernelGGL(lora_low_kernel<true>, gd, bd, 0, stream, p, d, scale, low, (int)turns);
-  else
-    hipLaunchKernelGGL(lora_low_kernel<false>, gd, bd, 0, stream, p, d, scale, low, (int)turns);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e =
+      f16 ? launch_low<true>(p, d, scale, low, stream) : launch_low<false>(p, d, scale, low, stream);
   if (e != hipSuccess) return e;
   return launch_form(kLora, f16, p, stream);
 }
