@@ -52,6 +52,7 @@ typedef __attribute__((address_space(3))) v4s lds_v4s;
 constexpr int kStageK = 64;       // contraction indexes per LDS stage
 constexpr int kThreads = 256;
 constexpr int kSuperM = 4, kSuperN = 8;  // tile block one XCD works on
+constexpr int kLowParts = 4;             // of the adapters' first product, where it is split
 
 enum Mode { kFprop = 0, kWgrad = 1, kDgrad = 2, kLora = 3 };
 template <int MODE> constexpr bool kColsA = MODE == kWgrad;
@@ -78,7 +79,11 @@ struct Args {
   char* ws;  // split workspace or null: no split
   int G, out_f32;
   // LORA
-  const uint16_t* low;     // [rows_cap, 2 r]: high and low halves of the scaled X A^T
+  const void* low;         // X A^T of each row's own adapter: [rows_cap, 2 r], high and low
+                           // halves of it scaled, or (low_parts: kLowParts, not 1)
+                           // float32 [kLowParts, rows_cap, r], parts of its contraction
+  const float* scale;      // [adapters]
+  int low_parts;
   const uint16_t* up;      // [adapters, n, r]
   const int32_t* adapter;  // [G], negative: none
   int num_adapters, r;
@@ -86,7 +91,7 @@ struct Args {
 
 struct Sched {
   int64_t off[kMaxGroups + 1];
-  int32_t cnt[kMaxGroups];
+  int32_t cnt[kMaxGroups];  // tiles of each group; LORA: adapter of each request, or -1
   int32_t pre[kMaxGroups + 1];
 };
 
@@ -129,10 +134,19 @@ __device__ __forceinline__ void wait_and_barrier() {
 
 // ---------------------------------------------------------------- tiles
 
+// Adapter of request g, or -1.
+__device__ __forceinline__ int adapter_of(const Args& p, int g) {
+  const int a = p.adapter[g];
+  return a < p.num_adapters ? a : -1;
+}
+
 // Loads the offsets and counts tiles; returns their number.  Every thread calls it.
 template <int MODE, int BM, int BN>
 __device__ __forceinline__ int count_tiles(const Args& p, Sched& sm) {
   const int tid = threadIdx.x;
+  if constexpr (MODE == kLora) {
+    for (int g = tid; g < p.G; g += kThreads) sm.cnt[g] = adapter_of(p, g);
+  }
   load_offsets_clamped(p.offsets, p.G, p.rows_cap, sm.off, blockIdx.x == 0 ? p.status : nullptr);
   const int64_t ntn = (p.n + BN - 1) / BN;
   if constexpr (MODE == kLora) {
@@ -353,12 +367,6 @@ __device__ __forceinline__ v4f mfma16(const v4i& x, const v4i& y, const v4f& acc
 
 // ---------------------------------------------------------------- adapters
 
-// Adapter of request g, or -1.
-__device__ __forceinline__ int adapter_of(const Args& p, int g) {
-  const int a = p.adapter[g];
-  return a < p.num_adapters ? a : -1;
-}
-
 // Request of a row in [off[0], off[G]).
 __device__ __forceinline__ int request_of(const int64_t* off, int G, int64_t row) {
   int lo = 0, hi = G - 1;
@@ -369,77 +377,139 @@ __device__ __forceinline__ int request_of(const int64_t* off, int G, int64_t row
   return lo;
 }
 
+template <bool F16>
+__device__ __forceinline__ float to_f32(uint32_t b) {
+  return F16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)b) : bf16_to_f32(b & 0xffffu);
+}
+
+// s as the sum of two 16-bit values: the nearest one and the nearest to what is
+// left (22 or 16 bits of s together).  The first is kept finite, so that a value
+// past the type's range turns into an infinity in the second and not into the
+// difference of two.
+template <bool F16>
+__device__ __forceinline__ void split16(float s, uint32_t& top, uint32_t& rest) {
+  constexpr float kMax = F16 ? 65504.0f : 3.3895313892515355e38f;
+  float c = s;
+  if (s > kMax) c = kMax;
+  if (s < -kMax) c = -kMax;
+  top = pack16<F16>(c, c) & 0xffffu;
+  const float left = s - to_f32<F16>(top);
+  rest = pack16<F16>(left, left) & 0xffffu;
+}
+
+// A lane's fragments (high and low halves) of a 16-row block's low values: `row` of
+// the wave's rows, rank columns at byte `at` / 2 and on (an offset past every range:
+// zeros).  rows: live rows from the wave's first on.
+template <bool F16>
+__device__ __forceinline__ void load_low(const Args& p, int64_t first, int rows, int row,
+                                         uint32_t at, float scale, v4i& top, v4i& rest) {
+  const int rank = p.r;
+  if (p.low_parts == 1) {
+    const __amdgpu_buffer_rsrc_t low = make_rsrc(
+        static_cast<const uint16_t*>(p.low) + first * 2 * rank, rows > 0 ? rows * 4 * rank : 0);
+    top = __builtin_amdgcn_raw_buffer_load_b128(low, (int)(at + row * 4 * rank), 0, 0);
+    rest = __builtin_amdgcn_raw_buffer_load_b128(low, (int)(at + row * 4 * rank + 2 * rank), 0, 0);
+    return;
+  }
+  const uint32_t o = at == (uint32_t)kDmaOutOfRange ? at : 2 * at + row * 4 * rank;
+  v4i v[kLowParts][2];
+#pragma unroll
+  for (int part = 0; part < kLowParts; ++part) {
+    const __amdgpu_buffer_rsrc_t low =
+        make_rsrc(static_cast<const float*>(p.low) + (part * p.rows_cap + first) * rank,
+                  rows > 0 ? rows * 4 * rank : 0);
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      v[part][b] = __builtin_amdgcn_raw_buffer_load_b128(low, (int)(o + 16 * b), 0, 0);
+  }
+  float s[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    s[e] = __int_as_float(v[0][e >> 2][e & 3]);
+#pragma unroll
+    for (int part = 1; part < kLowParts; ++part) s[e] += __int_as_float(v[part][e >> 2][e & 3]);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    uint32_t t0, r0, t1, r1;
+    split16<F16>(s[2 * e] * scale, t0, r0);
+    split16<F16>(s[2 * e + 1] * scale, t1, r1);
+    top[e] = (int)(t0 | t1 << 16);
+    rest[e] = (int)(r0 | r1 << 16);
+  }
+}
+
 // Adds each row's own low-rank product to a wave's accumulators: for every
-// adapter that occurs in the wave's rows one product of the rows' low values (both
-// halves) with the adapter's rows of `up`, kept for its own rows only.  So what an
-// adapter holds (infinities, NaN) never reaches a row of another request, and the
+// adapter that occurs in (64 of) the wave's rows one product of the rows' low values
+// (both halves) with the adapter's rows of `up`, kept for its own rows only.  So what
+// an adapter holds (infinities, NaN) never reaches a row of another request, and the
 // cost follows the adapters that meet in the wave's rows, not the requests.  The
-// operands come straight from the L2, 64 rank columns at a time: `up` is loaded
-// once an adapter, and the low values of up to four 16-row blocks together, so
-// that a load's latency is paid per adapter and not per block.
+// operands come straight from the L2, 64 rank columns at a time, the low values
+// once and `up` once an adapter, so that a load's latency is paid per adapter and
+// not per block.
 // ids: adapter of each of the tile's rows (-1: none).  A split tile's parts share
-// the adapters out: the c-th of a wave goes to part c % nparts.
+// the adapters out: the c-th of the rows goes to part c % nparts.
 template <bool F16, int MI, int NJ>
 __device__ __forceinline__ void add_low_rank(const Args& p, const Tile& t, const int* ids, int wrow,
                                              int wcol, int lane, int part, int nparts,
                                              v4f (&acc)[MI][NJ]) {
-  constexpr int kRows = 16 * MI, kI = MI < 4 ? MI : 4, kJ = NJ < 4 ? NJ : 4;
+  constexpr int kI = MI < 4 ? MI : 4, kJ = NJ < 4 ? NJ : 4;
   const int r = lane & 15, q = lane >> 4, rank = p.r;
-  const v4i zero = v4i{0, 0, 0, 0};
-  // rows lane and 64 + lane of the wave's
-  const int id0 = lane < kRows ? ids[wrow + lane] : -1;
-  const int id1 = 64 + lane < kRows ? ids[wrow + 64 + lane] : -1;
-  uint64_t todo0 = __ballot(id0 >= 0), todo1 = __ballot(id1 >= 0);
-  const uint16_t* low = p.low + (t.row0 + wrow) * 2 * rank + 8 * q;
-  const int last_row = t.a_rows - 1 - wrow;
-  int turn = 0;
-  while ((todo0 | todo1) != 0) {
-    const int a = todo0 != 0 ? __builtin_amdgcn_readlane(id0, __builtin_ctzll(todo0))
-                             : __builtin_amdgcn_readlane(id1, __builtin_ctzll(todo1));
-    const uint64_t own0 = __ballot(id0 == a), own1 = __ballot(id1 == a);
-    todo0 &= ~own0;
-    todo1 &= ~own1;
-    if (nparts > 1) {
-      const bool mine = turn == part;
-      turn = turn + 1 == nparts ? 0 : turn + 1;
-      if (!mine) continue;
+  // rows and columns past the tile's, and rank columns past the last, read as zeros
+  const int cols = t.b_rows - wcol;
+  for (int k = 0; k < rank; k += 64) {
+    uint32_t at[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int col = k + 32 * c + 8 * q;
+      at[c] = col < rank ? 2 * col : kDmaOutOfRange;
     }
-    const uint16_t* ua = p.up + ((int64_t)a * p.n + t.col0) * rank + 8 * q;
-    for (int k = 0; k < rank; k += 64) {
-      const bool in0 = k + 8 * q < rank, in1 = k + 32 + 8 * q < rank;  // the rank may end within
-      static_for<NJ / kJ>([&](auto hc) {
-        constexpr int jh = decltype(hc)::value * kJ;
-        fence();
-        v4i u[2][kJ];
+    static_for<MI / kI>([&](auto gc) {
+      constexpr int i0 = decltype(gc)::value * kI;
+      const int row0 = wrow + 16 * i0;
+      const int id = lane < 16 * kI ? ids[row0 + lane] : -1;  // of row lane
+      uint64_t todo = __ballot(id >= 0);
+      if (todo == 0) return;
+      v4i l[kI][2][2];  // [block][32 rank columns][half]
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          int col = wcol + 16 * (jh + j) + r;
-          if (col >= t.b_rows) col = t.b_rows - 1;  // such columns are not stored
-          const uint16_t* src = ua + (int64_t)col * rank + k;
-          u[0][j] = in0 ? *reinterpret_cast<const v4i*>(src) : zero;
-          u[1][j] = in1 ? *reinterpret_cast<const v4i*>(src + 32) : zero;
+      for (int i = 0; i < kI; ++i) {
+        float scale = 1.0f;
+        if (p.low_parts > 1) {
+          const int mine = ids[row0 + 16 * i + r];
+          scale = mine >= 0 ? p.scale[mine] : 0.0f;
         }
-        static_for<MI / kI>([&](auto gc) {
-          constexpr int i0 = decltype(gc)::value * kI;
-          const uint64_t own = i0 < 4 ? own0 : own1;
-          if (own == 0) return;
-          v4i l[kI][2][2];  // [block][half][32 rank columns]
 #pragma unroll
-          for (int i = 0; i < kI; ++i) {
-            int row = 16 * (i0 + i) + r;
-            if (row > last_row) row = last_row;
-            const uint16_t* src = low + (int64_t)row * 2 * rank + k;
+        for (int c = 0; c < 2; ++c)
+          load_low<F16>(p, t.row0 + row0, t.a_rows - row0, 16 * i + r, at[c], scale, l[i][c][0],
+                        l[i][c][1]);
+      }
+      int turn = 0;
+      while (todo != 0) {
+        const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+        const uint64_t own = __ballot(id == a);
+        todo &= ~own;
+        if (nparts > 1) {
+          const bool mine = turn == part;
+          turn = turn + 1 == nparts ? 0 : turn + 1;
+          if (!mine) continue;
+        }
+        const __amdgpu_buffer_rsrc_t up = make_rsrc(
+            p.up + ((int64_t)a * p.n + t.col0 + wcol) * rank, cols > 0 ? cols * 2 * rank : 0);
+        static_for<NJ / kJ>([&](auto hc) {
+          constexpr int jh = decltype(hc)::value * kJ;
+          fence();
+          v4i u[2][kJ];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              l[i][half][0] = in0 ? *reinterpret_cast<const v4i*>(src + half * rank) : zero;
-              l[i][half][1] = in1 ? *reinterpret_cast<const v4i*>(src + half * rank + 32) : zero;
-            }
-          }
+          for (int j = 0; j < kJ; ++j)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              u[c][j] = __builtin_amdgcn_raw_buffer_load_b128(
+                  up, (int)(at[c] + (16 * (jh + j) + r) * 2 * rank), 0, 0);
           static_for<kI>([&](auto ic) {
             constexpr int i = decltype(ic)::value;
-            const uint32_t rows = (uint32_t)(own >> (16 * i)) & 0xffffu;
-            if (rows == 0) return;
-            const bool mine = (rows >> r & 1) != 0;
+            const uint32_t these = (uint32_t)(own >> (16 * i)) & 0xffffu;
+            if (these == 0) return;
+            const bool mine = (these >> r & 1) != 0;
             static_for<kJ / 2>([&](auto jc) {
               constexpr int j0 = decltype(jc)::value * 2, ja = jh + j0;
               fence();
@@ -452,7 +522,7 @@ __device__ __forceinline__ void add_low_rank(const Args& p, const Tile& t, const
                 for (int half = 0; half < 2; ++half)
 #pragma unroll
                   for (int j = 0; j < 2; ++j)
-                    one[j] = mfma16<F16>(u[c][j0 + j], l[i][half][c], one[j]);
+                    one[j] = mfma16<F16>(u[c][j0 + j], l[i][c][half], one[j]);
               // opaque copies: the accumulators stay where they are between the adapters
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
@@ -467,8 +537,8 @@ __device__ __forceinline__ void add_low_rank(const Args& p, const Tile& t, const
             });
           });
         });
-      });
-    }
+      }
+    });
   }
 }
 
@@ -477,7 +547,7 @@ template <int BM>
 __device__ __forceinline__ void tile_adapters(const Args& p, const Sched& sm, const Tile& t,
                                               int* ids) {
   for (int i = threadIdx.x; i < BM; i += kThreads)
-    ids[i] = i < t.a_rows ? adapter_of(p, request_of(sm.off, p.G, t.row0 + i)) : -1;
+    ids[i] = i < t.a_rows ? sm.cnt[request_of(sm.off, p.G, t.row0 + i)] : -1;
 }
 
 // ---------------------------------------------------------------- epilogue

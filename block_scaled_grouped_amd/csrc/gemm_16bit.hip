@@ -7,67 +7,60 @@ using namespace g16;
 
 namespace {
 
-template <bool F16>
-__device__ __forceinline__ float to_f32(uint16_t b) {
-  return F16 ? (float)__builtin_bit_cast(_Float16, b) : bf16_to_f32(b);
-}
-
-// s as the sum of two 16-bit values: the nearest one and the nearest to what is
-// left (22 or 16 bits of s together).  The first is kept finite, so that a value
-// past the type's range turns into an infinity in the second and not into the
-// difference of two.
-template <bool F16>
-__device__ __forceinline__ void split16(float s, uint32_t& top, uint32_t& rest) {
-  constexpr float kMax = F16 ? 65504.0f : 3.3895313892515355e38f;
-  float c = s;
-  if (s > kMax) c = kMax;
-  if (s < -kMax) c = -kMax;
-  top = pack16<F16>(c, c) & 0xffffu;
-  const float left = s - to_f32<F16>((uint16_t)top);
-  rest = pack16<F16>(left, left) & 0xffffu;
-}
-
-// low[t, 0..r) + low[t, r..2r) = scale_a X[t, :] A_a^T.
+// The adapters' first product, X[t, :] A_a^T: scaled and as two halves, or (parts of
+// the contraction) as it is.
 //
-// A workgroup of eight waves takes 32 consecutive rows, 64 rank columns and one
-// of the adapters that occur in those rows; the waves take turns at the
-// contraction's runs of 64 (a 128-byte line of a row) and their sums are added
-// through LDS in one order.  Rows of another adapter are computed too and not
-// written.  Operands come straight from memory: X is read once an adapter and 64
-// rank columns, and nothing is shared between waves that LDS could serve.
+// A workgroup of eight waves takes 32 consecutive rows, 16 NB rank columns, one of
+// the adapters that occur in those rows and one part of the contraction; the waves
+// take turns at the part's runs of 64 (a 128-byte line of a row) and their sums are
+// added through LDS in one order.  Rows of another adapter are computed too and not
+// written.  Operands come straight from memory: nothing is shared between waves
+// that LDS could serve.  A compute unit takes 64 GB/s that way, 28 past its L2, so
+// where the rows are few the contraction is spread over several workgroups, whose
+// parts the second product adds.
 constexpr int kLowThreads = 512;
 constexpr int kLowWaves = kLowThreads / 64;
 constexpr int kLowRows = 32;
 
 template <bool F16, int NB>  // 16 NB <= 64 rank columns a workgroup
 __global__ __launch_bounds__(kLowThreads) void lora_low_kernel(Args p, const uint16_t* down,
-                                                               const float* scale, uint16_t* low,
                                                                int turns) {
   __shared__ int64_t off[kMaxGroups + 1];
+  __shared__ int adapters[kMaxGroups];
   __shared__ __attribute__((aligned(16))) v4f sums[kLowWaves][2][NB][64];
+  for (int g = threadIdx.x; g < p.G; g += kLowThreads) {
+    adapters[g] = adapter_of(p, g);
+    if (blockIdx.x == 0 && p.adapter[g] >= p.num_adapters) dev_status_or(p.status, kDevBadAdapter);
+  }
   load_offsets_clamped(p.offsets, p.G, p.rows_cap, off, nullptr);
   __syncthreads();
-  if (blockIdx.x == 0)
-    for (int g = threadIdx.x; g < p.G; g += kLowThreads)
-      if (p.adapter[g] >= p.num_adapters) dev_status_or(p.status, kDevBadAdapter);
   const int64_t first = uni64(off[0]), last = uni64(off[p.G]);
   const int lane = threadIdx.x & 63, w = uni((int)(threadIdx.x >> 6));
   const int r = lane & 15, q = lane >> 4, rank = p.r, k = (int)p.k;
   const int rank_blocks = (rank + 16 * NB - 1) / (16 * NB);
-  const int64_t items = (last - first + kLowRows - 1) / kLowRows * rank_blocks * turns;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int turn0 = uni((int)(it % turns));
-    const int j0 = uni((int)(it / turns % rank_blocks)) * (16 * NB);
-    const int64_t row0 = first + it / turns / rank_blocks * kLowRows;
+  const int parts = p.low_parts;
+  uint16_t* low16 = const_cast<uint16_t*>(static_cast<const uint16_t*>(p.low));
+  float* low32 = const_cast<float*>(static_cast<const float*>(p.low));
+  const int64_t blocks = (last - first + kLowRows - 1) / kLowRows * rank_blocks;
+  const int64_t items = blocks * turns * parts;
+  const int runs = (k + 63) / 64;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    // the turns come last: most blocks hold one adapter, and their later turns nothing
+    const int part = uni((int)(item % parts));
+    const int64_t it = item / parts % blocks;
+    const int run0 = runs * part / parts, run1 = runs * (part + 1) / parts;
+    const int turn0 = uni((int)(item / parts / blocks));
+    const int j0 = uni((int)(it % rank_blocks)) * (16 * NB);
+    const int64_t row0 = first + it / rank_blocks * kLowRows;
     // lane l: adapter of row l % 32
     const int64_t mine_row = row0 + (lane & 31);
-    const int id = mine_row < last ? adapter_of(p, request_of(off, p.G, mine_row)) : -1;
-    const uint16_t* x[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t row = row0 + 16 * i + r;
-      x[i] = p.a + (row < last ? row : last - 1) * p.lda + 8 * q;
-    }
+    const int id = mine_row < last ? adapters[request_of(off, p.G, mine_row)] : -1;
+    // rows past the last, rank columns past the last and chunks past the contraction
+    // read as zeros
+    const int ldx2 = (int)(p.lda * 2), k2 = k * 2;
+    const int64_t rows = last - row0;
+    const __amdgpu_buffer_rsrc_t x =
+        make_rsrc(p.a + row0 * p.lda, (rows < kLowRows ? rows : kLowRows) * ldx2);
     uint32_t todo = (uint32_t)__ballot(id >= 0);
     int turn = 0;
     while (todo != 0) {
@@ -77,13 +70,9 @@ __global__ __launch_bounds__(kLowThreads) void lora_low_kernel(Args p, const uin
       const bool mine = turn == turn0;
       turn = turn + 1 == turns ? 0 : turn + 1;
       if (!mine) continue;
-      const uint16_t* d[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        int j = j0 + 16 * b + r;
-        if (j >= rank) j = rank - 1;  // such columns are not written
-        d[b] = down + ((int64_t)a * rank + j) * p.k + 8 * q;
-      }
+      const int left = rank - j0;
+      const __amdgpu_buffer_rsrc_t d = make_rsrc(down + ((int64_t)a * rank + j0) * p.k,
+                                                 (int64_t)(left < 16 * NB ? left : 16 * NB) * k2);
       v4f acc[2][NB];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -91,19 +80,20 @@ __global__ __launch_bounds__(kLowThreads) void lora_low_kernel(Args p, const uin
         for (int b = 0; b < NB; ++b) acc[i][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
       // kRuns of the wave's runs are loaded before the first is used
       constexpr int kRuns = NB == 4 ? 2 : 4;
-      for (int k0 = 64 * w; k0 < k; k0 += 64 * kLowWaves * kRuns) {
+      const int end = 64 * run1 < k ? 64 * run1 : k;
+      for (int k0 = 64 * (run0 + w); k0 < end; k0 += 64 * kLowWaves * kRuns) {
         v4i fx[2 * kRuns][2], fd[2 * kRuns][NB];
 #pragma unroll
         for (int c = 0; c < 2 * kRuns; ++c) {
           const int at = k0 + (c >> 1) * 64 * kLowWaves + 32 * (c & 1);
-          const bool in = at + 8 * q < k;
-          const v4i zero = v4i{0, 0, 0, 0};
+          const uint32_t o = at + 8 * q < end ? 2 * (at + 8 * q) : kDmaOutOfRange;
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            fx[c][i] = in ? *reinterpret_cast<const v4i*>(x[i] + at) : zero;
+            fx[c][i] =
+                __builtin_amdgcn_raw_buffer_load_b128(x, (int)(o + (16 * i + r) * ldx2), 0, 0);
 #pragma unroll
           for (int b = 0; b < NB; ++b)
-            fd[c][b] = in ? *reinterpret_cast<const v4i*>(d[b] + at) : zero;
+            fd[c][b] = __builtin_amdgcn_raw_buffer_load_b128(d, (int)(o + (16 * b + r) * k2), 0, 0);
         }
         fence();
 #pragma unroll
@@ -129,16 +119,22 @@ __global__ __launch_bounds__(kLowThreads) void lora_low_kernel(Args p, const uin
           for (int e = 0; e < 4; ++e) s[e] += t[e];
         }
         const int j = j0 + 16 * b + 4 * q;
+        const int64_t row = row0 + 16 * i + r;
         if ((own >> (16 * i + r) & 1) != 0 && j < rank) {
-          const float f = scale[a];
-          uint32_t top[4], rest[4];
+          if (parts > 1) {
+            float* dst = low32 + (part * p.rows_cap + row) * rank + j;
+            *reinterpret_cast<v4f*>(dst) = s;
+          } else {
+            const float f = p.scale[a];
+            uint32_t top[4], rest[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) split16<F16>(s[e] * f, top[e], rest[e]);
-          uint16_t* dst = low + (row0 + 16 * i + r) * 2 * rank + j;
-          *reinterpret_cast<v2i*>(dst) =
-              v2i{(int)(top[0] | top[1] << 16), (int)(top[2] | top[3] << 16)};
-          *reinterpret_cast<v2i*>(dst + rank) =
-              v2i{(int)(rest[0] | rest[1] << 16), (int)(rest[2] | rest[3] << 16)};
+            for (int e = 0; e < 4; ++e) split16<F16>(s[e] * f, top[e], rest[e]);
+            uint16_t* dst = low16 + row * 2 * rank + j;
+            *reinterpret_cast<v2i*>(dst) =
+                v2i{(int)(top[0] | top[1] << 16), (int)(top[2] | top[3] << 16)};
+            *reinterpret_cast<v2i*>(dst + rank) =
+                v2i{(int)(rest[0] | rest[1] << 16), (int)(rest[2] | rest[3] << 16)};
+          }
         }
       }
       __syncthreads();
@@ -146,12 +142,15 @@ __global__ __launch_bounds__(kLowThreads) void lora_low_kernel(Args p, const uin
   }
 }
 
+// Parts of the first product's contraction: several where the rows are few.
+int low_parts(int64_t rows_cap, int64_t k) { return rows_cap <= 64 && k >= 1024 ? kLowParts : 1; }
+
 template <bool F16>
-hipError_t launch_low(const Args& p, const uint16_t* down, const float* scale, uint16_t* low,
-                      hipStream_t stream) {
+hipError_t launch_low(const Args& p, const uint16_t* down, hipStream_t stream) {
   const int nb = p.r <= 16 ? 1 : p.r <= 32 ? 2 : 4;
   // as many workgroups share a block's adapters as fill the compute units
-  const int64_t blocks = (p.rows_cap + kLowRows - 1) / kLowRows * ((p.r + 16 * nb - 1) / (16 * nb));
+  const int64_t blocks = (p.rows_cap + kLowRows - 1) / kLowRows *
+                         ((p.r + 16 * nb - 1) / (16 * nb)) * p.low_parts;
   const int64_t cap = 2 * (int64_t)device_cu_count();
   int64_t turns = cap / blocks;
   turns = turns < 1 ? 1 : turns > kLowRows ? kLowRows : turns;
@@ -160,12 +159,9 @@ hipError_t launch_low(const Args& p, const uint16_t* down, const float* scale, u
   const int64_t grid = blocks * turns < cap ? blocks * turns : cap;
   const dim3 gd((unsigned)grid), bd(kLowThreads);
   const int tn = (int)turns;
-  if (nb == 1)
-    hipLaunchKernelGGL((lora_low_kernel<F16, 1>), gd, bd, 0, stream, p, down, scale, low, tn);
-  else if (nb == 2)
-    hipLaunchKernelGGL((lora_low_kernel<F16, 2>), gd, bd, 0, stream, p, down, scale, low, tn);
-  else
-    hipLaunchKernelGGL((lora_low_kernel<F16, 4>), gd, bd, 0, stream, p, down, scale, low, tn);
+  if (nb == 1) hipLaunchKernelGGL((lora_low_kernel<F16, 1>), gd, bd, 0, stream, p, down, tn);
+  else if (nb == 2) hipLaunchKernelGGL((lora_low_kernel<F16, 2>), gd, bd, 0, stream, p, down, tn);
+  else hipLaunchKernelGGL((lora_low_kernel<F16, 4>), gd, bd, 0, stream, p, down, tn);
   return hipGetLastError();
 }
 
@@ -213,8 +209,8 @@ hipError_t launch_gemm_16bit(int mode, int f16, int G, const void* a, int64_t ld
 
 size_t lora_gemm_16bit_workspace_bytes(int64_t rows_cap, int64_t n, int64_t k, int64_t r) {
   (void)n;
-  (void)k;
-  return gemm_16bit_workspace_bytes() + align256((size_t)rows_cap * (size_t)r * 4);
+  return gemm_16bit_workspace_bytes() +
+         align256((size_t)rows_cap * (size_t)r * 4 * (size_t)low_parts(rows_cap, k));
 }
 
 hipError_t launch_lora_gemm_16bit(int f16, int G, const void* x, int64_t ldx, const void* w,
@@ -224,7 +220,6 @@ hipError_t launch_lora_gemm_16bit(int f16, int G, const void* x, int64_t ldx, co
                                   int64_t n, int64_t k, void* out, int64_t ldo, int out_f32,
                                   void* ws, uint32_t* status, hipStream_t stream) {
   if (rows_cap <= 0) return hipSuccess;
-  uint16_t* low = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + gemm_16bit_workspace_bytes());
   Args p{};
   p.a = static_cast<const uint16_t*>(x);
   p.b = static_cast<const uint16_t*>(w);
@@ -235,14 +230,15 @@ hipError_t launch_lora_gemm_16bit(int f16, int G, const void* x, int64_t ldx, co
   p.status = status;
   p.ws = static_cast<char*>(ws);
   p.G = G; p.out_f32 = out_f32;
-  p.low = low;
+  p.low = static_cast<char*>(ws) + gemm_16bit_workspace_bytes();
+  p.low_parts = low_parts(rows_cap, k);
+  p.scale = scale;
   p.up = static_cast<const uint16_t*>(up);
   p.adapter = adapter;
   p.num_adapters = (int)num_adapters;
   p.r = (int)r;
   const uint16_t* d = static_cast<const uint16_t*>(down);
-  const hipError_t e =
-      f16 ? launch_low<true>(p, d, scale, low, stream) : launch_low<false>(p, d, scale, low, stream);
+  const hipError_t e = f16 ? launch_low<true>(p, d, stream) : launch_low<false>(p, d, stream);
   if (e != hipSuccess) return e;
   return launch_form(kLora, f16, p, stream);
 }
