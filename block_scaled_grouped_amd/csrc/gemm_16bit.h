@@ -656,7 +656,8 @@ __device__ __forceinline__ void store_blocks(const v4f (&acc)[MI][NJ], const Out
 // not depend on which part ended first.
 //
 // Workspace: header (L, S), a record for each split tile, then the parts.
-constexpr int kSplitMax = 16;
+constexpr int kSplitMax = 32;
+constexpr int kLeastStages = 4;  // of a part
 constexpr int64_t kWsHeader = 16384;
 constexpr int kMaxSplitTiles = (int)((kWsHeader - 64) / 32);
 

@@ -13,14 +13,15 @@ namespace {
 // A workgroup of eight waves takes 32 consecutive rows, 16 NB rank columns, one of
 // the adapters that occur in those rows and one part of the contraction; the waves
 // take turns at the part's runs of 64 (a 128-byte line of a row) and their sums are
-// added through LDS in one order.  Rows of another adapter are computed too and not
+// added through LDS in one order.  Rows of another adapter are neither read nor
 // written.  Operands come straight from memory: nothing is shared between waves
 // that LDS could serve.  A compute unit takes 64 GB/s that way, 28 past its L2, so
-// where the rows are few the contraction is spread over several workgroups, whose
-// parts the second product adds.
+// where the rows are few, 16 rank columns and a part of the contraction make a
+// workgroup, and the second product adds the parts.
 constexpr int kLowThreads = 512;
 constexpr int kLowWaves = kLowThreads / 64;
 constexpr int kLowRows = 32;
+constexpr int64_t kFewRows = 1024;  // 32 blocks of rows leave compute units idle
 
 template <bool F16, int NB>  // 16 NB <= 64 rank columns a workgroup
 __global__ __launch_bounds__(kLowThreads) void lora_low_kernel(Args p, const uint16_t* down,
@@ -74,10 +75,14 @@ __global__ __launch_bounds__(kLowThreads) void lora_low_kernel(Args p, const uin
       const __amdgpu_buffer_rsrc_t d = make_rsrc(down + ((int64_t)a * rank + j0) * p.k,
                                                  (int64_t)(left < 16 * NB ? left : 16 * NB) * k2);
       v4f acc[2][NB];
+      uint32_t xrow[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
+        xrow[i] = (own >> (16 * i + r) & 1) != 0 ? (uint32_t)((16 * i + r) * ldx2)
+                                                 : (uint32_t)kDmaOutOfRange;
 #pragma unroll
         for (int b = 0; b < NB; ++b) acc[i][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      }
       // kRuns of the wave's runs are loaded before the first is used
       constexpr int kRuns = NB == 4 ? 2 : 4;
       const int end = 64 * run1 < k ? 64 * run1 : k;
@@ -89,8 +94,7 @@ __global__ __launch_bounds__(kLowThreads) void lora_low_kernel(Args p, const uin
           const uint32_t o = at + 8 * q < end ? 2 * (at + 8 * q) : kDmaOutOfRange;
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            fx[c][i] =
-                __builtin_amdgcn_raw_buffer_load_b128(x, (int)(o + (16 * i + r) * ldx2), 0, 0);
+            fx[c][i] = __builtin_amdgcn_raw_buffer_load_b128(x, (int)(o + xrow[i]), 0, 0);
 #pragma unroll
           for (int b = 0; b < NB; ++b)
             fd[c][b] = __builtin_amdgcn_raw_buffer_load_b128(d, (int)(o + (16 * b + r) * k2), 0, 0);
@@ -143,11 +147,13 @@ __global__ __launch_bounds__(kLowThreads) void lora_low_kernel(Args p, const uin
 }
 
 // Parts of the first product's contraction: several where the rows are few.
-int low_parts(int64_t rows_cap, int64_t k) { return rows_cap <= 64 && k >= 1024 ? kLowParts : 1; }
+int low_parts(int64_t rows_cap, int64_t k) {
+  return rows_cap <= kFewRows && k >= 1024 ? kLowParts : 1;
+}
 
 template <bool F16>
 hipError_t launch_low(const Args& p, const uint16_t* down, hipStream_t stream) {
-  const int nb = p.r <= 16 ? 1 : p.r <= 32 ? 2 : 4;
+  const int nb = p.rows_cap <= kFewRows || p.r <= 16 ? 1 : p.r <= 32 ? 2 : 4;
   // as many workgroups share a block's adapters as fill the compute units
   const int64_t blocks = (p.rows_cap + kLowRows - 1) / kLowRows *
                          ((p.r + 16 * nb - 1) / (16 * nb)) * p.low_parts;
@@ -167,18 +173,62 @@ hipError_t launch_low(const Args& p, const uint16_t* down, hipStream_t stream) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Runs the form whose tiles fit the rows a group has on average.
-hipError_t launch_form(int mode, int f16, const Args& p, hipStream_t stream) {
-  int64_t per = mode == kLora ? p.rows_cap : p.rows_cap / p.G;
-  int64_t tiles;
+// The form with the least expected time, by what a round of tiles costs in each:
+//   stages of the longest workgroup * us a stage + us a tile + us of the second step
+// where the last round is split.  Measured with every slot taken: a stage of 64
+// contraction indexes costs a workgroup 1.45 us with 256 x 256 tiles (1.5 PFLOP/s in
+// all), 1.14, 0.70 and 0.52 us with 128, 64 and 32 x 128 (0.94, 0.77 and 0.52
+// PFLOP/s, two workgroups a compute unit).  So large tiles win where they fill the
+// chip, and small ones where few rows, short contractions or narrow outputs leave
+// them idle: 16384 x 14336 x 4096 in 8 groups 1.45 against 2.05 ms (128) and 3.72 ms
+// (32), 844 rows of three groups x 312 x 2864 31 (256) against 23 us (64).  Over 70
+// calls of random sizes the choice costs 1.5 % over the best of the four.  Group sizes
+// are on the device, so a nonempty group counts for half a tile more than its rows.
+struct Form {
+  int bm, bn;
+  double stage_us, tile_us, reduce_us;
+};
+constexpr Form kForms[4] = {
+    {32, 128, 0.52, 1.5, 4.0}, {64, 128, 0.70, 2.0, 5.0}, {128, 128, 1.14, 3.0, 8.0},
+    {256, 256, 1.45, 7.0, 18.0}};
+
+double expected_us(const Form& f, int mode, const Args& p) {
+  const int64_t slots = (f.bm == 256 ? 1 : 2) * (int64_t)device_cu_count();
+  const int64_t ntn = (p.n + f.bn - 1) / f.bn;
+  int64_t tiles, stages, split_stages;
   if (mode == kWgrad) {
-    tiles = (int64_t)p.G * ((p.n + 255) / 256) * ((p.k + 255) / 256);
-    per = 256;
+    tiles = p.G * ((p.n + f.bm - 1) / f.bm) * ((p.k + f.bn - 1) / f.bn);
+    split_stages = (p.rows_cap + kStageK - 1) / kStageK;
+    stages = (p.rows_cap / p.G + kStageK - 1) / kStageK;
+    if (stages < 1) stages = 1;
   } else {
-    tiles = (p.rows_cap + 255) / 256 * ((p.n + 255) / 256);
+    const int64_t groups = mode == kLora ? 1 : p.rows_cap < p.G ? p.rows_cap : p.G;
+    tiles = ((p.rows_cap + f.bm - 1) / f.bm + (groups > 1 ? groups / 2 : 0)) * ntn;
+    split_stages = stages = (p.k + kStageK - 1) / kStageK;
   }
-  if (per >= 160 && 4 * tiles >= 3 * device_cu_count()) return launch_large(mode, f16, p, stream);
-  return launch_small(mode, f16, per <= 40 ? 32 : per <= 96 ? 64 : 128, p, stream);
+  const int64_t full = tiles / slots, left = tiles % slots;
+  double us = (double)full * ((double)stages * f.stage_us + f.tile_us);
+  if (left > 0) {
+    const int parts =
+        p.ws == nullptr ? 1 : split_parts((int)slots, (int)left, (int)split_stages, kLeastStages);
+    us += (double)((stages + parts - 1) / parts) * f.stage_us + f.tile_us +
+          (parts > 1 ? f.reduce_us : 0.0);
+  }
+  return us;
+}
+
+hipError_t launch_form(int mode, int f16, const Args& p, hipStream_t stream) {
+  int best = mode == kWgrad ? 2 : 0;  // weight gradients have no forms of fewer rows
+  double us = expected_us(kForms[best], mode, p);
+  for (int i = best + 1; i < 4; ++i) {
+    const double t = expected_us(kForms[i], mode, p);
+    if (t < us) {
+      us = t;
+      best = i;
+    }
+  }
+  const int bm = kForms[best].bm;
+  return bm == 256 ? launch_large(mode, f16, p, stream) : launch_small(mode, f16, bm, p, stream);
 }
 
 }  // namespace

@@ -183,7 +183,7 @@ __global__ __launch_bounds__(kThreads) void large_kernel(Args p) {
       p.ws == nullptr
           ? 1
           : split_parts(grid, left,
-                        (int)(((MODE == kWgrad ? p.rows_cap : p.k) + kStageK - 1) / kStageK), 4);
+                        (int)(((MODE == kWgrad ? p.rows_cap : p.k) + kStageK - 1) / kStageK), kLeastStages);
   write_split_header(p.ws, total, nsplit);
   const int slot = xcd_slot();
   for (int round = 0;; ++round) {
@@ -228,7 +228,7 @@ hipError_t launch(const Args& p, hipStream_t stream) {
   else bound = ((p.rows_cap + BM - 1) / BM + (MODE == kLora ? 0 : p.G)) * ((p.n + BN - 1) / BN);
   const int cus = device_cu_count();
   const int64_t kl = MODE == kWgrad ? p.rows_cap : p.k;
-  const int parts = p.ws != nullptr ? split_parts(cus, 1, (int)((kl + kStageK - 1) / kStageK), 4) : 1;
+  const int parts = p.ws != nullptr ? split_parts(cus, 1, (int)((kl + kStageK - 1) / kStageK), kLeastStages) : 1;
   int64_t grid = bound * parts < cus ? bound * parts : cus;
   if (grid <= 0) return hipSuccess;
   hipLaunchKernelGGL((large_kernel<MODE, F16>), dim3((unsigned)grid), dim3(kThreads), 0, stream, p);

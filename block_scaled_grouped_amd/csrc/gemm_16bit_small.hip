@@ -103,7 +103,7 @@ __global__ __launch_bounds__(kThreads, kWgPerCu) void small_kernel(Args p) {
       p.ws == nullptr
           ? 1
           : split_parts(grid, left,
-                        (int)(((MODE == kWgrad ? p.rows_cap : p.k) + kStageK - 1) / kStageK), 4);
+                        (int)(((MODE == kWgrad ? p.rows_cap : p.k) + kStageK - 1) / kStageK), kLeastStages);
   write_split_header(p.ws, total, nsplit);
   const int slot = xcd_slot();
   for (int round = 0;; ++round) {
@@ -147,7 +147,7 @@ hipError_t launch(const Args& p, hipStream_t stream) {
   else bound = ((p.rows_cap + BM - 1) / BM + (MODE == kLora ? 0 : p.G)) * ((p.n + BN - 1) / BN);
   const int cap = kWgPerCu * device_cu_count();
   const int64_t kl = MODE == kWgrad ? p.rows_cap : p.k;
-  const int parts = p.ws != nullptr ? split_parts(cap, 1, (int)((kl + kStageK - 1) / kStageK), 4) : 1;
+  const int parts = p.ws != nullptr ? split_parts(cap, 1, (int)((kl + kStageK - 1) / kStageK), kLeastStages) : 1;
   const int64_t grid = bound * parts < cap ? bound * parts : cap;
   if (grid <= 0) return hipSuccess;
   hipLaunchKernelGGL((small_kernel<MODE, F16, BM>), dim3((unsigned)grid), dim3(kThreads), 0, stream,
