@@ -283,6 +283,15 @@ struct Side {
     }
   }
 
+  // Says again that what is uniform is (it is carried from one tile to the next).
+  __device__ __forceinline__ void make_uniform() {
+    base = (uint64_t)uni64((int64_t)base);
+    range = uni(range);
+    ld2 = uni(ld2);
+    kl = uni(kl);
+    last = (uint64_t)uni64((int64_t)last);
+  }
+
   // Lanes whose chunk lies within the contraction in stage kt of `stages`.
   __device__ __forceinline__ uint64_t mask(int kt, int stages) const {
     return kt == stages - 1 ? last : ~0ull;
@@ -559,90 +568,118 @@ struct OutTile {
   int ldo, rows, cols;
 };
 
+// This lane's byte offset of a block's columns 4 q + [0, 4) in an output tile: a
+// column past out_cols gets an offset past every range.
+template <int ESZ>
+__device__ __forceinline__ int block_off(int ldo, int row, int col, int out_cols) {
+  return col < out_cols ? (row * ldo + col) * ESZ : (int)kDropped;
+}
+
+// The addend of one 16 x 16 block as it lies in memory, and as numbers.
+template <bool F32>
+struct Addend {
+  v4i v;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rc, int off) {
+    if constexpr (F32) {
+      v = __builtin_amdgcn_raw_buffer_load_b128(rc, off, 0, 0);
+    } else {
+      const v2i t = __builtin_amdgcn_raw_buffer_load_b64(rc, off, 0, 0);
+      v[0] = t[0];
+      v[1] = t[1];
+    }
+  }
+  template <bool F16>
+  __device__ __forceinline__ float at(int e) const {
+    if constexpr (F32) return __int_as_float(v[e]);
+    const uint32_t bits = ((uint32_t)v[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+    return F16 ? (float)__builtin_bit_cast(_Float16, (unsigned short)bits) : bf16_to_f32(bits);
+  }
+};
+
 // Two neighbouring 16 x 16 blocks of accumulators, the first at column col0: this
 // lane's row `row`, columns col0 + 16 b + 4 q + [0, 4).  Rows past the live ones
-// are dropped by the descriptors' range, columns past out_cols by an offset past
-// every range.  C is added in float32 before the one rounding.
+// are dropped by the descriptors' range.
 //   float32: a store is 16 bytes a lane, 64-byte runs of 16 rows.
 //   16-bit:  lanes trade halves of the two blocks (v_permlane16_swap), after which
 //            lane (r, q) holds columns 8 (q / 2) + [0, 8) of block q % 2: 16 bytes
 //            a lane, and again 64-byte runs of 16 rows.
 template <bool F32, bool F16>
-__device__ __forceinline__ void store_pair(v4f y0, v4f y1, __amdgpu_buffer_rsrc_t ro,
-                                           __amdgpu_buffer_rsrc_t rc, bool add, int ldo, int row,
-                                           int col0, int q, int out_cols) {
-  constexpr int esz = F32 ? 4 : 2;
-  int off[2];
-#pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    const int col = col0 + 16 * b + 4 * q;
-    off[b] = col < out_cols ? (row * ldo + col) * esz : (int)kDropped;
-  }
-  if (add) {
-    float c[8];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      if constexpr (F32) {
-        const v4i v = __builtin_amdgcn_raw_buffer_load_b128(rc, off[b], 0, 0);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c[4 * b + e] = __int_as_float(v[e]);
-      } else {
-        const v2i v = __builtin_amdgcn_raw_buffer_load_b64(rc, off[b], 0, 0);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t bits = ((uint32_t)v[e >> 1] >> (16 * (e & 1))) & 0xffffu;
-          c[4 * b + e] = F16 ? (float)__builtin_bit_cast(_Float16, (unsigned short)bits)
-                             : bf16_to_f32(bits);
-        }
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      y0[e] += c[e];
-      y1[e] += c[4 + e];
-    }
-  }
+__device__ __forceinline__ void store_pair(const v4f& y0, const v4f& y1, __amdgpu_buffer_rsrc_t ro,
+                                           int ldo, int row, int col0, int q, int out_cols) {
   if constexpr (F32) {
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, y0), ro, off[0], 0, 0);
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, y1), ro, off[1], 0, 0);
+    const int col = col0 + 4 * q;
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, y0), ro,
+                                           block_off<4>(ldo, row, col, out_cols), 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, y1), ro,
+                                           block_off<4>(ldo, row, col + 16, out_cols), 0, 0);
   } else {
     const auto lo = __builtin_amdgcn_permlane16_swap((int)pack16<F16>(y0[0], y0[1]),
                                                      (int)pack16<F16>(y1[0], y1[1]), false, false);
     const auto hi = __builtin_amdgcn_permlane16_swap((int)pack16<F16>(y0[2], y0[3]),
                                                      (int)pack16<F16>(y1[2], y1[3]), false, false);
     const int col = col0 + 16 * (q & 1) + 8 * (q >> 1);
-    const int at = col < out_cols ? (row * ldo + col) * 2 : (int)kDropped;
-    __builtin_amdgcn_raw_buffer_store_b128(
-        (v4i){(int)lo[0], (int)hi[0], (int)lo[1], (int)hi[1]}, ro, at, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128((v4i){(int)lo[0], (int)hi[0], (int)lo[1], (int)hi[1]},
+                                           ro, block_off<2>(ldo, row, col, out_cols), 0, 0);
   }
 }
 
-// A wave's MI x NJ blocks, the first at (wrow, wcol) of the tile, two at a time:
-// the accumulators are copied out right before their loads and stores.
-template <bool F16, int MI, int NJ>
-__device__ __forceinline__ void store_blocks(const v4f (&acc)[MI][NJ], const OutTile& o,
-                                             int out_f32, int wrow, int wcol, int lane) {
+// A wave's MI x NJ blocks, the first at (wrow, wcol) of the tile, two at a time: the
+// accumulators are copied out right before their stores.  The addend, if there is
+// one, is added in float32 before the one rounding, and read a row of blocks ahead.
+template <bool F16, bool F32, bool ADD, int MI, int NJ>
+__device__ __forceinline__ void store_rows(const v4f (&acc)[MI][NJ], const OutTile& o, int wrow,
+                                           int wcol, int lane) {
   static_assert(NJ % 2 == 0, "blocks are stored in pairs");
-  const int esz = out_f32 ? 4 : 2;
+  constexpr int esz = F32 ? 4 : 2;
   int ldo = o.ldo;
   asm volatile("" : "+s"(ldo));  // keeps all the store offsets from being hoisted
   const __amdgpu_buffer_rsrc_t ro = make_rsrc(o.out, (int64_t)o.rows * o.ldo * esz);
-  const bool add = o.c != nullptr;
-  const __amdgpu_buffer_rsrc_t rc = make_rsrc(o.c, add ? (int64_t)o.rows * o.ldo * esz : 0);
+  const __amdgpu_buffer_rsrc_t rc = make_rsrc(o.c, ADD ? (int64_t)o.rows * o.ldo * esz : 0);
   const int q = lane >> 4, row = wrow + (lane & 15);
+  Addend<F32> c[2][NJ];
+  if constexpr (ADD) {
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
+    for (int j = 0; j < NJ; ++j)
+      c[0][j].load(rc, block_off<esz>(ldo, row, wcol + 16 * j + 4 * q, o.cols));
+  }
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    if constexpr (ADD) {
+      fence();
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        if (i + 1 < MI)
+          c[(i + 1) & 1][j].load(
+              rc, block_off<esz>(ldo, row + 16 * (i + 1), wcol + 16 * j + 4 * q, o.cols));
+    }
 #pragma unroll
     for (int j = 0; j < NJ; j += 2) {
       fence();
       v4f y0 = acc[i][j], y1 = acc[i][j + 1];
       asm volatile("" : "+v"(y0), "+v"(y1));
-      if (out_f32)
-        store_pair<true, F16>(y0, y1, ro, rc, add, ldo, row + 16 * i, wcol + 16 * j, q, o.cols);
-      else
-        store_pair<false, F16>(y0, y1, ro, rc, add, ldo, row + 16 * i, wcol + 16 * j, q, o.cols);
+      if constexpr (ADD) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y0[e] += c[i & 1][j].template at<F16>(e);
+          y1[e] += c[i & 1][j + 1].template at<F16>(e);
+        }
+      }
+      store_pair<F32, F16>(y0, y1, ro, ldo, row + 16 * i, wcol + 16 * j, q, o.cols);
       fence();
     }
+  }
+}
+
+template <bool F16, int MI, int NJ>
+__device__ __forceinline__ void store_blocks(const v4f (&acc)[MI][NJ], const OutTile& o,
+                                             int out_f32, int wrow, int wcol, int lane) {
+  if (o.c != nullptr) {
+    if (out_f32) store_rows<F16, true, true>(acc, o, wrow, wcol, lane);
+    else store_rows<F16, false, true>(acc, o, wrow, wcol, lane);
+  } else {
+    if (out_f32) store_rows<F16, true, false>(acc, o, wrow, wcol, lane);
+    else store_rows<F16, false, false>(acc, o, wrow, wcol, lane);
+  }
 }
 
 // ---------------------------------------------------------------- split contractions

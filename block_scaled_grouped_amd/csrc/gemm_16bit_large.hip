@@ -96,40 +96,49 @@ __device__ __forceinline__ void mfma(const Half& a, const Half& b, v4f (&acc)[8]
 // Wait states before the accumulators of a run are read by vector instructions.
 __device__ __forceinline__ void mfma_drain() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
-// One tile's contraction.
-template <int MODE, bool F16>
-__device__ __forceinline__ void contract(uint32_t lds, const Tile& t, int w, int lane,
-                                         v4f (&acc)[8][8]) {
-  const int stages = uni((t.kl + kStageK - 1) / kStageK);
-  if (stages == 0) return;
-  Copies<MODE> c;
+// Begins a tile: the copies of its first two stages, into the two buffers.
+template <int MODE>
+__device__ __forceinline__ void begin_tile(Copies<MODE>& c, uint32_t lds, const Tile& t, int w,
+                                           int lane) {
   c.a.init(t.a, t.lda, t.a_rows, t.kl, w, lane);
   c.b.init(t.b, t.ldb, t.b_rows, t.kl, w, lane);
-  c.lds = uni(lds + w * 1024);
-  c.stages = stages;
+  c.stages = uni((t.kl + kStageK - 1) / kStageK);
+  if (c.stages == 0) return;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    c.lds = uni(lds + s * kBufBytes + w * 1024);
+    c.begin(s);
+    static_for<kCopies>([&](auto q) {
+      constexpr int P = decltype(q)::value;
+      c.template copy_end<P>(c.template copy_begin<P>());
+    });
+  }
+}
+
+// A tile's contraction, begun by begin_tile.  stored: the epilogue of the tile before
+// came after those copies, with at least kEpilogueStores stores.
+constexpr int kEpilogueStores = 32;
+
+template <int MODE, bool F16>
+__device__ __forceinline__ void contract(Copies<MODE>& c, uint32_t lds, int w, int lane,
+                                         bool stored, v4f (&acc)[8][8]) {
+  c.stages = uni(c.stages);
+  if (c.stages == 0) return;
+  c.a.make_uniform();
+  c.b.make_uniform();
   using FragsA = FragOff<kColsA<MODE>, BM, 8>;
   using FragsB = FragOff<kColsB<MODE>, BN, 8>;
   FragsA fa;
   FragsB fb;
   fa.init(lds, (w >> 1) * 128, lane);
   fb.init(lds + kTileBytes, (w & 1) * 128, lane);
-  c.begin(0);
-  static_for<kCopies>([&](auto q) {
-    constexpr int P = decltype(q)::value;
-    c.template copy_end<P>(c.template copy_begin<P>());
-  });
-  c.lds += kBufBytes;
-  c.begin(1);
-  static_for<kCopies>([&](auto q) {
-    constexpr int P = decltype(q)::value;
-    c.template copy_end<P>(c.template copy_begin<P>());
-  });
-  c.lds -= kBufBytes;
-  wait_and_barrier<kCopies>();
+  c.lds = uni(lds + w * 1024);
+  if (stored) wait_and_barrier<kCopies + kEpilogueStores>();
+  else wait_and_barrier<kCopies>();
   Half a0, b0, a1, b1;
   static_for<16>([&](auto q) { read_frag<MODE, 0, decltype(q)::value>(fa, fb, a0, b0); });
   int other = kBufBytes;  // bytes to the other buffer
-  for (int kt = 0; kt < stages; ++kt) {
+  for (int kt = 0; kt < c.stages; ++kt) {
     c.begin(kt + 2);
     int voff = 0;
     fence();
@@ -171,6 +180,8 @@ __device__ __forceinline__ void contract(uint32_t lds, const Tile& t, int w, int
   fence();
 }
 
+// A tile's copies are begun before the epilogue of the one before it, so that they
+// arrive while that one's stores go out.
 template <int MODE, bool F16>
 __global__ __launch_bounds__(kThreads) void large_kernel(Args p) {
   __shared__ __attribute__((aligned(16))) uint8_t ring[2 * kBufBytes];
@@ -183,14 +194,18 @@ __global__ __launch_bounds__(kThreads) void large_kernel(Args p) {
       p.ws == nullptr
           ? 1
           : split_parts(grid, left,
-                        (int)(((MODE == kWgrad ? p.rows_cap : p.k) + kStageK - 1) / kStageK), kLeastStages);
+                        (int)(((MODE == kWgrad ? p.rows_cap : p.k) + kStageK - 1) / kStageK),
+                        kLeastStages);
   write_split_header(p.ws, total, nsplit);
   const int slot = xcd_slot();
-  for (int round = 0;; ++round) {
-    const Work work = take_work(round, slot, total, nsplit);
-    if (work.tile < 0) break;
-    Tile t = find_tile<MODE, BM, BN>(p, sm, uni(work.tile));
-    if (work.part >= 0) narrow_tile<MODE>(t, uni(work.part), nsplit);
+  Work work = take_work(0, slot, total, nsplit);
+  if (work.tile < 0) return;
+  Tile t = find_tile<MODE, BM, BN>(p, sm, uni(work.tile));
+  if (work.part >= 0) narrow_tile<MODE>(t, uni(work.part), nsplit);
+  Copies<MODE> c;
+  begin_tile(c, lds, t, uni((int)(threadIdx.x >> 6)), threadIdx.x & 63);
+  bool stored = false;
+  for (int round = 1;; ++round) {
     // opaque per-tile copy of the thread index: keeps the offsets of the tile body
     // from being hoisted out of the persistent loop
     int tid = threadIdx.x;
@@ -201,12 +216,22 @@ __global__ __launch_bounds__(kThreads) void large_kernel(Args p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int j = 0; j < 8; ++j) {
+        acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        asm volatile("" : "+a"(acc[i][j]));
+      }
     if constexpr (MODE == kLora) tile_adapters<BM>(p, sm, t, ids);
-    contract<MODE, F16>(lds, t, w, lane, acc);
+    contract<MODE, F16>(c, lds, w, lane, stored, acc);
     // every copy has landed and no wave still reads a buffer before the next
     // tile's first copies
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    const Work next = take_work(round, slot, total, nsplit);
+    Tile tn = t;
+    if (next.tile >= 0) {
+      tn = find_tile<MODE, BM, BN>(p, sm, uni(next.tile));
+      if (next.part >= 0) narrow_tile<MODE>(tn, uni(next.part), nsplit);
+      begin_tile(c, lds, tn, w, lane);
+    }
     if constexpr (MODE == kLora) {
       add_low_rank<F16, 8, 8>(p, t, ids, wrow, wcol, lane, uni(work.part), work.nparts, acc);
       __syncthreads();  // ids are read before the next tile's
@@ -218,6 +243,10 @@ __global__ __launch_bounds__(kThreads) void large_kernel(Args p) {
     } else {
       store_blocks<F16, 8, 8>(acc, out_tile(p, t), p.out_f32, wrow, wcol, lane);
     }
+    if (next.tile < 0) break;
+    stored = work.part < 0;
+    work = next;
+    t = tn;
   }
 }
 
