@@ -176,13 +176,13 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 // The form with the least expected time, by what a round of tiles costs in each:
 //   stages of the longest workgroup * us a stage + us a tile + us of the second step
 // where the last round is split.  Measured with every slot taken: a stage of 64
-// contraction indexes costs a workgroup 1.45 us with 256 x 256 tiles (1.5 PFLOP/s in
+// contraction indexes costs a workgroup 1.37 us with 256 x 256 tiles (1.57 PFLOP/s in
 // all), 1.14, 0.70 and 0.52 us with 128, 64 and 32 x 128 (0.94, 0.77 and 0.52
 // PFLOP/s, two workgroups a compute unit).  So large tiles win where they fill the
 // chip, and small ones where few rows, short contractions or narrow outputs leave
-// them idle: 16384 x 14336 x 4096 in 8 groups 1.45 against 2.05 ms (128) and 3.72 ms
-// (32), 844 rows of three groups x 312 x 2864 31 (256) against 23 us (64).  Over 70
-// calls of random sizes the choice costs 1.5 % over the best of the four.  Group sizes
+// them idle: 16384 x 14336 x 4096 in 8 groups 1.39 against 2.05 ms (128) and 3.72 ms
+// (32), 844 rows of three groups x 312 x 2864 31 (256) against 23 us (64).  Over 170
+// calls of random sizes the choice costs 1 % over the best of the four.  Group sizes
 // are on the device, so a nonempty group counts for half a tile more than its rows.
 struct Form {
   int bm, bn;
@@ -190,7 +190,7 @@ struct Form {
 };
 constexpr Form kForms[4] = {
     {32, 128, 0.52, 1.5, 4.0}, {64, 128, 0.70, 2.0, 5.0}, {128, 128, 1.14, 3.0, 8.0},
-    {256, 256, 1.45, 7.0, 18.0}};
+    {256, 256, 1.37, 5.0, 18.0}};
 
 double expected_us(const Form& f, int mode, const Args& p) {
   const int64_t slots = (f.bm == 256 ? 1 : 2) * (int64_t)device_cu_count();
