@@ -746,20 +746,21 @@ def _types_16bit(t, name, out_dtype, like=None):
     raise ValueError("out_dtype %r is neither the operands' type nor BSG_OUT_F32" % (out_dtype,))
 
 
-def _strided(t, name, dims, dtype):
-    """Row (and matrix) strides of a tensor whose rows are contiguous: (ld, stride).  A size-1
-    dimension's stride is never used and torch leaves it arbitrary, so a dense one stands in."""
+def _strided(t, name, dims, dtype, index):
+    """Row (and matrix) strides of a tensor on device `index` whose rows are contiguous: (ld,
+    stride).  A size-1 dimension's stride is never used and torch leaves it arbitrary, so a
+    dense one stands in."""
     if t.dim() != dims:
         raise ValueError("%s must be %d-D, not %d-D" % (name, dims, t.dim()))
-    if not t.is_cuda:
-        raise ValueError("%s must be a device tensor" % name)
+    if t.get_device() != index:
+        raise ValueError("%s must be a device tensor, on cuda:%d" % (name, index) if index >= 0
+                         else "%s must be a device tensor" % name)
     if t.dtype != dtype:
         raise ValueError("%s must be %s, not %s" % (name, _dtype_name(dtype), _dtype_name(t.dtype)))
-    st = t.stride()
     if dims == 2:
-        (rows, cols), (ld, one) = t.shape, st
+        (rows, cols), (ld, one) = t.shape, t.stride()
     else:
-        (groups, rows, cols), (stride, ld, one) = t.shape, st
+        (groups, rows, cols), (stride, ld, one) = t.shape, t.stride()
     if one != 1 and cols > 1:
         raise ValueError("the rows of %s must be contiguous" % name)
     if rows <= 1:
@@ -767,6 +768,20 @@ def _strided(t, name, dims, dtype):
     if dims == 2:
         return ld, 0
     return ld, (stride if groups > 1 else rows * ld)
+
+
+def _dense(t, name, nbytes, dtype, index):
+    """_req for a tensor that has to be on device `index`; returns its address."""
+    if t.dtype != dtype or t.get_device() != index or not t.is_contiguous() or t.nbytes < nbytes:
+        _req(t, name, nbytes, dtype)
+        raise ValueError("%s is on %s, not on cuda:%d" % (name, t.device, index))
+    return t.data_ptr()
+
+
+def _device_index(t, name):
+    if not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    return t.get_device()
 
 
 def _same_device(ref, **others):
@@ -796,48 +811,48 @@ def grouped_gemm_16bit(mode, a, b, offsets, c=None, out=None, out_dtype=None, wo
     accumulate).  out_dtype: the operands' type or BSG_OUT_F32; None takes that of `out`
     or `c` where given, else the operands'.  Rows may be strided (strides multiples of 8
     elements).  See include/bsg.h."""
+    import torch
     lib = load_library()
     code, od, odt = _types_16bit(a, "a", out_dtype, out if out is not None else c)
-    lda, _ = _strided(a, "a", 2, a.dtype)
-    _req(offsets, "offsets", 16, _i64())
+    dt, dev = a.dtype, _device_index(a, "a")
+    lda, _ = _strided(a, "a", 2, dt, dev)
+    off = _dense(offsets, "offsets", 16, torch.int64, dev)
     G = offsets.numel() - 1
-    rows = a.shape[0]
+    rows, acols = a.shape
     if mode == BSG_WGRAD_NT:
-        ldb, stride_b = _strided(b, "b", 2, a.dtype)
-        n, k = a.shape[1], b.shape[1]
+        ldb, stride_b = _strided(b, "b", 2, dt, dev)
+        n, k = acols, b.shape[1]
         if b.shape[0] != rows:
             raise ValueError("a has %d rows, b has %d" % (rows, b.shape[0]))
         shape = (G, n, k)
-    elif mode in (BSG_FPROP_TN, BSG_DGRAD_NN):
-        ldb, stride_b = _strided(b, "b", 3, a.dtype)
-        k = a.shape[1]
-        n = b.shape[1] if mode == BSG_FPROP_TN else b.shape[2]
-        if b.shape[0] != G or b.shape[2 if mode == BSG_FPROP_TN else 1] != k:
+    elif mode == BSG_FPROP_TN or mode == BSG_DGRAD_NN:
+        ldb, stride_b = _strided(b, "b", 3, dt, dev)
+        k = acols
+        groups, n, bk = b.shape
+        if mode == BSG_DGRAD_NN:
+            n, bk = bk, n
+        if groups != G or bk != k:
             raise ValueError("b is %s; %d groups contracting %d are needed" % (tuple(b.shape), G, k))
         shape = (rows, n)
     else:
         raise ValueError("mode %r has no 16-bit product" % (mode,))
     out = _out_or_new(out, shape, odt, a)
-    ldo, stride_o = _strided(out, "out", len(shape), odt)
+    ldo, stride_o = _strided(out, "out", len(shape), odt, dev)
     if c is not None:
         if tuple(c.shape) != shape:
             raise ValueError("c is %s; the output is %s" % (tuple(c.shape), shape))
-        if _strided(c, "c", len(shape), odt) != (ldo, stride_o):
+        if _strided(c, "c", len(shape), odt, dev) != (ldo, stride_o):
             raise ValueError("c must have the strides of out")
-    _same_device(a, b=b, offsets=offsets, c=c, out=out, workspace=workspace, status=status)
-    _req(status, "status", 4, optional=True)
-    wbytes = 0
-    if workspace is not None:
-        _req(workspace, "workspace", 0)
-        wbytes = workspace.nbytes
     if n == 0 or k == 0:
         raise ValueError("n and k must be positive")
-    if out.numel() == 0:
-        return out
-    _check(lib.grouped_gemm_16bit(mode, code, G, _ptr(a) or _ptr(out), lda,
-                                  _ptr(b) or _ptr(out), ldb, stride_b, _ptr(offsets), rows, n, k,
-                                  _ptr(c), _ptr(out), ldo, stride_o, od, _ptr(workspace), wbytes,
-                                  _ptr(status), _stream(a)))
+    optr = out.data_ptr()
+    _check(lib.grouped_gemm_16bit(
+        mode, code, G, a.data_ptr() or optr, lda, b.data_ptr() or optr, ldb, stride_b, off, rows, n,
+        k, None if c is None else c.data_ptr(), optr, ldo, stride_o, od,
+        None if workspace is None else _dense(workspace, "workspace", 0, workspace.dtype, dev),
+        0 if workspace is None else workspace.nbytes,
+        None if status is None else _dense(status, "status", 4, status.dtype, dev),
+        _stream(a)) if optr else 0)
     return out
 
 
@@ -862,36 +877,29 @@ def grouped_lora_gemm_16bit(x, w, lora_a, lora_b, offsets, adapter, scale, out=N
     import torch
     lib = load_library()
     code, od, odt = _types_16bit(x, "x", out_dtype, out)
-    ldx, _ = _strided(x, "x", 2, x.dtype)
-    ldw, _ = _strided(w, "w", 2, x.dtype)
-    (rows, k), n = x.shape, w.shape[0]
+    dt, dev = x.dtype, _device_index(x, "x")
+    ldx, _ = _strided(x, "x", 2, dt, dev)
+    ldw, _ = _strided(w, "w", 2, dt, dev)
+    (rows, k), (n, wk) = x.shape, w.shape
     if lora_a.dim() != 3 or lora_b.dim() != 3:
         raise ValueError("lora_a and lora_b must be 3-D")
-    count, rank = lora_a.shape[0], lora_a.shape[1]
-    if w.shape[1] != k or lora_a.shape[2] != k or tuple(lora_b.shape) != (count, n, rank):
+    count, rank, ak = lora_a.shape
+    if wk != k or ak != k or tuple(lora_b.shape) != (count, n, rank):
         raise ValueError("x %s, w %s, lora_a %s and lora_b %s do not fit" % (
             tuple(x.shape), tuple(w.shape), tuple(lora_a.shape), tuple(lora_b.shape)))
-    _req(offsets, "offsets", 16, torch.int64)
     G = offsets.numel() - 1
-    _req(adapter, "adapter", 4 * G, torch.int32)
-    _req(scale, "scale", 4 * count, torch.float32)
-    _req(lora_a, "lora_a", 0, x.dtype)
-    _req(lora_b, "lora_b", 0, x.dtype)
-    _req(status, "status", 4, optional=True)
     out = _out_or_new(out, (rows, n), odt, x)
-    ldo, _ = _strided(out, "out", 2, odt)
+    ldo, _ = _strided(out, "out", 2, odt, dev)
     if workspace is None:
         workspace = grouped_lora_gemm_16bit_workspace(rows, n, k, rank, x.device)
-    _req(workspace, "workspace", 0)
-    _same_device(x, w=w, lora_a=lora_a, lora_b=lora_b, offsets=offsets, adapter=adapter, scale=scale,
-                 out=out, workspace=workspace, status=status)
-    if rows == 0:
-        return out
-    _check(lib.grouped_lora_gemm_16bit(code, G, _ptr(x), ldx, _ptr(w), ldw, _ptr(lora_a),
-                                       _ptr(lora_b), count, rank, _ptr(offsets), _ptr(adapter),
-                                       _ptr(scale), rows, n, k, _ptr(out), ldo, od, _ptr(workspace),
-                                       workspace.nbytes, _ptr(status),
-                                       _stream(x)))
+    args = (_dense(lora_a, "lora_a", 0, dt, dev), _dense(lora_b, "lora_b", 0, dt, dev), count, rank,
+            _dense(offsets, "offsets", 16, torch.int64, dev),
+            _dense(adapter, "adapter", 4 * G, torch.int32, dev),
+            _dense(scale, "scale", 4 * count, torch.float32, dev), rows, n, k, out.data_ptr(), ldo, od,
+            _dense(workspace, "workspace", 0, workspace.dtype, dev), workspace.nbytes,
+            None if status is None else _dense(status, "status", 4, status.dtype, dev), _stream(x))
+    if rows:
+        _check(lib.grouped_lora_gemm_16bit(code, G, x.data_ptr(), ldx, w.data_ptr(), ldw, *args))
     return out
 
 

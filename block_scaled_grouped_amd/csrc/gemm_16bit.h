@@ -67,6 +67,28 @@ __device__ __forceinline__ void static_for(F&& f) {
   static_for_impl(f, std::make_integer_sequence<int, N>{});
 }
 
+// Division of a < 2^31 by a number that the host knows: m = ceil(2^(31 + s) / d) with
+// 2^s >= d > 2^(s - 1) gives a / d as the high half of m * 2 a, shifted by s.  What
+// stands before a tile's first copy is short calls' latency, and an inlined division is
+// some 30 instructions to fetch.
+struct Div {
+  uint32_t m, s, d;
+};
+inline Div make_div(int64_t d) {
+  Div v{0, 0, (uint32_t)d};
+  while (((int64_t)1 << v.s) < d) ++v.s;
+  v.m = (uint32_t)((((uint64_t)1 << (31 + v.s)) + (uint64_t)d - 1) / (uint64_t)d);
+  return v;
+}
+__device__ __forceinline__ int div_by(int a, const Div& v) {
+  return (int)(__umulhi(v.m, 2u * (uint32_t)a) >> v.s);
+}
+// a / b of small numbers (a < 2^20, b >= 1): the float quotient is off by less than one
+// step of 1 / b at a whole number.
+__device__ __forceinline__ int div_small(int a, int b) {
+  return (int)(((float)a + 0.5f) * __builtin_amdgcn_rcpf((float)b));
+}
+
 struct Args {
   const uint16_t* a;
   const uint16_t* b;
@@ -78,6 +100,7 @@ struct Args {
   uint32_t* status;
   char* ws;  // split workspace or null: no split
   int G, out_f32;
+  Div grid, band;  // workgroups; tiles of kSuperM rows of tiles
   // LORA
   const void* low;         // X A^T of each row's own adapter: [rows_cap, 2 r], high and low
                            // halves of it scaled, or (low_parts: kLowParts, not 1)
@@ -166,6 +189,28 @@ __device__ __forceinline__ int count_tiles(const Args& p, Sched& sm) {
   }
 }
 
+// Position (mt, nt) of tile u of mtiles x ntiles, as super_tile has it; band divides by
+// kSuperM * ntiles.
+__device__ __forceinline__ void place_tile(int u, int mtiles, int ntiles, const Div& band, int& mt,
+                                           int& nt) {
+  static_assert(kSuperM == 4 && kSuperN == 8, "shifts");
+  const int full_rows = mtiles >> 2;
+  int br = full_rows, hgt = mtiles & 3;
+  if (u < full_rows * (4 * ntiles)) {
+    br = div_by(u, band);
+    hgt = 4;
+  }
+  u -= br * (4 * ntiles);
+  const auto by_hgt = [hgt](uint32_t v) {  // 1, 2, 3 or 4
+    return hgt == 3 ? __umulhi(v, 0x55555556u) : v >> (hgt >> 1);
+  };
+  const int bc = (int)by_hgt((uint32_t)u >> 3);
+  u -= bc * (8 * hgt);
+  const int q = (int)by_hgt((uint32_t)u);
+  mt = br * 4 + u - q * hgt;
+  nt = bc * 8 + q;
+}
+
 template <int MODE, int BM, int BN>
 __device__ __forceinline__ Tile find_tile(const Args& p, const Sched& sm, int tile) {
   const int esz = p.out_f32 ? 4 : 2;
@@ -173,8 +218,8 @@ __device__ __forceinline__ Tile find_tile(const Args& p, const Sched& sm, int ti
   int mt, nt;
   if constexpr (MODE == kWgrad) {
     const int g = uni(find_group(sm.pre, p.G, tile));
-    super_tile<kSuperM, kSuperN>(tile - uni(sm.pre[g]), (int)((p.n + BM - 1) / BM),
-                                 (int)((p.k + BN - 1) / BN), mt, nt);
+    place_tile(tile - uni(sm.pre[g]), (int)((p.n + BM - 1) / BM), (int)((p.k + BN - 1) / BN),
+               p.band, mt, nt);
     const int64_t i0 = (int64_t)mt * BM, j0 = (int64_t)nt * BN;
     const int64_t t0 = uni64(sm.off[g]);
     t.a = p.a + t0 * p.lda + i0;
@@ -189,8 +234,8 @@ __device__ __forceinline__ Tile find_tile(const Args& p, const Sched& sm, int ti
     const int g = MODE == kLora ? 0 : uni(find_group(sm.pre, p.G, tile));
     const int64_t first = uni64(sm.off[g]);
     const int64_t m = MODE == kLora ? uni64(sm.off[p.G]) - first : uni64(group_extent(sm.off, g));
-    super_tile<kSuperM, kSuperN>(MODE == kLora ? tile : tile - uni(sm.pre[g]),
-                                 (int)((m + BM - 1) / BM), (int)((p.n + BN - 1) / BN), mt, nt);
+    place_tile(MODE == kLora ? tile : tile - uni(sm.pre[g]), (int)((m + BM - 1) / BM),
+               (int)((p.n + BN - 1) / BN), p.band, mt, nt);
     const int64_t r0 = (int64_t)mt * BM, n0 = (int64_t)nt * BN;
     t.a = p.a + (first + r0) * p.lda;
     t.b = p.b + (MODE == kLora ? 0 : g * p.stride_b) + (MODE == kDgrad ? n0 : n0 * p.ldb);
@@ -706,13 +751,40 @@ struct SplitRecord {
 static_assert(sizeof(SplitRecord) == 32, "records fill the header");
 
 // Parts of a contraction of `stages` stages when `left` tiles are on `grid`
-// workgroups; a part keeps at least `least` stages.
-__host__ __device__ __forceinline__ int split_parts(int grid, int left, int stages, int least) {
+// workgroups; a part keeps at least kLeastStages.
+__host__ __device__ __forceinline__ int split_parts(int grid, int left, int stages) {
   if (left <= 0 || left > kMaxSplitTiles) return 1;
+#ifdef __HIP_DEVICE_COMPILE__
+  int s = div_small(grid, left);
+#else
   int s = grid / left;
+#endif
   if (s > kSplitMax) s = kSplitMax;
-  if (s > stages / least) s = stages / least;
+  if (s > stages / kLeastStages) s = stages / kLeastStages;
   return s < 2 ? 1 : s;
+}
+
+// The rounds of a launch: `full` whole ones, then `left` tiles in nsplit parts each.
+struct Rounds {
+  int full, left, nsplit;
+};
+
+template <int MODE>
+__device__ __forceinline__ Rounds plan_rounds(const Args& p, int total) {
+  Rounds r;
+  r.full = div_by(total, p.grid);
+  r.left = total - r.full * (int)p.grid.d;
+  r.nsplit = 1;
+  if (p.ws != nullptr) {
+    const int64_t kl = MODE == kWgrad ? p.rows_cap : p.k;
+    r.nsplit = split_parts((int)p.grid.d, r.left, (int)((kl + kStageK - 1) / kStageK));
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      int32_t* hdr = reinterpret_cast<int32_t*>(p.ws);
+      hdr[0] = r.nsplit > 1 ? r.left : 0;
+      hdr[1] = r.nsplit;
+    }
+  }
+  return r;
 }
 
 struct Work {
@@ -720,30 +792,21 @@ struct Work {
 };
 
 // The work of a workgroup in a round; tile < 0: none left.
-__device__ __forceinline__ Work take_work(int round, int slot, int total, int nsplit) {
-  const int grid = (int)gridDim.x;
-  const int full = total / grid, left = total - full * grid;
+__device__ __forceinline__ Work take_work(const Args& p, const Rounds& r, int round, int slot) {
   Work k;
   k.part = -1;
   k.nparts = 1;
-  if (nsplit > 1 && round == full) {
-    const bool mine = slot < left * nsplit;
-    k.tile = mine ? full * grid + slot / nsplit : -1;
-    k.part = slot % nsplit;
-    k.nparts = nsplit;
+  k.tile = round * (int)p.grid.d + slot;
+  if (round < r.full) return k;
+  if (r.nsplit > 1 && round == r.full) {
+    const int t = div_small(slot, r.nsplit);
+    k.tile = t < r.left ? round * (int)p.grid.d + t : -1;
+    k.part = slot - t * r.nsplit;
+    k.nparts = r.nsplit;
     return k;
   }
-  k.tile = round * grid + slot;
-  if (k.tile >= total) k.tile = -1;
+  if (round > r.full || slot >= r.left) k.tile = -1;
   return k;
-}
-
-__device__ __forceinline__ void write_split_header(char* ws, int total, int nsplit) {
-  if (ws != nullptr && blockIdx.x == 0 && threadIdx.x == 0) {
-    int32_t* hdr = reinterpret_cast<int32_t*>(ws);
-    hdr[0] = nsplit > 1 ? total % (int)gridDim.x : 0;
-    hdr[1] = nsplit;
-  }
 }
 
 __device__ __forceinline__ void write_split_record(char* ws, int slot, int nsplit, const Tile& t) {
@@ -827,6 +890,13 @@ __global__ __launch_bounds__(kThreads) void split_reduce_kernel(const char* __re
     o.cols = rec.cols;
     store_blocks<F16, 1, 2>(y, o, out_f32, wrow, wcol, lane);
   }
+}
+
+// Workgroups of the second step: at most half of the slots hold split tiles.
+inline unsigned reduce_grid(int slots, int units) {
+  const int64_t waves = (int64_t)(slots / 2) * units, cap = 8 * (int64_t)device_cu_count();
+  const int64_t wgs = (waves + kThreads / 64 - 1) / (kThreads / 64);
+  return (unsigned)(wgs < cap ? wgs : cap);
 }
 
 __device__ __forceinline__ OutTile out_tile(const Args& p, const Tile& t) {

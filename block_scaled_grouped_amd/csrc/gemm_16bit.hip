@@ -189,8 +189,8 @@ struct Form {
   double stage_us, tile_us, reduce_us;
 };
 constexpr Form kForms[4] = {
-    {32, 128, 0.52, 1.5, 4.0}, {64, 128, 0.70, 2.0, 5.0}, {128, 128, 1.14, 3.0, 8.0},
-    {256, 256, 1.37, 5.0, 18.0}};
+    {32, 128, 0.52, 1.5, 4.0}, {64, 128, 0.70, 2.0, 4.5}, {128, 128, 1.14, 3.0, 6.0},
+    {256, 256, 1.37, 5.0, 13.0}};
 
 double expected_us(const Form& f, int mode, const Args& p) {
   const int64_t slots = (f.bm == 256 ? 1 : 2) * (int64_t)device_cu_count();
@@ -210,7 +210,7 @@ double expected_us(const Form& f, int mode, const Args& p) {
   double us = (double)full * ((double)stages * f.stage_us + f.tile_us);
   if (left > 0) {
     const int parts =
-        p.ws == nullptr ? 1 : split_parts((int)slots, (int)left, (int)split_stages, kLeastStages);
+        p.ws == nullptr ? 1 : split_parts((int)slots, (int)left, (int)split_stages);
     us += (double)((stages + parts - 1) / parts) * f.stage_us + f.tile_us +
           (parts > 1 ? f.reduce_us : 0.0);
   }

@@ -189,16 +189,10 @@ __global__ __launch_bounds__(kThreads) void large_kernel(Args p) {
   __shared__ int ids[MODE == kLora ? BM : 1];
   const uint32_t lds = lds_offset(ring);
   const int total = count_tiles<MODE, BM, BN>(p, sm);
-  const int grid = (int)gridDim.x, left = total % grid;
-  const int nsplit =
-      p.ws == nullptr
-          ? 1
-          : split_parts(grid, left,
-                        (int)(((MODE == kWgrad ? p.rows_cap : p.k) + kStageK - 1) / kStageK),
-                        kLeastStages);
-  write_split_header(p.ws, total, nsplit);
+  const Rounds rounds = plan_rounds<MODE>(p, total);
+  const int nsplit = rounds.nsplit;
   const int slot = xcd_slot();
-  Work work = take_work(0, slot, total, nsplit);
+  Work work = take_work(p, rounds, 0, slot);
   if (work.tile < 0) return;
   Tile t = find_tile<MODE, BM, BN>(p, sm, uni(work.tile));
   if (work.part >= 0) narrow_tile<MODE>(t, uni(work.part), nsplit);
@@ -225,7 +219,7 @@ __global__ __launch_bounds__(kThreads) void large_kernel(Args p) {
     // every copy has landed and no wave still reads a buffer before the next
     // tile's first copies
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    const Work next = take_work(round, slot, total, nsplit);
+    const Work next = take_work(p, rounds, round, slot);
     Tile tn = t;
     if (next.tile >= 0) {
       tn = find_tile<MODE, BM, BN>(p, sm, uni(next.tile));
@@ -251,20 +245,23 @@ __global__ __launch_bounds__(kThreads) void large_kernel(Args p) {
 }
 
 template <int MODE, bool F16>
-hipError_t launch(const Args& p, hipStream_t stream) {
+hipError_t launch(Args p, hipStream_t stream) {
   int64_t bound;
   if (MODE == kWgrad) bound = (int64_t)p.G * ((p.n + BM - 1) / BM) * ((p.k + BN - 1) / BN);
   else bound = ((p.rows_cap + BM - 1) / BM + (MODE == kLora ? 0 : p.G)) * ((p.n + BN - 1) / BN);
   const int cus = device_cu_count();
   const int64_t kl = MODE == kWgrad ? p.rows_cap : p.k;
-  const int parts = p.ws != nullptr ? split_parts(cus, 1, (int)((kl + kStageK - 1) / kStageK), kLeastStages) : 1;
+  const int parts = p.ws != nullptr ? split_parts(cus, 1, (int)((kl + kStageK - 1) / kStageK)) : 1;
   int64_t grid = bound * parts < cus ? bound * parts : cus;
   if (grid <= 0) return hipSuccess;
+  p.grid = make_div(grid);
+  p.band = make_div(kSuperM * (((MODE == kWgrad ? p.k : p.n) + BN - 1) / BN));
   hipLaunchKernelGGL((large_kernel<MODE, F16>), dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || parts < 2) return e;
-  hipLaunchKernelGGL((split_reduce_kernel<F16, BM, BN, 2, 8, 8>), dim3((unsigned)cus),
-                     dim3(kThreads), 0, stream, p.ws, p.out, p.c, p.ldo, p.out_f32);
+  hipLaunchKernelGGL((split_reduce_kernel<F16, BM, BN, 2, 8, 8>),
+                     dim3(reduce_grid((int)grid, BM * BN / 512)), dim3(kThreads), 0, stream, p.ws,
+                     p.out, p.c, p.ldo, p.out_f32);
   return hipGetLastError();
 }
 

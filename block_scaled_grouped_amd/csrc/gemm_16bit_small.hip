@@ -98,16 +98,11 @@ __global__ __launch_bounds__(kThreads, kWgPerCu) void small_kernel(Args p) {
   __shared__ int ids[MODE == kLora ? BM : 1];
   const uint32_t lds = lds_offset(ring);
   const int total = count_tiles<MODE, BM, BN>(p, sm);
-  const int grid = (int)gridDim.x, left = total % grid;
-  const int nsplit =
-      p.ws == nullptr
-          ? 1
-          : split_parts(grid, left,
-                        (int)(((MODE == kWgrad ? p.rows_cap : p.k) + kStageK - 1) / kStageK), kLeastStages);
-  write_split_header(p.ws, total, nsplit);
+  const Rounds rounds = plan_rounds<MODE>(p, total);
+  const int nsplit = rounds.nsplit;
   const int slot = xcd_slot();
   for (int round = 0;; ++round) {
-    const Work work = take_work(round, slot, total, nsplit);
+    const Work work = take_work(p, rounds, round, slot);
     if (work.tile < 0) break;
     Tile t = find_tile<MODE, BM, BN>(p, sm, uni(work.tile));
     if (work.part >= 0) narrow_tile<MODE>(t, uni(work.part), nsplit);
@@ -141,21 +136,23 @@ __global__ __launch_bounds__(kThreads, kWgPerCu) void small_kernel(Args p) {
 }
 
 template <int MODE, bool F16, int BM>
-hipError_t launch(const Args& p, hipStream_t stream) {
+hipError_t launch(Args p, hipStream_t stream) {
   int64_t bound;
   if (MODE == kWgrad) bound = (int64_t)p.G * ((p.n + BM - 1) / BM) * ((p.k + BN - 1) / BN);
   else bound = ((p.rows_cap + BM - 1) / BM + (MODE == kLora ? 0 : p.G)) * ((p.n + BN - 1) / BN);
   const int cap = kWgPerCu * device_cu_count();
   const int64_t kl = MODE == kWgrad ? p.rows_cap : p.k;
-  const int parts = p.ws != nullptr ? split_parts(cap, 1, (int)((kl + kStageK - 1) / kStageK), kLeastStages) : 1;
+  const int parts = p.ws != nullptr ? split_parts(cap, 1, (int)((kl + kStageK - 1) / kStageK)) : 1;
   const int64_t grid = bound * parts < cap ? bound * parts : cap;
   if (grid <= 0) return hipSuccess;
+  p.grid = make_div(grid);
+  p.band = make_div(kSuperM * (((MODE == kWgrad ? p.k : p.n) + BN - 1) / BN));
   hipLaunchKernelGGL((small_kernel<MODE, F16, BM>), dim3((unsigned)grid), dim3(kThreads), 0, stream,
                      p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || parts < 2) return e;
   hipLaunchKernelGGL((split_reduce_kernel<F16, BM, BN, kWavesN<BM>, kMI<BM>, kNJ<BM>>),
-                     dim3((unsigned)device_cu_count()), dim3(kThreads), 0, stream, p.ws, p.out, p.c,
+                     dim3(reduce_grid((int)grid, BM * BN / 512)), dim3(kThreads), 0, stream, p.ws, p.out, p.c,
                      p.ldo, p.out_f32);
   return hipGetLastError();
 }
