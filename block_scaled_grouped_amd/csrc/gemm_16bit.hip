@@ -24,7 +24,7 @@ constexpr int kLowRows = 32;
 constexpr int64_t kFewRows = 1024;  // 32 blocks of rows leave compute units idle
 
 template <bool F16, int NB>  // 16 NB <= 64 rank columns a workgroup
-__global__ __launch_bounds__(kLowThreads) void lora_low_kernel(Args p, const uint16_t* down,
+__global__ __launch_bounds__(kLowThreads, NB == 1 ? 4 : 2) void lora_low_kernel(Args p, const uint16_t* down,
                                                                int turns) {
   __shared__ int64_t off[kMaxGroups + 1];
   __shared__ int adapters[kMaxGroups];
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(kLowThreads) void lora_low_kernel(Args p, const uin
         for (int b = 0; b < NB; ++b) acc[i][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
       }
       // kRuns of the wave's runs are loaded before the first is used
-      constexpr int kRuns = NB == 4 ? 2 : 4;
+      constexpr int kRuns = NB == 1 ? 3 : NB == 2 ? 4 : 2;
       const int end = 64 * run1 < k ? 64 * run1 : k;
       for (int k0 = 64 * (run0 + w); k0 < end; k0 += 64 * kLowWaves * kRuns) {
         v4i fx[2 * kRuns][2], fd[2 * kRuns][NB];
