@@ -899,6 +899,27 @@ inline unsigned reduce_grid(int slots, int units) {
   return (unsigned)(wgs < cap ? wgs : cap);
 }
 
+// Grid of a launch with `slots` workgroups resident (0: nothing to do), and the numbers
+// that the kernel divides by.  Where the host knows that no tile is split it leaves the
+// workspace out, and the second step is not launched: contractions too short for two
+// parts, and weight gradients (whose tiles it can count) whose rounds come out even.
+template <int MODE, int BM, int BN>
+int prepare_launch(Args& p, int slots) {
+  const int64_t ntn = ((MODE == kWgrad ? p.k : p.n) + BN - 1) / BN;
+  const int64_t bound =
+      MODE == kWgrad ? p.G * ((p.n + BM - 1) / BM) * ntn
+                     : ((p.rows_cap + BM - 1) / BM + (MODE == kLora ? 0 : p.G)) * ntn;
+  const int stages = (int)(((MODE == kWgrad ? p.rows_cap : p.k) + kStageK - 1) / kStageK);
+  const int most = p.ws != nullptr ? split_parts(slots, 1, stages) : 1;
+  const int grid = (int)(bound * most < slots ? bound * most : slots);
+  if (grid <= 0) return 0;
+  if (most < 2 || (MODE == kWgrad && split_parts(grid, (int)(bound % grid), stages) < 2))
+    p.ws = nullptr;
+  p.grid = make_div(grid);
+  p.band = make_div(kSuperM * ntn);
+  return grid;
+}
+
 __device__ __forceinline__ OutTile out_tile(const Args& p, const Tile& t) {
   OutTile o;
   o.out = p.out + t.out_off;

@@ -246,22 +246,14 @@ __global__ __launch_bounds__(kThreads) void large_kernel(Args p) {
 
 template <int MODE, bool F16>
 hipError_t launch(Args p, hipStream_t stream) {
-  int64_t bound;
-  if (MODE == kWgrad) bound = (int64_t)p.G * ((p.n + BM - 1) / BM) * ((p.k + BN - 1) / BN);
-  else bound = ((p.rows_cap + BM - 1) / BM + (MODE == kLora ? 0 : p.G)) * ((p.n + BN - 1) / BN);
-  const int cus = device_cu_count();
-  const int64_t kl = MODE == kWgrad ? p.rows_cap : p.k;
-  const int parts = p.ws != nullptr ? split_parts(cus, 1, (int)((kl + kStageK - 1) / kStageK)) : 1;
-  int64_t grid = bound * parts < cus ? bound * parts : cus;
-  if (grid <= 0) return hipSuccess;
-  p.grid = make_div(grid);
-  p.band = make_div(kSuperM * (((MODE == kWgrad ? p.k : p.n) + BN - 1) / BN));
-  hipLaunchKernelGGL((large_kernel<MODE, F16>), dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || parts < 2) return e;
+  const int grid = prepare_launch<MODE, BM, BN>(p, device_cu_count());
+  if (grid == 0) return hipSuccess;
+  hipLaunchKernelGGL((large_kernel<MODE, F16>), dim3(grid), dim3(kThreads), 0, stream, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.ws == nullptr) return e;
   hipLaunchKernelGGL((split_reduce_kernel<F16, BM, BN, 2, 8, 8>),
-                     dim3(reduce_grid((int)grid, BM * BN / 512)), dim3(kThreads), 0, stream, p.ws,
-                     p.out, p.c, p.ldo, p.out_f32);
+                     dim3(reduce_grid(grid, BM * BN / 512)), dim3(kThreads), 0, stream, p.ws, p.out,
+                     p.c, p.ldo, p.out_f32);
   return hipGetLastError();
 }
 

@@ -137,23 +137,14 @@ __global__ __launch_bounds__(kThreads, kWgPerCu) void small_kernel(Args p) {
 
 template <int MODE, bool F16, int BM>
 hipError_t launch(Args p, hipStream_t stream) {
-  int64_t bound;
-  if (MODE == kWgrad) bound = (int64_t)p.G * ((p.n + BM - 1) / BM) * ((p.k + BN - 1) / BN);
-  else bound = ((p.rows_cap + BM - 1) / BM + (MODE == kLora ? 0 : p.G)) * ((p.n + BN - 1) / BN);
-  const int cap = kWgPerCu * device_cu_count();
-  const int64_t kl = MODE == kWgrad ? p.rows_cap : p.k;
-  const int parts = p.ws != nullptr ? split_parts(cap, 1, (int)((kl + kStageK - 1) / kStageK)) : 1;
-  const int64_t grid = bound * parts < cap ? bound * parts : cap;
-  if (grid <= 0) return hipSuccess;
-  p.grid = make_div(grid);
-  p.band = make_div(kSuperM * (((MODE == kWgrad ? p.k : p.n) + BN - 1) / BN));
-  hipLaunchKernelGGL((small_kernel<MODE, F16, BM>), dim3((unsigned)grid), dim3(kThreads), 0, stream,
-                     p);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || parts < 2) return e;
+  const int grid = prepare_launch<MODE, BM, BN>(p, kWgPerCu * device_cu_count());
+  if (grid == 0) return hipSuccess;
+  hipLaunchKernelGGL((small_kernel<MODE, F16, BM>), dim3(grid), dim3(kThreads), 0, stream, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.ws == nullptr) return e;
   hipLaunchKernelGGL((split_reduce_kernel<F16, BM, BN, kWavesN<BM>, kMI<BM>, kNJ<BM>>),
-                     dim3(reduce_grid((int)grid, BM * BN / 512)), dim3(kThreads), 0, stream, p.ws, p.out, p.c,
-                     p.ldo, p.out_f32);
+                     dim3(reduce_grid(grid, BM * BN / 512)), dim3(kThreads), 0, stream, p.ws, p.out,
+                     p.c, p.ldo, p.out_f32);
   return hipGetLastError();
 }
 
