@@ -38,6 +38,17 @@ __device__ __forceinline__ uint32_t f32_to_bf16_rne(float f) {
   return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
 }
 
+// Two floats rounded to nearest even as a pair of fp16 (F16) or bf16 values.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (F16) {
+    typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){lo, hi}, v2h));
+  } else {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){lo, hi}, v2bf));
+  }
+}
+
 // 16-byte load of an input that is read once (the quantizers' bf16 inputs):
 // non-temporal, so the stream does not displace cached lines on its way.
 __device__ __forceinline__ uint4 load_stream16(const void* p) {

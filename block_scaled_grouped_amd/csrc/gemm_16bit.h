@@ -326,6 +326,10 @@ struct Side {
         off[i] = c * 8 < rows ? k * ld2 + c * 16 : kDmaOutOfRange;
       }
     }
+    // a buffer instruction has to be five wait states later than the vector
+    // instructions that wrote its descriptor, which the compiler does not know of
+    // instructions in asm
+    asm volatile("s_nop 4" : "+s"(base), "+s"(range), "+s"(ld2));
   }
 
   // Says again that what is uniform is (it is carried from one tile to the next).

@@ -12,7 +12,6 @@
 // block, then the blocks' sums in one order), so a norm repeats bit for bit.
 // The multiply-adds are far from the vector units' 64-bit rate.
 #include "bsg_internal.h"
-#include "store_tile.h"
 
 namespace bsg {
 

@@ -23,19 +23,7 @@ namespace bsg {
 //   Otherwise: one store per element.
 constexpr uint32_t kDropped = 0xfffffff0u;
 
-// Two floats rounded to nearest even as a pair of fp16 (F16) or bf16 values.
-template <bool F16>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
-  if constexpr (F16) {
-    typedef _Float16 v2h __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){lo, hi}, v2h));
-  } else {
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){lo, hi}, v2bf));
-  }
-}
-
-// F16 (with WIDE): the 16-bit output is fp16 instead of bf16.
-template <bool WIDE, bool F32, bool F16 = false>
+template <bool WIDE, bool F32>
 __device__ __forceinline__ void store_block(const v16f& acc, __amdgpu_buffer_rsrc_t ro, int ldc,
                                             int row, int col0, int h, int out_cols) {
   constexpr int esz = F32 ? 4 : 2;
@@ -46,7 +34,8 @@ __device__ __forceinline__ void store_block(const v16f& acc, __amdgpu_buffer_rsr
     for (int q = 0; q < 4; ++q) {
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        d[2 * q + e] = (int)pack16<F16>(acc[4 * q + 2 * e], acc[4 * q + 2 * e + 1]);
+        d[2 * q + e] = __builtin_bit_cast(
+            int, __builtin_convertvector((v2f){acc[4 * q + 2 * e], acc[4 * q + 2 * e + 1]}, v2bf));
     }
     // lane (r, 0) keeps d[0..3] and receives lane (r, 1)'s d[0..3] as d[4..7];
     // lane (r, 1) receives lane (r, 0)'s d[4..7] as d[0..3] and keeps d[4..7]
