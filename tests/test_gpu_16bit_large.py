@@ -197,3 +197,63 @@ def test_rows_20_bits_apart():
     bsg.grouped_gemm_16bit(bsg.BSG_DGRAD_NN, a, w, off, out=out)
     ref, mag = _reference(bsg.BSG_DGRAD_NN, a, w, o)
     _assert_close(out, ref, mag, k)
+
+
+def test_adapters_of_few_rows_with_a_large_intermediate():
+    """x A^T past fp16's largest value where its contraction is spread over workgroups (few rows, k >= 1024)."""
+    dev = device()
+    x = torch.full((3, 1024), 100.0, dtype=torch.float16, device=dev)
+    w = torch.zeros((8, 1024), dtype=torch.float16, device=dev)
+    A = torch.full((1, 8, 1024), 0.9375, dtype=torch.float16, device=dev)      # x A^T = 96000
+    B = torch.full((1, 8, 8), 2.0 ** -10, dtype=torch.float16, device=dev)
+    y = bsg.grouped_lora_gemm_16bit(x, w, A, B, torch.tensor([0, 3], device=dev),
+                                    torch.zeros(1, dtype=torch.int32, device=dev), torch.ones(1, device=dev),
+                                    out_dtype=bsg.BSG_OUT_F32)
+    assert torch.equal(y, torch.full_like(y, 96000 * 8 * 2.0 ** -10))
+
+
+@pytest.mark.parametrize("rows", [1, 16, 33, 64, 100, 1024, 1025])
+def test_adapters_from_one_row_to_more_than_a_thousand(rows):
+    """The first product's forms meet at 1024 rows and at k = 1024."""
+    gen = torch.Generator().manual_seed(rows)
+    n, r = 136, 40
+    ids = [i % 3 - 1 for i in range(min(rows, 7))]
+    cuts = sorted(torch.randperm(rows + 1, generator=gen)[:len(ids) - 1].tolist())
+    lengths = [b - a for a, b in zip([0] + cuts, cuts + [rows])]
+    o, off = _offsets(lengths)
+    for k in (1016, 1024, 1544):
+        x, w = _rand(gen, (rows, k), torch.bfloat16), _rand(gen, (n, k), torch.bfloat16, std=0.1)
+        A = _rand(gen, (2, r, k), torch.bfloat16, std=0.1)
+        B = _rand(gen, (2, n, r), torch.bfloat16, std=0.5)
+        scale = (torch.rand(2, generator=gen) + 0.5).to(x.device)
+        y = bsg.grouped_lora_gemm_16bit(x, w, A, B, off, torch.tensor(ids, dtype=torch.int32, device=x.device),
+                                        scale, out_dtype=bsg.BSG_OUT_F32)
+        ref, tol = _lora_reference(x, w, A, B, o, ids, scale, torch.bfloat16)
+        err = (y.cpu().to(F64) - ref).abs()
+        bound = tol + 2.0 ** -24 * (ref.abs() + tol) + TINY[torch.float32]
+        assert bool((err <= bound).all()), float((err / bound).max())
+
+
+@pytest.mark.parametrize("mode", [bsg.BSG_FPROP_TN, bsg.BSG_DGRAD_NN, bsg.BSG_WGRAD_NT])
+def test_two_streams_with_a_workspace_each(mode):
+    """Calls on two streams at once, each with its own workspace, give what they give alone."""
+    dt = torch.bfloat16
+    o, off = _offsets([130, 0, 700, 60])
+    T, n, k = o[-1], 520, 1544
+    ops = []
+    for i in range(2):
+        a = _dev_rand(60 + i, (T, n if mode == bsg.BSG_WGRAD_NT else k), dt)
+        b = _dev_rand(70 + i, (T, k) if mode == bsg.BSG_WGRAD_NT else
+                      (4, n, k) if mode == bsg.BSG_FPROP_TN else (4, k, n), dt)
+        work = bsg.gemm_workspace()
+        ops.append((a, b, work, bsg.grouped_gemm_16bit(mode, a, b, off, workspace=work)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ops]
+    got = []
+    for _ in range(4):
+        for s, (a, b, work, _) in zip(streams, ops):
+            with torch.cuda.stream(s):
+                got.append(bsg.grouped_gemm_16bit(mode, a, b, off, workspace=work))
+    torch.cuda.synchronize()
+    for i, y in enumerate(got):
+        assert torch.equal(y, ops[i % 2][3])
