@@ -735,8 +735,8 @@ __device__ __forceinline__ void store_blocks(const v4f (&acc)[MI][NJ], const Out
 
 // With T tiles on a grid of P workgroups the last round holds L = T mod P tiles
 // (all of them when T < P).  Given a workspace, each of those is split along the
-// contraction into S <= min(P / L, kSplitMax) parts of whole stages; workgroup
-// L s' + s of that round takes part s of its tile s' and writes its float32
+// contraction into S <= min(P / L, kSplitMax) parts of whole stages; place
+// S t + s of that round takes part s of its tile t and writes its float32
 // accumulators to the workspace, and a second kernel on the same stream adds each
 // tile's parts in the order s = 0, 1, .. and stores the tile, so the result does
 // not depend on which part ended first.
@@ -769,11 +769,16 @@ __host__ __device__ __forceinline__ int split_parts(int grid, int left, int stag
 }
 
 // The rounds of a launch: `full` whole ones, then `left` tiles in nsplit parts each.
+// slot: this workgroup's place in the whole rounds; last_slot: in the last one.  SPREAD
+// deals its places, if they are fewer, out over all XCDs: the slots of an XCD are
+// consecutive, so that 256 of 512 would lie on four of the eight, twice on each of their
+// compute units.  (70 calls of random sizes: 2 % less time in the small form; the large
+// one, with one workgroup a compute unit, loses 1 % in shared panels and does without.)
 struct Rounds {
-  int full, left, nsplit;
+  int full, left, nsplit, slot, last_slot;
 };
 
-template <int MODE>
+template <int MODE, bool SPREAD>
 __device__ __forceinline__ Rounds plan_rounds(const Args& p, int total) {
   Rounds r;
   r.full = div_by(total, p.grid);
@@ -788,28 +793,40 @@ __device__ __forceinline__ Rounds plan_rounds(const Args& p, int total) {
       hdr[1] = r.nsplit;
     }
   }
+  r.slot = xcd_slot();
+  r.last_slot = r.slot;
+  if constexpr (SPREAD) {
+    const int b = (int)blockIdx.x, places = (r.left * r.nsplit + kXcds - 1) / kXcds;
+    r.last_slot = b;
+    if (places * kXcds <= (int)p.grid.d && b < places * kXcds)
+      r.last_slot = b % kXcds * places + b / kXcds;
+  }
   return r;
 }
 
 struct Work {
   int tile, part, nparts;  // part < 0: a whole tile
+  int slot;                // of a part
 };
 
 // The work of a workgroup in a round; tile < 0: none left.
-__device__ __forceinline__ Work take_work(const Args& p, const Rounds& r, int round, int slot) {
+__device__ __forceinline__ Work take_work(const Args& p, const Rounds& r, int round) {
   Work k;
   k.part = -1;
   k.nparts = 1;
-  k.tile = round * (int)p.grid.d + slot;
-  if (round < r.full) return k;
-  if (r.nsplit > 1 && round == r.full) {
-    const int t = div_small(slot, r.nsplit);
-    k.tile = t < r.left ? round * (int)p.grid.d + t : -1;
-    k.part = slot - t * r.nsplit;
+  k.slot = r.last_slot;
+  if (round < r.full) {
+    k.tile = round * (int)p.grid.d + r.slot;
+  } else if (round > r.full || r.last_slot >= r.left * r.nsplit) {
+    k.tile = -1;
+  } else if (r.nsplit > 1) {
+    const int t = div_small(r.last_slot, r.nsplit);
+    k.tile = round * (int)p.grid.d + t;
+    k.part = r.last_slot - t * r.nsplit;
     k.nparts = r.nsplit;
-    return k;
+  } else {
+    k.tile = round * (int)p.grid.d + r.last_slot;
   }
-  if (round > r.full || slot >= r.left) k.tile = -1;
   return k;
 }
 

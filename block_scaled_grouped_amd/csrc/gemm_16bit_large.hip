@@ -196,10 +196,9 @@ __global__ __launch_bounds__(kThreads) void large_kernel(Args p) {
   __shared__ int ids[MODE == kLora ? BM : 1];
   const uint32_t lds = lds_offset(ring);
   const int total = count_tiles<MODE, BM, BN>(p, sm);
-  const Rounds rounds = plan_rounds<MODE>(p, total);
+  const Rounds rounds = plan_rounds<MODE, false>(p, total);
   const int nsplit = rounds.nsplit;
-  const int slot = xcd_slot();
-  Work work = take_work(p, rounds, 0, slot);
+  Work work = take_work(p, rounds, 0);
   if (work.tile < 0) return;
   Tile t = find_tile<MODE, BM, BN>(p, sm, uni(work.tile));
   if (work.part >= 0) narrow_tile<MODE>(t, uni(work.part), nsplit);
@@ -226,7 +225,7 @@ __global__ __launch_bounds__(kThreads) void large_kernel(Args p) {
     // every copy has landed and no wave still reads a buffer before the next
     // tile's first copies
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    const Work next = take_work(p, rounds, round, slot);
+    const Work next = take_work(p, rounds, round);
     Tile tn = t;
     if (next.tile >= 0) {
       tn = find_tile<MODE, BM, BN>(p, sm, uni(next.tile));
@@ -238,9 +237,10 @@ __global__ __launch_bounds__(kThreads) void large_kernel(Args p) {
       __syncthreads();  // ids are read before the next tile's
     }
     if (work.part >= 0) {
-      write_split_record(p.ws, slot, nsplit, t);
-      store_part<8, 8>(reinterpret_cast<float*>(p.ws + kWsHeader + (int64_t)slot * kPartBytes), acc,
-                       w, lane, wrow, t.a_rows);
+      write_split_record(p.ws, work.slot, nsplit, t);
+      store_part<8, 8>(
+          reinterpret_cast<float*>(p.ws + kWsHeader + (int64_t)work.slot * kPartBytes), acc, w,
+          lane, wrow, t.a_rows);
     } else {
       store_blocks<F16, 8, 8>(acc, out_tile(p, t), p.out_f32, wrow, wcol, lane);
     }

@@ -98,11 +98,10 @@ __global__ __launch_bounds__(kThreads, kWgPerCu) void small_kernel(Args p) {
   __shared__ int ids[MODE == kLora ? BM : 1];
   const uint32_t lds = lds_offset(ring);
   const int total = count_tiles<MODE, BM, BN>(p, sm);
-  const Rounds rounds = plan_rounds<MODE>(p, total);
+  const Rounds rounds = plan_rounds<MODE, true>(p, total);
   const int nsplit = rounds.nsplit;
-  const int slot = xcd_slot();
   for (int round = 0;; ++round) {
-    const Work work = take_work(p, rounds, round, slot);
+    const Work work = take_work(p, rounds, round);
     if (work.tile < 0) break;
     Tile t = find_tile<MODE, BM, BN>(p, sm, uni(work.tile));
     if (work.part >= 0) narrow_tile<MODE>(t, uni(work.part), nsplit);
@@ -125,9 +124,9 @@ __global__ __launch_bounds__(kThreads, kWgPerCu) void small_kernel(Args p) {
       __syncthreads();  // ids are read before the next tile's
     }
     if (work.part >= 0) {
-      write_split_record(p.ws, slot, nsplit, t);
+      write_split_record(p.ws, work.slot, nsplit, t);
       store_part<MI, NJ>(
-          reinterpret_cast<float*>(p.ws + kWsHeader + (int64_t)slot * kPartBytes<BM>), acc, w, lane,
+          reinterpret_cast<float*>(p.ws + kWsHeader + (int64_t)work.slot * kPartBytes<BM>), acc, w, lane,
           wrow, t.a_rows);
     } else {
       store_blocks<F16, MI, NJ>(acc, out_tile(p, t), p.out_f32, wrow, wcol, lane);
