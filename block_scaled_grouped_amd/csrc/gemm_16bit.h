@@ -53,6 +53,8 @@ constexpr int kStageK = 64;       // contraction indexes per LDS stage
 constexpr int kThreads = 256;
 constexpr int kSuperM = 4, kSuperN = 8;  // tile block one XCD works on
 constexpr int kLowParts = 4;             // of the adapters' first product, where it is split
+constexpr int kLowValues = 2;            // 16-bit values that carry a sum of it to the second
+constexpr int kLowChunk = 64;            // rank columns that share a row's power of two
 
 enum Mode { kFprop = 0, kWgrad = 1, kDgrad = 2, kLora = 3 };
 template <int MODE> constexpr bool kColsA = MODE == kWgrad;
@@ -102,9 +104,11 @@ struct Args {
   int G, out_f32;
   Div grid, band;  // workgroups; tiles of kSuperM rows of tiles
   // LORA
-  const void* low;         // X A^T of each row's own adapter: [rows_cap, 2 r], high and low
-                           // halves of it scaled, or (low_parts: kLowParts, not 1)
+  const void* low;         // X A^T of each row's own adapter: 16-bit [rows_cap, kLowValues, r],
+                           // the values that carry it, or (low_parts: kLowParts, not 1)
                            // float32 [kLowParts, rows_cap, r], parts of its contraction
+  const float* low_power;  // fp16, low_parts 1: [rows_cap, r / kLowChunk rounded up], the power
+                           // of two to multiply the values of a row's chunk by
   const float* scale;      // [adapters]
   int low_parts;
   const uint16_t* up;      // [adapters, n, r]
@@ -440,66 +444,121 @@ __device__ __forceinline__ float to_f32(uint32_t b) {
   return F16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)b) : bf16_to_f32(b & 0xffffu);
 }
 
-// s as the sum of two 16-bit values: the nearest one and the nearest to what is
-// left (22 or 16 bits of s together).  The first is kept finite, so that a value
-// past the type's range turns into an infinity in the second and not into the
-// difference of two.
-template <bool F16>
-__device__ __forceinline__ void split16(float s, uint32_t& top, uint32_t& rest) {
-  constexpr float kMax = F16 ? 65504.0f : 3.3895313892515355e38f;
-  float c = s;
-  if (s > kMax) c = kMax;
-  if (s < -kMax) c = -kMax;
-  top = pack16<F16>(c, c) & 0xffffu;
-  const float left = s - to_f32<F16>(top);
-  rest = pack16<F16>(left, left) & 0xffffu;
+// The sums x A^T go into the second product as 16-bit values whose sum they are.  A bf16
+// value has float32's range, so the values are the nearest one to the sum and the nearest to
+// what is left.  An fp16 value has 40 binades with its subnormals, so
+//   - the rank columns of a row's chunk are divided by a power of two that puts the largest
+//     into [2^14, 2^15), and the products multiplied by it again, and
+//   - what the first value leaves is held times 2^11 and summed apart, so that it reaches
+//     below fp16's smallest values.
+// Both are exact.  What the values hold of a sum: 16 bits (bf16) or 22 (fp16, of one that is
+// no less than 2^-28 of the largest in its row's chunk).
+//
+// low_scales: multiplies by `down` before and `up` after, for a chunk's largest magnitude m
+// (zero, infinite and NaN too).
+struct LowScales {
+  float down, up;
+};
+__device__ __forceinline__ LowScales low_scales(float m) {
+  int e = (int)(__float_as_uint(m) >> 23 & 255u);
+  if (e < 15) e = 15;  // both powers stay normal numbers
+  return {__uint_as_float((uint32_t)(268 - e) << 23), __uint_as_float((uint32_t)(e - 14) << 23)};
 }
 
-// A lane's fragments (high and low halves) of a 16-row block's low values: `row` of
-// the wave's rows, rank columns at byte `at` / 2 and on (an offset past every range:
-// zeros).  rows: live rows from the wave's first on.
+constexpr float kRestScale = 2048.0f;  // fp16: of the values after the first
+
+// Two sums, in place of the low and the high half of each word.  A value that others follow
+// is kept finite, so that an infinity stays one in the last and does not turn into the
+// difference of two (a NaN passes the same way: the median of a NaN is a number).
 template <bool F16>
-__device__ __forceinline__ void load_low(const Args& p, int64_t first, int rows, int row,
-                                         uint32_t at, float scale, v4i& top, v4i& rest) {
+__device__ __forceinline__ void split_low(float a, float b, uint32_t (&word)[kLowValues]) {
+  constexpr float kMax = F16 ? 65504.0f : 3.3895313892515355e38f;
+#pragma unroll
+  for (int h = 0; h < kLowValues - 1; ++h) {
+    word[h] = pack16<F16>(__builtin_amdgcn_fmed3f(a, -kMax, kMax),
+                          __builtin_amdgcn_fmed3f(b, -kMax, kMax));
+    a -= to_f32<F16>(word[h] & 0xffffu);
+    b -= to_f32<F16>(word[h] >> 16);
+    if (F16 && h == 0) {
+      a *= kRestScale;
+      b *= kRestScale;
+    }
+  }
+  word[kLowValues - 1] = pack16<F16>(a, b);
+}
+
+// A lane's fragments of a 16-row block's low values: `row` of the wave's rows, 32 rank columns
+// and 32 more, each from byte 2 * column = at[c] on (an offset past every range: zeros), all
+// of the chunk that begins at column k.  Returns what the products have to be multiplied by.
+// rows: live rows from the wave's first on.
+template <bool F16>
+__device__ __forceinline__ float load_low(const Args& p, int64_t first, int rows, int row, int k,
+                                          const uint32_t (&at)[2], v4i (&v)[2][kLowValues]) {
   const int rank = p.r;
   if (p.low_parts == 1) {
-    const __amdgpu_buffer_rsrc_t low = make_rsrc(
-        static_cast<const uint16_t*>(p.low) + first * 2 * rank, rows > 0 ? rows * 4 * rank : 0);
-    top = __builtin_amdgcn_raw_buffer_load_b128(low, (int)(at + row * 4 * rank), 0, 0);
-    rest = __builtin_amdgcn_raw_buffer_load_b128(low, (int)(at + row * 4 * rank + 2 * rank), 0, 0);
-    return;
-  }
-  const uint32_t o = at == (uint32_t)kDmaOutOfRange ? at : 2 * at + row * 4 * rank;
-  v4i v[kLowParts][2];
-#pragma unroll
-  for (int part = 0; part < kLowParts; ++part) {
+    const int line = 2 * kLowValues * rank;
     const __amdgpu_buffer_rsrc_t low =
-        make_rsrc(static_cast<const float*>(p.low) + (part * p.rows_cap + first) * rank,
-                  rows > 0 ? rows * 4 * rank : 0);
+        make_rsrc(static_cast<const uint16_t*>(p.low) + first * kLowValues * rank,
+                  rows > 0 ? rows * line : 0);
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-      v[part][b] = __builtin_amdgcn_raw_buffer_load_b128(low, (int)(o + 16 * b), 0, 0);
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int h = 0; h < kLowValues; ++h)
+        v[c][h] = __builtin_amdgcn_raw_buffer_load_b128(
+            low, (int)(at[c] + row * line + 2 * h * rank), 0, 0);
+    if constexpr (!F16) return 1.0f;
+    const int chunks = (rank + kLowChunk - 1) / kLowChunk;
+    const __amdgpu_buffer_rsrc_t power =
+        make_rsrc(p.low_power + first * chunks, rows > 0 ? rows * chunks * 4 : 0);
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+        power, 4 * (row * chunks + k / kLowChunk), 0, 0));
   }
-  float s[8];
+  float s[2][8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    s[e] = __int_as_float(v[0][e >> 2][e & 3]);
+  for (int c = 0; c < 2; ++c) {
+    const uint32_t o = at[c] == (uint32_t)kDmaOutOfRange ? at[c] : 2 * at[c] + row * 4 * rank;
+    v4i part[kLowParts][2];
 #pragma unroll
-    for (int part = 1; part < kLowParts; ++part) s[e] += __int_as_float(v[part][e >> 2][e & 3]);
+    for (int i = 0; i < kLowParts; ++i) {
+      const __amdgpu_buffer_rsrc_t low =
+          make_rsrc(static_cast<const float*>(p.low) + (i * p.rows_cap + first) * rank,
+                    rows > 0 ? rows * 4 * rank : 0);
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        part[i][b] = __builtin_amdgcn_raw_buffer_load_b128(low, (int)(o + 16 * b), 0, 0);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      s[c][e] = __int_as_float(part[0][e >> 2][e & 3]);
+#pragma unroll
+      for (int i = 1; i < kLowParts; ++i) s[c][e] += __int_as_float(part[i][e >> 2][e & 3]);
+    }
+  }
+  LowScales f{1.0f, 1.0f};
+  if constexpr (F16) {
+    // the row's other columns are in the lanes 16, 32 and 48 further
+    float m = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(s[e >> 3][e & 7]));
+    m = fmaxf(m, __shfl_xor(m, 16, 64));
+    m = fmaxf(m, __shfl_xor(m, 32, 64));
+    f = low_scales(m);
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    uint32_t t0, r0, t1, r1;
-    split16<F16>(s[2 * e] * scale, t0, r0);
-    split16<F16>(s[2 * e + 1] * scale, t1, r1);
-    top[e] = (int)(t0 | t1 << 16);
-    rest[e] = (int)(r0 | r1 << 16);
-  }
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t word[kLowValues];
+      split_low<F16>(s[c][2 * e] * f.down, s[c][2 * e + 1] * f.down, word);
+#pragma unroll
+      for (int h = 0; h < kLowValues; ++h) v[c][h][e] = (int)word[h];
+    }
+  return f.up;
 }
 
 // Adds each row's own low-rank product to a wave's accumulators: for every
 // adapter that occurs in (64 of) the wave's rows one product of the rows' low values
-// (both halves) with the adapter's rows of `up`, kept for its own rows only.  So what
+// with the adapter's rows of `up`, kept for its own rows only.  So what
 // an adapter holds (infinities, NaN) never reaches a row of another request, and the
 // cost follows the adapters that meet in the wave's rows, not the requests.  The
 // operands come straight from the L2, 64 rank columns at a time, the low values
@@ -528,18 +587,14 @@ __device__ __forceinline__ void add_low_rank(const Args& p, const Tile& t, const
       const int id = lane < 16 * kI ? ids[row0 + lane] : -1;  // of row lane
       uint64_t todo = __ballot(id >= 0);
       if (todo == 0) return;
-      v4i l[kI][2][2];  // [block][32 rank columns][half]
+      v4i l[kI][2][kLowValues];  // [block][32 rank columns]
+      float factor[kI];          // of a row's products
 #pragma unroll
       for (int i = 0; i < kI; ++i) {
-        float scale = 1.0f;
-        if (p.low_parts > 1) {
-          const int mine = ids[row0 + 16 * i + r];
-          scale = mine >= 0 ? p.scale[mine] : 0.0f;
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          load_low<F16>(p, t.row0 + row0, t.a_rows - row0, 16 * i + r, at[c], scale, l[i][c][0],
-                        l[i][c][1]);
+        const int mine = ids[row0 + 16 * i + r];
+        factor[i] =
+            load_low<F16>(p, t.row0 + row0, t.a_rows - row0, 16 * i + r, k, at, l[i]) *
+            (mine >= 0 ? p.scale[mine] : 0.0f);
       }
       int turn = 0;
       while (todo != 0) {
@@ -571,23 +626,31 @@ __device__ __forceinline__ void add_low_rank(const Args& p, const Tile& t, const
             static_for<kJ / 2>([&](auto jc) {
               constexpr int j0 = decltype(jc)::value * 2, ja = jh + j0;
               fence();
-              v4f one[2];
+              // fp16: the values after the first are summed apart
+              constexpr int kSums = F16 ? 2 : 1;
+              v4f one[kSums][2];
 #pragma unroll
-              for (int j = 0; j < 2; ++j) one[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+              for (int z = 0; z < 2 * kSums; ++z) one[z >> 1][z & 1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
               for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
+                for (int h = kLowValues - 1; h >= 0; --h)
 #pragma unroll
-                  for (int j = 0; j < 2; ++j)
-                    one[j] = mfma16<F16>(u[c][j0 + j], l[i][c][half], one[j]);
+                  for (int j = 0; j < 2; ++j) {
+                    v4f& sum = one[h > 0 ? kSums - 1 : 0][j];
+                    sum = mfma16<F16>(u[c][j0 + j], l[i][c][h], sum);
+                  }
               // opaque copies: the accumulators stay where they are between the adapters
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
                 v4f y = acc[i0 + i][ja + j];
                 asm volatile("" : "+v"(y));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = mine ? y[e] + one[j][e] : y[e];
+                for (int e = 0; e < 4; ++e) {
+                  const float all = F16 ? fmaf(one[kSums - 1][j][e], 1.0f / kRestScale, one[0][j][e])
+                                        : one[0][j][e];
+                  y[e] = mine ? fmaf(all, factor[i], y[e]) : y[e];
+                }
                 acc[i0 + i][ja + j] = y;
                 if constexpr (MI * NJ == 64) asm volatile("" : "+a"(acc[i0 + i][ja + j]));
               }

@@ -7,8 +7,8 @@ using namespace g16;
 
 namespace {
 
-// The adapters' first product, X[t, :] A_a^T: scaled and as two halves, or (parts of
-// the contraction) as it is.
+// The adapters' first product, X[t, :] A_a^T: as 16-bit values, or (parts of the
+// contraction) as it is.
 //
 // A workgroup of eight waves takes 32 consecutive rows, 16 NB rank columns, one of
 // the adapters that occur in those rows and one part of the contraction; the waves
@@ -29,6 +29,7 @@ __global__ __launch_bounds__(kLowThreads, NB == 1 ? 4 : 2) void lora_low_kernel(
   __shared__ int64_t off[kMaxGroups + 1];
   __shared__ int adapters[kMaxGroups];
   __shared__ __attribute__((aligned(16))) v4f sums[kLowWaves][2][NB][64];
+  __shared__ float peaks[2][NB][16];  // largest magnitudes of a row's 16 columns
   for (int g = threadIdx.x; g < p.G; g += kLowThreads) {
     adapters[g] = adapter_of(p, g);
     if (blockIdx.x == 0 && p.adapter[g] >= p.num_adapters) dev_status_or(p.status, kDevBadAdapter);
@@ -42,6 +43,8 @@ __global__ __launch_bounds__(kLowThreads, NB == 1 ? 4 : 2) void lora_low_kernel(
   const int parts = p.low_parts;
   uint16_t* low16 = const_cast<uint16_t*>(static_cast<const uint16_t*>(p.low));
   float* low32 = const_cast<float*>(static_cast<const float*>(p.low));
+  float* low_power = const_cast<float*>(p.low_power);
+  const int chunks = (rank + kLowChunk - 1) / kLowChunk;
   const int64_t blocks = (last - first + kLowRows - 1) / kLowRows * rank_blocks;
   const int64_t items = blocks * turns * parts;
   const int runs = (k + 63) / 64;
@@ -113,32 +116,44 @@ __global__ __launch_bounds__(kLowThreads, NB == 1 ? 4 : 2) void lora_low_kernel(
         for (int b = 0; b < NB; ++b) sums[w][i][b][lane] = acc[i][b];
       __syncthreads();
       // wave w adds block (w / NB, w % NB)
+      const int i = w / NB % 2, b = w % NB;
+      v4f s = v4f{0.0f, 0.0f, 0.0f, 0.0f};
       if (w < 2 * NB) {
-        const int i = w / NB, b = w % NB;
-        v4f s = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int v = 0; v < kLowWaves; ++v) {
           const v4f t = sums[v][i][b][lane];
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[e] += t[e];
         }
-        const int j = j0 + 16 * b + 4 * q;
-        const int64_t row = row0 + 16 * i + r;
-        if ((own >> (16 * i + r) & 1) != 0 && j < rank) {
-          if (parts > 1) {
-            float* dst = low32 + (part * p.rows_cap + row) * rank + j;
-            *reinterpret_cast<v4f*>(dst) = s;
-          } else {
-            const float f = p.scale[a];
-            uint32_t top[4], rest[4];
+      }
+      LowScales f{1.0f, 1.0f};
+      if constexpr (F16) {
+        if (parts == 1) {
+          float m = fmaxf(fmaxf(fabsf(s[0]), fabsf(s[1])), fmaxf(fabsf(s[2]), fabsf(s[3])));
+          m = fmaxf(m, __shfl_xor(m, 16, 64));
+          m = fmaxf(m, __shfl_xor(m, 32, 64));
+          if (w < 2 * NB && q == 0) peaks[i][b][r] = m;
+          __syncthreads();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) split16<F16>(s[e] * f, top[e], rest[e]);
-            uint16_t* dst = low16 + row * 2 * rank + j;
-            *reinterpret_cast<v2i*>(dst) =
-                v2i{(int)(top[0] | top[1] << 16), (int)(top[2] | top[3] << 16)};
-            *reinterpret_cast<v2i*>(dst + rank) =
-                v2i{(int)(rest[0] | rest[1] << 16), (int)(rest[2] | rest[3] << 16)};
-          }
+          for (int c = 0; c < NB; ++c) m = fmaxf(m, peaks[i][c][r]);
+          f = low_scales(m);
+        }
+      }
+      const int j = j0 + 16 * b + 4 * q;
+      const int64_t row = row0 + 16 * i + r;
+      if (w < 2 * NB && (own >> (16 * i + r) & 1) != 0 && j < rank) {
+        if (parts > 1) {
+          float* dst = low32 + (part * p.rows_cap + row) * rank + j;
+          *reinterpret_cast<v4f*>(dst) = s;
+        } else {
+          uint32_t lo[kLowValues], hi[kLowValues];
+          split_low<F16>(s[0] * f.down, s[1] * f.down, lo);
+          split_low<F16>(s[2] * f.down, s[3] * f.down, hi);
+          uint16_t* dst = low16 + row * kLowValues * rank + j;
+#pragma unroll
+          for (int h = 0; h < kLowValues; ++h)
+            *reinterpret_cast<v2i*>(dst + h * rank) = v2i{(int)lo[h], (int)hi[h]};
+          if (F16 && b == 0 && q == 0) low_power[row * chunks + j0 / kLowChunk] = f.up;
         }
       }
       __syncthreads();
@@ -153,7 +168,10 @@ int low_parts(int64_t rows_cap, int64_t k) {
 
 template <bool F16>
 hipError_t launch_low(const Args& p, const uint16_t* down, hipStream_t stream) {
-  const int nb = p.rows_cap <= kFewRows || p.r <= 16 ? 1 : p.r <= 32 ? 2 : 4;
+  // all rank columns of a chunk (one power of two) in a workgroup, but where the parts are
+  // put together by the second product
+  static_assert(kLowChunk == 64, "16 * 4 columns");
+  const int nb = p.low_parts > 1 || p.r <= 16 ? 1 : p.r <= 32 ? 2 : 4;
   // as many workgroups share a block's adapters as fill the compute units
   const int64_t blocks = (p.rows_cap + kLowRows - 1) / kLowRows *
                          ((p.r + 16 * nb - 1) / (16 * nb)) * p.low_parts;
@@ -170,6 +188,10 @@ hipError_t launch_low(const Args& p, const uint16_t* down, hipStream_t stream) {
   else hipLaunchKernelGGL((lora_low_kernel<F16, 4>), gd, bd, 0, stream, p, down, tn);
   return hipGetLastError();
 }
+
+// Bytes a row of what the first product leaves for the second.
+size_t low_values_bytes(int64_t r) { return (size_t)(2 * kLowValues * r); }
+size_t low_power_bytes(int64_t r) { return (size_t)(4 * ((r + kLowChunk - 1) / kLowChunk)); }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -259,8 +281,10 @@ hipError_t launch_gemm_16bit(int mode, int f16, int G, const void* a, int64_t ld
 
 size_t lora_gemm_16bit_workspace_bytes(int64_t rows_cap, int64_t n, int64_t k, int64_t r) {
   (void)n;
+  const int parts = low_parts(rows_cap, k);
   return gemm_16bit_workspace_bytes() +
-         align256((size_t)rows_cap * (size_t)r * 4 * (size_t)low_parts(rows_cap, k));
+         align256((size_t)rows_cap * (parts > 1 ? (size_t)r * 4 * (size_t)parts
+                                                : low_values_bytes(r) + low_power_bytes(r)));
 }
 
 hipError_t launch_lora_gemm_16bit(int f16, int G, const void* x, int64_t ldx, const void* w,
@@ -282,6 +306,8 @@ hipError_t launch_lora_gemm_16bit(int f16, int G, const void* x, int64_t ldx, co
   p.G = G; p.out_f32 = out_f32;
   p.low = static_cast<char*>(ws) + gemm_16bit_workspace_bytes();
   p.low_parts = low_parts(rows_cap, k);
+  p.low_power = reinterpret_cast<const float*>(static_cast<const char*>(p.low) +
+                                               (size_t)rows_cap * low_values_bytes(r));
   p.scale = scale;
   p.up = static_cast<const uint16_t*>(up);
   p.adapter = adapter;
