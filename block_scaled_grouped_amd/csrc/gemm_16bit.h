@@ -53,7 +53,7 @@ constexpr int kStageK = 64;       // contraction indexes per LDS stage
 constexpr int kThreads = 256;
 constexpr int kSuperM = 4, kSuperN = 8;  // tile block one XCD works on
 constexpr int kLowParts = 4;             // of the adapters' first product, where it is split
-constexpr int kLowValues = 2;            // 16-bit values that carry a sum of it to the second
+constexpr int kLowValues = 3;            // 16-bit values that carry a sum of it to the second
 constexpr int kLowChunk = 64;            // rank columns that share a row's power of two
 
 enum Mode { kFprop = 0, kWgrad = 1, kDgrad = 2, kLora = 3 };
@@ -445,14 +445,16 @@ __device__ __forceinline__ float to_f32(uint32_t b) {
 }
 
 // The sums x A^T go into the second product as 16-bit values whose sum they are.  A bf16
-// value has float32's range, so the values are the nearest one to the sum and the nearest to
-// what is left.  An fp16 value has 40 binades with its subnormals, so
+// value has float32's range, so the values are the nearest one to the sum, the nearest to
+// what is left of it and what is left then.  An fp16 value has 40 binades with its
+// subnormals, so
 //   - the rank columns of a row's chunk are divided by a power of two that puts the largest
 //     into [2^14, 2^15), and the products multiplied by it again, and
-//   - what the first value leaves is held times 2^11 and summed apart, so that it reaches
-//     below fp16's smallest values.
-// Both are exact.  What the values hold of a sum: 16 bits (bf16) or 22 (fp16, of one that is
-// no less than 2^-28 of the largest in its row's chunk).
+//   - what the first value leaves is held times 2^11 and its products are summed apart, so
+//     that it reaches below fp16's smallest values.
+// Both are exact.  So the second product takes the sum as float32 has it, all 24 bits: three
+// values of 8 or 11 bits are what that takes.  (fp16: of a sum that is under 2^-26 of the
+// largest in its row's chunk, what lies above 2^-50 of that.)
 //
 // low_scales: multiplies by `down` before and `up` after, for a chunk's largest magnitude m
 // (zero, infinite and NaN too).
@@ -490,10 +492,11 @@ __device__ __forceinline__ void split_low(float a, float b, uint32_t (&word)[kLo
 // A lane's fragments of a 16-row block's low values: `row` of the wave's rows, 32 rank columns
 // and 32 more, each from byte 2 * column = at[c] on (an offset past every range: zeros), all
 // of the chunk that begins at column k.  Returns what the products have to be multiplied by.
-// rows: live rows from the wave's first on.
+// rows: live rows from the wave's first on; halves: 1 leaves the second fragments alone.
 template <bool F16>
 __device__ __forceinline__ float load_low(const Args& p, int64_t first, int rows, int row, int k,
-                                          const uint32_t (&at)[2], v4i (&v)[2][kLowValues]) {
+                                          int halves, const uint32_t (&at)[2],
+                                          v4i (&v)[2][kLowValues]) {
   const int rank = p.r;
   if (p.low_parts == 1) {
     const int line = 2 * kLowValues * rank;
@@ -516,6 +519,9 @@ __device__ __forceinline__ float load_low(const Args& p, int64_t first, int rows
   float s[2][8];
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[c][e] = 0.0f;
+    if (c >= halves) continue;
     const uint32_t o = at[c] == (uint32_t)kDmaOutOfRange ? at[c] : 2 * at[c] + row * 4 * rank;
     v4i part[kLowParts][2];
 #pragma unroll
@@ -545,7 +551,8 @@ __device__ __forceinline__ float load_low(const Args& p, int64_t first, int rows
     f = low_scales(m);
   }
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
+  for (int c = 0; c < 2; ++c) {
+    if (c >= halves) continue;  // what v holds there is not used
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       uint32_t word[kLowValues];
@@ -553,6 +560,7 @@ __device__ __forceinline__ float load_low(const Args& p, int64_t first, int rows
 #pragma unroll
       for (int h = 0; h < kLowValues; ++h) v[c][h][e] = (int)word[h];
     }
+  }
   return f.up;
 }
 
@@ -571,10 +579,16 @@ __device__ __forceinline__ void add_low_rank(const Args& p, const Tile& t, const
                                              int wcol, int lane, int part, int nparts,
                                              v4f (&acc)[MI][NJ]) {
   constexpr int kI = MI < 4 ? MI : 4, kJ = NJ < 4 ? NJ : 4;
-  const int r = lane & 15, q = lane >> 4, rank = p.r;
+  const int q = lane >> 4, rank = p.r;
   // rows and columns past the tile's, and rank columns past the last, read as zeros
   const int cols = t.b_rows - wcol;
-  for (int k = 0; k < rank; k += 64) {
+  for (int k = 0; k < rank; k += kLowChunk) {
+    // opaque: keeps the offsets of all loads from being hoisted out of the loop
+    int r = lane & 15;
+    asm volatile("" : "+v"(r));
+    // halves of the chunk that hold rank columns (one workgroup a compute unit has no scalar
+    // registers to spare for the branches, and loses 1 % with them)
+    const int halves = MI == 8 || rank - k > kLowChunk / 2 ? 2 : 1;
     uint32_t at[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -593,7 +607,7 @@ __device__ __forceinline__ void add_low_rank(const Args& p, const Tile& t, const
       for (int i = 0; i < kI; ++i) {
         const int mine = ids[row0 + 16 * i + r];
         factor[i] =
-            load_low<F16>(p, t.row0 + row0, t.a_rows - row0, 16 * i + r, k, at, l[i]) *
+            load_low<F16>(p, t.row0 + row0, t.a_rows - row0, 16 * i + r, k, halves, at, l[i]) *
             (mine >= 0 ? p.scale[mine] : 0.0f);
       }
       int turn = 0;
@@ -632,7 +646,8 @@ __device__ __forceinline__ void add_low_rank(const Args& p, const Tile& t, const
 #pragma unroll
               for (int z = 0; z < 2 * kSums; ++z) one[z >> 1][z & 1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-              for (int c = 0; c < 2; ++c)
+              for (int c = 0; c < 2; ++c) {
+                if (c >= halves) continue;
 #pragma unroll
                 for (int h = kLowValues - 1; h >= 0; --h)
 #pragma unroll
@@ -640,6 +655,7 @@ __device__ __forceinline__ void add_low_rank(const Args& p, const Tile& t, const
                     v4f& sum = one[h > 0 ? kSums - 1 : 0][j];
                     sum = mfma16<F16>(u[c][j0 + j], l[i][c][h], sum);
                   }
+              }
               // opaque copies: the accumulators stay where they are between the adapters
 #pragma unroll
               for (int j = 0; j < 2; ++j) {

@@ -168,10 +168,11 @@ int low_parts(int64_t rows_cap, int64_t k) {
 
 template <bool F16>
 hipError_t launch_low(const Args& p, const uint16_t* down, hipStream_t stream) {
-  // all rank columns of a chunk (one power of two) in a workgroup, but where the parts are
-  // put together by the second product
+  // the rank columns that share a power of two (fp16, where no parts are left to the second
+  // product) are a workgroup's
   static_assert(kLowChunk == 64, "16 * 4 columns");
-  const int nb = p.low_parts > 1 || p.r <= 16 ? 1 : p.r <= 32 ? 2 : 4;
+  const bool narrow = F16 ? p.low_parts > 1 : p.rows_cap <= kFewRows;
+  const int nb = narrow || p.r <= 16 ? 1 : p.r <= 32 ? 2 : 4;
   // as many workgroups share a block's adapters as fill the compute units
   const int64_t blocks = (p.rows_cap + kLowRows - 1) / kLowRows *
                          ((p.r + 16 * nb - 1) / (16 * nb)) * p.low_parts;

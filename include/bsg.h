@@ -650,10 +650,10 @@ int grouped_gemm_16bit(int mode, int in_dtype, int64_t G, const void* a, int64_t
  *               zeros).
  *   adapter     [G] int32, scale [num_adapters] float32, device.
  *   out         [rows_cap, n], ldo; the operands' type or BSG_OUT_F32, rounded once.
- *               X A^T is accumulated in FP32 and kept as two 16-bit values for the
- *               second product: 16 bits of it (bf16), or 22 at any magnitude (fp16;
- *               fewer of what is under 2^-28 of the largest of its row in 64 rank
- *               columns).  scale multiplies the second product, in FP32.
+ *               X A^T is accumulated in FP32 and enters the second product with all
+ *               24 bits, as three 16-bit values (fp16: at any magnitude; of what is
+ *               under 2^-26 of the largest of its row in 64 rank columns, what lies
+ *               above 2^-50 of that).  scale multiplies the second product, in FP32.
  *   workspace   grouped_lora_gemm_16bit_workspace_size(rows_cap, n, k, rank) bytes,
  *               256-byte aligned.
  * Constraints on n, k and strides and errors as grouped_gemm_16bit.

@@ -112,3 +112,23 @@ def test_infinities_come_out_as_the_formula_has_them(shape, dtype, value):
         assert torch.equal(rows.float().isnan(), want.isnan().expand(rows.shape[0], -1))
         same = ~want.isnan()
         assert bool((rows.float()[:, same] == want[same]).all())
+
+
+@pytest.mark.parametrize("shape", range(len(SHAPES)))
+@pytest.mark.parametrize("dtype,exps", [(torch.float16, e) for e in MAGNITUDES] +
+                         [(torch.bfloat16, e) for e in ((0, 0, 0, 0), (-40, -30, 9, 3), (30, 44, -60, -7))])
+def test_all_24_bits_are_kept(dtype, exps, shape):
+    """x A^T as float32 holds it: the result is the formula's, bit for bit."""
+    xe, ae, be, se = exps
+    args, ref = _inputs(dtype, SHAPES[shape], lambda t: xe, lambda j: ae, be, se, 10 * shape + 4)
+    assert torch.equal(bsg.grouped_lora_gemm_16bit(*args, out_dtype=bsg.BSG_OUT_F32).to(F64), ref)
+
+
+@pytest.mark.parametrize("shape", range(len(SHAPES)))
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_all_24_bits_are_kept_of_values_far_apart(dtype, shape):
+    """Rank columns 2^25 apart (fp16) and 2^50 (bf16) in one row."""
+    args, ref = _inputs(dtype, SHAPES[shape], lambda t: -12 + 17 * (t % 2) - t % 7,
+                        (lambda j: 5 - j % 26) if dtype == torch.float16 else (lambda j: 20 - j % 51), -3, -6,
+                        10 * shape + 5)
+    assert torch.equal(bsg.grouped_lora_gemm_16bit(*args, out_dtype=bsg.BSG_OUT_F32).to(F64), ref)
