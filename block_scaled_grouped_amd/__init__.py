@@ -917,8 +917,9 @@ class GradClipPlan:
 def grad_clip_plan(tensors, outs=None, device=None):
     """Plan for grad_norm and clip_grad_norm over contiguous bf16, fp16 or float32 device
     tensors (any number, any sizes, aligned to their elements).  outs: where the clipped
-    gradients go (same types and sizes); None clips in place.  device: needed only where
-    there are no tensors."""
+    gradients go (same types and sizes); None clips in place.  An output may share memory
+    with its own tensor only, so a tensor that is used twice (tied weights) is listed once.
+    device: needed only where there are no tensors."""
     import torch
     lib = load_library()
     tensors = list(tensors)

@@ -7,6 +7,8 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "bsg_internal.h"
 
 namespace {
@@ -670,6 +672,41 @@ int grouped_lora_gemm_16bit(int in_dtype, int64_t G, const void* x, int64_t ldx,
       fn);
 }
 
+namespace {
+
+size_t grad_elem_bytes(int32_t dtype) { return dtype == BSG_GRAD_F32 ? 4 : 2; }
+
+// Whether a tensor is written while another one, or another part of the same, is read or
+// written: workgroups would race.  Returns its index, or -1.  The table that is about to be
+// filled serves as scratch: a record for each tensor that holds elements, by its output.
+int64_t find_overlap(const void* const* src, void* const* dst, const int64_t* numels,
+                     const int32_t* dtypes, bsg::GradChunk* rec, int32_t count) {
+  const auto bytes = [&](int32_t i) { return (uintptr_t)numels[i] * grad_elem_bytes(dtypes[i]); };
+  const auto begin = [](const bsg::GradChunk& r) { return reinterpret_cast<uintptr_t>(r.dst); };
+  int64_t used = 0;
+  for (int32_t i = 0; i < count; ++i)
+    if (numels[i] != 0) rec[used++] = bsg::GradChunk{src[i], dst[i], i, 0};
+  std::sort(rec, rec + used,
+            [&](const bsg::GradChunk& a, const bsg::GradChunk& b) { return begin(a) < begin(b); });
+  for (int64_t r = 1; r < used; ++r)
+    if (begin(rec[r]) < begin(rec[r - 1]) + bytes(rec[r - 1].n)) return rec[r].n;
+  for (int32_t i = 0; i < count; ++i) {
+    if (numels[i] == 0) continue;
+    // the last output that begins before the input's end: where none, or this tensor's own in
+    // the same place, no other reaches into the input
+    const uintptr_t s = reinterpret_cast<uintptr_t>(src[i]);
+    const bsg::GradChunk* after =
+        std::lower_bound(rec, rec + used, s + bytes(i),
+                         [&](const bsg::GradChunk& r, uintptr_t end) { return begin(r) < end; });
+    if (after == rec) continue;
+    const bsg::GradChunk& d = after[-1];
+    if (begin(d) + bytes(d.n) > s && !(d.n == i && begin(d) == s)) return i;
+  }
+  return -1;
+}
+
+}  // namespace
+
 int grad_clip_plan_fill(int64_t num_tensors, const void* const* src, void* const* dst,
                         const int64_t* numels, const int32_t* dtypes, void* plan,
                         size_t plan_bytes, int64_t* num_chunks) {
@@ -677,9 +714,15 @@ int grad_clip_plan_fill(int64_t num_tensors, const void* const* src, void* const
   if (num_chunks == nullptr || src == nullptr || dst == nullptr || numels == nullptr ||
       dtypes == nullptr)
     return fail(BSG_ERR_NULL, "%s: src, dst, numels, dtypes and num_chunks must be non-NULL", fn);
-  if (num_tensors < 0) return fail(BSG_ERR_SHAPE, "%s: num_tensors=%lld", fn, (long long)num_tensors);
+  if (num_tensors < 0 || num_tensors >= ((int64_t)1 << 31))
+    return fail(BSG_ERR_SHAPE, "%s: num_tensors=%lld", fn, (long long)num_tensors);
   bsg::GradChunk* out = static_cast<bsg::GradChunk*>(plan);
   const int64_t room = plan != nullptr ? (int64_t)(plan_bytes / sizeof(bsg::GradChunk)) : 0;
+  // the first chunk is as much shorter as puts the later ones on 128-byte lines
+  const auto first_chunk = [&](int64_t i) {
+    return bsg::kGradChunk - (int64_t)(reinterpret_cast<uintptr_t>(src[i]) % 128 /
+                                       grad_elem_bytes(dtypes[i]));
+  };
   int64_t count = 0;
   for (int64_t i = 0; i < num_tensors; ++i) {
     if (dtypes[i] != BSG_GRAD_BF16 && dtypes[i] != BSG_GRAD_F16 && dtypes[i] != BSG_GRAD_F32)
@@ -690,25 +733,28 @@ int grad_clip_plan_fill(int64_t num_tensors, const void* const* src, void* const
     if (numels[i] == 0) continue;
     if (src[i] == nullptr || dst[i] == nullptr)
       return fail(BSG_ERR_NULL, "%s: tensor %lld has no data", fn, (long long)i);
-    const uintptr_t esz = dtypes[i] == BSG_GRAD_F32 ? 4 : 2;
-    const uintptr_t s = reinterpret_cast<uintptr_t>(src[i]), d = reinterpret_cast<uintptr_t>(dst[i]);
-    if (s % esz != 0 || d % esz != 0)
+    const uintptr_t esz = grad_elem_bytes(dtypes[i]);
+    if (reinterpret_cast<uintptr_t>(src[i]) % esz != 0 || reinterpret_cast<uintptr_t>(dst[i]) % esz != 0)
       return fail(BSG_ERR_ALIGN, "%s: tensor %lld is not aligned to its elements", fn, (long long)i);
-    // the first chunk is as much shorter as puts the later ones on 128-byte lines
-    int64_t take = bsg::kGradChunk - (int64_t)((s % 128) / esz);
-    for (int64_t at = 0; at < numels[i];) {
-      const int64_t left = numels[i] - at;
-      if (take > left) take = left;
-      if (plan != nullptr) {
-        if (count >= room)
-          return fail(BSG_ERR_WORKSPACE, "%s: a plan of %zu bytes is too small", fn, plan_bytes);
-        out[count] = bsg::GradChunk{reinterpret_cast<const void*>(s + (uintptr_t)at * esz),
-                                    reinterpret_cast<void*>(d + (uintptr_t)at * esz), (int32_t)take,
-                                    dtypes[i]};
+    const int64_t rest = numels[i] - first_chunk(i);
+    count += 1 + (rest > 0 ? (rest + bsg::kGradChunk - 1) / bsg::kGradChunk : 0);
+  }
+  if (plan != nullptr) {
+    if (count > room)
+      return fail(BSG_ERR_WORKSPACE, "%s: a plan of %zu bytes is too small", fn, plan_bytes);
+    const int64_t bad = find_overlap(src, dst, numels, dtypes, out, (int32_t)num_tensors);
+    if (bad >= 0)
+      return fail(BSG_ERR_SHAPE, "%s: tensor %lld shares memory with another one's output, or in "
+                  "part with its own", fn, (long long)bad);
+    for (int64_t i = 0; i < num_tensors; ++i) {
+      const uintptr_t esz = grad_elem_bytes(dtypes[i]);
+      int64_t take = first_chunk(i);
+      for (int64_t at = 0; at < numels[i]; at += take, take = bsg::kGradChunk) {
+        if (take > numels[i] - at) take = numels[i] - at;
+        *out++ = bsg::GradChunk{static_cast<const char*>(src[i]) + (uintptr_t)at * esz,
+                                static_cast<char*>(dst[i]) + (uintptr_t)at * esz, (int32_t)take,
+                                dtypes[i]};
       }
-      ++count;
-      at += take;
-      take = bsg::kGradChunk;
     }
   }
   *num_chunks = count;

@@ -675,7 +675,9 @@ int grouped_lora_gemm_16bit(int in_dtype, int64_t G, const void* x, int64_t ldx,
  * walks, on the host: no device is touched.
  *   src, dst    [host] arrays of num_tensors device pointers, aligned to their
  *               elements; dst[i] receives the clipped src[i] and may equal it.
- *               Other overlaps are not allowed.
+ *               An output that shares memory with another tensor's input or output,
+ *               or in part with its own input, is refused (BSG_ERR_SHAPE): workgroups
+ *               would race.  So a tensor is listed once, also where it is used twice.
  *   numels      [host] elements (>= 0); dtypes [host] bsg_grad_dtype.
  *   plan        [host] buffer of plan_bytes, or NULL to ask for the size only.
  *   num_chunks  [host] output; the plan takes 24 bytes per chunk.
