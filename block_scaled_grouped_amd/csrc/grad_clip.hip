@@ -132,7 +132,8 @@ __device__ __forceinline__ void write_norm(double sumsq, float* norm, double* ou
   const float n = (float)sqrt(sumsq);
   if (norm != nullptr) *norm = n;
   if (out_sumsq != nullptr) *out_sumsq = sumsq;
-  if (!(sumsq < __builtin_inf())) dev_status_or(status, kDevNonFinite);
+  // the norm as the caller gets it: a finite sum's may be past float32's largest value
+  if (!(n < __builtin_inff())) dev_status_or(status, kDevNonFinite);
 }
 
 __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const double* __restrict__ partials,

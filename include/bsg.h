@@ -691,8 +691,9 @@ int grouped_lora_gemm_16bit(int in_dtype, int64_t G, const void* x, int64_t ldx,
  *                 sumsq: a float64 on the device to take for the sum of squares
  *                 (NULL: this call computes it).  In place and within max_norm,
  *                 nothing is written.
- * Sums are float64, in a fixed order.  A norm that is not finite sets
- * BSG_DEV_NONFINITE; the formula then gives zeros and NaN.
+ * Sums are float64, in a fixed order.  A norm that is not finite in float32 sets
+ * BSG_DEV_NONFINITE; where the sum of squares is not finite either, the formula
+ * gives zeros and NaN.
  *   workspace   grad_clip_workspace_size() bytes, 8-byte aligned.
  *   max_norm    >= 0 (infinity: no clipping).
  * Errors: BSG_ERR_NULL, BSG_ERR_SHAPE (counts, max_norm), BSG_ERR_UNSUPPORTED
