@@ -143,22 +143,34 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const double* __res
   if (threadIdx.x == 0) write_norm(s, norm, out_sumsq, status);
 }
 
+// A factor in two steps, x * a * b.  A norm of more than max_norm * 2^126 makes factors below
+// float32's normal numbers, where fewer than 24 bits are left of them: there a is the factor
+// times 2^64 and b 2^-64.  Elsewhere b is 1, which changes nothing.
+struct Factor {
+  float a, b;
+};
+__device__ __forceinline__ Factor make_factor(double f) {
+  if (f < 0x1p-126) return {(float)(f * 0x1p64), 0x1p-64f};
+  return {(float)f, 1.0f};
+}
+__device__ __forceinline__ float times(float x, const Factor& f) { return x * f.a * f.b; }
+
 template <int DT>
-__device__ __forceinline__ v4i scaled(const v4i& v, float f) {
+__device__ __forceinline__ v4i scaled(const v4i& v, const Factor& f) {
   v4i y;
   if constexpr (DT == 2) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = __float_as_int(elem<2>(v, e) * f);
+    for (int e = 0; e < 4; ++e) y[e] = __float_as_int(times(elem<2>(v, e), f));
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      y[e] = (int)pack16<DT == 1>(elem<DT>(v, 2 * e) * f, elem<DT>(v, 2 * e + 1) * f);
+      y[e] = (int)pack16<DT == 1>(times(elem<DT>(v, 2 * e), f), times(elem<DT>(v, 2 * e + 1), f));
   }
   return y;
 }
 
 template <int DT>
-__device__ __forceinline__ void chunk_scale(const GradChunk& c, float f) {
+__device__ __forceinline__ void chunk_scale(const GradChunk& c, const Factor& f) {
   constexpr int per = DT == 2 ? 4 : 8;
   const gchar* src = (const gchar*)c.src;
   gchar* dst = (gchar*)c.dst;
@@ -176,7 +188,7 @@ __device__ __forceinline__ void chunk_scale(const GradChunk& c, float f) {
     store16_last(dst + (int64_t)i * 16, scaled<DT>(load16_last(src + (int64_t)i * 16), f));
   const int tail = whole * per + threadIdx.x;
   if (tail < c.n) {
-    const float x = one_elem<DT>(src, tail) * f;
+    const float x = times(one_elem<DT>(src, tail), f);
     if constexpr (DT == 2) {
       *reinterpret_cast<__attribute__((address_space(1))) float*>(dst + (int64_t)tail * 4) = x;
     } else {
@@ -195,11 +207,11 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(
   if (blockIdx.x == 0 && threadIdx.x == 0) write_norm(sumsq, norm, nullptr, status);
   double f = (double)max_norm / (sqrt(sumsq) + 1e-6);
   if (f > 1.0) f = 1.0;  // a NaN stays one
-  const float factor = (float)f;
+  const Factor factor = make_factor(f);
   // the second pass begins with what the first one read last
   for (int64_t i = num_chunks - 1 - blockIdx.x; i >= 0; i -= gridDim.x) {
     const GradChunk c = plan[i];
-    if (factor == 1.0f && c.dst == c.src) continue;
+    if (factor.a == 1.0f && factor.b == 1.0f && c.dst == c.src) continue;
     if (c.dtype == 2) chunk_scale<2>(c, factor);
     else if (c.dtype == 1) chunk_scale<1>(c, factor);
     else chunk_scale<0>(c, factor);
