@@ -857,7 +857,9 @@ def grouped_gemm_16bit(mode, a, b, offsets, c=None, out=None, out_dtype=None, wo
 
 
 def grouped_lora_gemm_16bit_workspace(rows_cap, n, k, rank, device=None):
-    """A uint8 device tensor for the `workspace` argument of grouped_lora_gemm_16bit."""
+    """A uint8 device tensor for the `workspace` argument of grouped_lora_gemm_16bit, with
+    up to rows_cap rows and a rank of up to `rank`.  Calls that may run at the same time (on
+    different streams) need a workspace each."""
     import torch
     nbytes = int(load_library().grouped_lora_gemm_16bit_workspace_size(rows_cap, n, k, rank))
     if nbytes == 0:
@@ -873,7 +875,7 @@ def grouped_lora_gemm_16bit(x, w, lora_a, lora_b, offsets, adapter, scale, out=N
     x [rows, k], w [n, k] (rows may be strided), lora_a [adapters, rank, k] and lora_b
     [adapters, n, rank] of one 16-bit type; adapter int32 [G], scale float32 [adapters].
     workspace: grouped_lora_gemm_16bit_workspace(rows, n, k, rank), or None for a new
-    one.  See include/bsg.h."""
+    one (some 67 MB a call).  See include/bsg.h."""
     import torch
     lib = load_library()
     code, od, odt = _types_16bit(x, "x", out_dtype, out)

@@ -624,7 +624,7 @@ int grouped_gemm_16bit(int mode, int in_dtype, int64_t G, const void* a, int64_t
 
 size_t grouped_lora_gemm_16bit_workspace_size(int64_t rows_cap, int64_t n, int64_t k, int64_t rank) {
   if (rows_cap < 0 || n < 0 || k < 0 || rank < 0 || rank > BSG_MAX_LORA_RANK) return 0;
-  return bsg::lora_gemm_16bit_workspace_bytes(rows_cap, n, k, rank);
+  return bsg::lora_gemm_16bit_workspace_bytes(rows_cap, rank);
 }
 
 int grouped_lora_gemm_16bit(int in_dtype, int64_t G, const void* x, int64_t ldx, const void* w,
@@ -662,7 +662,7 @@ int grouped_lora_gemm_16bit(int in_dtype, int64_t G, const void* x, int64_t ldx,
   if (!aligned4(adapter) || !aligned4(scale))
     return fail(BSG_ERR_ALIGN, "%s: adapter and scale must be 4-byte aligned", fn);
   const int wc = check_16bit_workspace(
-      fn, workspace, workspace_bytes, bsg::lora_gemm_16bit_workspace_bytes(rows_cap, n, k, rank));
+      fn, workspace, workspace_bytes, bsg::lora_gemm_16bit_workspace_bytes(rows_cap, rank));
   if (wc != BSG_OK) return wc;
   return hip_result(
       bsg::launch_lora_gemm_16bit(in_dtype == BSG_IN_F16, (int)G, x, ldx, w, ldw, lora_a, lora_b,

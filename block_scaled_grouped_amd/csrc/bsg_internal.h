@@ -267,7 +267,7 @@ hipError_t launch_gemm_16bit(int mode, int f16, int G, const void* a, int64_t ld
                              int64_t ldo, int64_t stride_o, int out_f32, void* ws, uint32_t* status,
                              hipStream_t stream);
 
-size_t lora_gemm_16bit_workspace_bytes(int64_t rows_cap, int64_t n, int64_t k, int64_t r);
+size_t lora_gemm_16bit_workspace_bytes(int64_t rows_cap, int64_t r);
 
 hipError_t launch_lora_gemm_16bit(int f16, int G, const void* x, int64_t ldx, const void* w,
                                   int64_t ldw, const void* down, const void* up,

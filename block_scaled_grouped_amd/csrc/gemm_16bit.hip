@@ -280,12 +280,14 @@ hipError_t launch_gemm_16bit(int mode, int f16, int G, const void* a, int64_t ld
   return launch_form(mode, f16, p, stream);
 }
 
-size_t lora_gemm_16bit_workspace_bytes(int64_t rows_cap, int64_t n, int64_t k, int64_t r) {
-  (void)n;
-  const int parts = low_parts(rows_cap, k);
-  return gemm_16bit_workspace_bytes() +
-         align256((size_t)rows_cap * (parts > 1 ? (size_t)r * 4 * (size_t)parts
-                                                : low_values_bytes(r) + low_power_bytes(r)));
+// Never less for more rows or a larger rank, and the same for every n and k, so that the
+// workspace of the largest call serves all: the parts of few rows take more than the values
+// of a few rows more.
+size_t lora_gemm_16bit_workspace_bytes(int64_t rows_cap, int64_t r) {
+  const size_t few = (size_t)(rows_cap < kFewRows ? rows_cap : kFewRows);
+  const size_t parts = few * (size_t)r * 4 * kLowParts;
+  const size_t values = (size_t)rows_cap * (low_values_bytes(r) + low_power_bytes(r));
+  return gemm_16bit_workspace_bytes() + align256(parts > values ? parts : values);
 }
 
 hipError_t launch_lora_gemm_16bit(int f16, int G, const void* x, int64_t ldx, const void* w,

@@ -622,7 +622,8 @@ int grouped_gemm_nvfp4_rowscaled_wgrad_ex(int64_t G, const uint8_t* a, const uin
  *               between rows (a multiple of 8), stride_o between groups (WGRAD).
  *   workspace   grouped_gemm_16bit_workspace_size() bytes, 256-byte aligned, or
  *               NULL.  With it, products with few output tiles are split along the
- *               contraction and summed in a fixed order by a second kernel.
+ *               contraction and summed in a fixed order by a second kernel.  Calls
+ *               that may run at the same time need a workspace each.
  * Results do not depend on the order in which workgroups run.
  * Errors: BSG_ERR_NULL, BSG_ERR_SHAPE, BSG_ERR_UNSUPPORTED (mode, types),
  * BSG_ERR_ALIGN (a, b, c, out 16-byte), BSG_ERR_WORKSPACE.
@@ -655,7 +656,9 @@ int grouped_gemm_16bit(int mode, int in_dtype, int64_t G, const void* a, int64_t
  *               under 2^-26 of the largest of its row in 64 rank columns, what lies
  *               above 2^-50 of that).  scale multiplies the second product, in FP32.
  *   workspace   grouped_lora_gemm_16bit_workspace_size(rows_cap, n, k, rank) bytes,
- *               256-byte aligned.
+ *               256-byte aligned.  The size never decreases in any of the four, so
+ *               one workspace serves calls of up to that many rows and that rank.
+ *               Calls that may run at the same time need a workspace each.
  * Constraints on n, k and strides and errors as grouped_gemm_16bit.
  * The gradients of the adapters are products of grouped_gemm_16bit.
  */
