@@ -104,10 +104,10 @@ struct Args {
   int G, out_f32;
   Div grid, band;  // workgroups; tiles of kSuperM rows of tiles
   // LORA
-  const void* low;         // X A^T of each row's own adapter: 16-bit [rows_cap, kLowValues, r],
+  void* low;               // X A^T of each row's own adapter: 16-bit [rows_cap, kLowValues, r],
                            // the values that carry it, or (low_parts: kLowParts, not 1)
                            // float32 [kLowParts, rows_cap, r], parts of its contraction
-  const float* low_power;  // fp16, low_parts 1: [rows_cap, r / kLowChunk rounded up], the power
+  float* low_power;        // fp16, low_parts 1: [rows_cap, r / kLowChunk rounded up], the power
                            // of two to multiply the values of a row's chunk by
   const float* scale;      // [adapters]
   int low_parts;
@@ -260,8 +260,8 @@ __device__ __forceinline__ Tile find_tile(const Args& p, const Sched& sm, int ti
 
 template <int BR>
 __device__ __forceinline__ int swz(int k) {
-  const int low = BR >= 128 ? 4 * (k & 3) : BR == 64 ? 4 * ((k >> 1) & 1) : 0;
-  return low + 2 * ((k >> 3) & 1);
+  static_assert(BR >= 128, "a row of 16 chunks or more");
+  return 4 * (k & 3) + 2 * ((k >> 3) & 1);
 }
 
 // A global -> LDS copy of 16 bytes a lane (1 KiB at `at` + IMM) in two steps, so that
@@ -501,7 +501,7 @@ __device__ __forceinline__ float load_low(const Args& p, int64_t first, int rows
   if (p.low_parts == 1) {
     const int line = 2 * kLowValues * rank;
     const __amdgpu_buffer_rsrc_t low =
-        make_rsrc(static_cast<const uint16_t*>(p.low) + first * kLowValues * rank,
+        make_rsrc(static_cast<uint16_t*>(p.low) + first * kLowValues * rank,
                   rows > 0 ? rows * line : 0);
 #pragma unroll
     for (int c = 0; c < 2; ++c)
@@ -527,7 +527,7 @@ __device__ __forceinline__ float load_low(const Args& p, int64_t first, int rows
 #pragma unroll
     for (int i = 0; i < kLowParts; ++i) {
       const __amdgpu_buffer_rsrc_t low =
-          make_rsrc(static_cast<const float*>(p.low) + (i * p.rows_cap + first) * rank,
+          make_rsrc(static_cast<float*>(p.low) + (i * p.rows_cap + first) * rank,
                     rows > 0 ? rows * 4 * rank : 0);
 #pragma unroll
       for (int b = 0; b < 2; ++b)

@@ -41,9 +41,8 @@ __global__ __launch_bounds__(kLowThreads, NB == 1 ? 4 : 2) void lora_low_kernel(
   const int r = lane & 15, q = lane >> 4, rank = p.r, k = (int)p.k;
   const int rank_blocks = (rank + 16 * NB - 1) / (16 * NB);
   const int parts = p.low_parts;
-  uint16_t* low16 = const_cast<uint16_t*>(static_cast<const uint16_t*>(p.low));
-  float* low32 = const_cast<float*>(static_cast<const float*>(p.low));
-  float* low_power = const_cast<float*>(p.low_power);
+  uint16_t* low16 = static_cast<uint16_t*>(p.low);
+  float* low32 = static_cast<float*>(p.low);
   const int chunks = (rank + kLowChunk - 1) / kLowChunk;
   const int64_t blocks = (last - first + kLowRows - 1) / kLowRows * rank_blocks;
   const int64_t items = blocks * turns * parts;
@@ -153,7 +152,7 @@ __global__ __launch_bounds__(kLowThreads, NB == 1 ? 4 : 2) void lora_low_kernel(
 #pragma unroll
           for (int h = 0; h < kLowValues; ++h)
             *reinterpret_cast<v2i*>(dst + h * rank) = v2i{(int)lo[h], (int)hi[h]};
-          if (F16 && b == 0 && q == 0) low_power[row * chunks + j0 / kLowChunk] = f.up;
+          if (F16 && b == 0 && q == 0) p.low_power[row * chunks + j0 / kLowChunk] = f.up;
         }
       }
       __syncthreads();
@@ -309,8 +308,8 @@ hipError_t launch_lora_gemm_16bit(int f16, int G, const void* x, int64_t ldx, co
   p.G = G; p.out_f32 = out_f32;
   p.low = static_cast<char*>(ws) + gemm_16bit_workspace_bytes();
   p.low_parts = low_parts(rows_cap, k);
-  p.low_power = reinterpret_cast<const float*>(static_cast<const char*>(p.low) +
-                                               (size_t)rows_cap * low_values_bytes(r));
+  p.low_power =
+      reinterpret_cast<float*>(static_cast<char*>(p.low) + (size_t)rows_cap * low_values_bytes(r));
   p.scale = scale;
   p.up = static_cast<const uint16_t*>(up);
   p.adapter = adapter;
