@@ -47,8 +47,9 @@ EXPORTS = ("bsg_last_error", "bsg_version", "group_offsets_i32_to_i64", "grouped
            "grouped_gemm_mxfp8_workspace_size", "grouped_gemm_mxfp8_ws",
            "grouped_gemm_nvfp4_workspace_size", "grouped_gemm_nvfp4_rowscaled_ws",
            "grouped_gemm_nvfp4_pertensor_ws",
-           "grouped_gemm_16bit_workspace_size", "grouped_gemm_16bit",
-           "grouped_lora_gemm_16bit_workspace_size", "grouped_lora_gemm_16bit",
+           "grouped_gemm_16bit_workspace_size", "grouped_gemm_16bit_tile_rows", "grouped_gemm_16bit",
+           "grouped_lora_gemm_16bit_workspace_size", "grouped_lora_gemm_16bit_tile_rows",
+           "grouped_lora_gemm_16bit",
            "grad_clip_plan_fill", "grad_clip_workspace_size", "grad_norm", "clip_grad_norm")
 BSG_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -134,11 +135,15 @@ def load_library(path=LIB_PATH):
     SZ = ctypes.c_size_t
     lib.grouped_gemm_16bit_workspace_size.restype = SZ
     lib.grouped_gemm_16bit_workspace_size.argtypes = []
+    lib.grouped_gemm_16bit_tile_rows.restype = I32
+    lib.grouped_gemm_16bit_tile_rows.argtypes = [I32, I64, I64, I64, I64, I32]
     lib.grouped_gemm_16bit.restype = I32
     lib.grouped_gemm_16bit.argtypes = [I32, I32, I64, P, I64, P, I64, I64, P, I64, I64, I64, P, P,
                                        I64, I64, I32, P, SZ, P, P]
     lib.grouped_lora_gemm_16bit_workspace_size.restype = SZ
     lib.grouped_lora_gemm_16bit_workspace_size.argtypes = [I64, I64, I64, I64]
+    lib.grouped_lora_gemm_16bit_tile_rows.restype = I32
+    lib.grouped_lora_gemm_16bit_tile_rows.argtypes = [I64, I64, I64]
     lib.grouped_lora_gemm_16bit.restype = I32
     lib.grouped_lora_gemm_16bit.argtypes = [I32, I64, P, I64, P, I64, P, P, I64, I64, P, P, P, I64,
                                             I64, I64, P, I64, I32, P, SZ, P, P]
@@ -854,6 +859,25 @@ def grouped_gemm_16bit(mode, a, b, offsets, c=None, out=None, out_dtype=None, wo
         None if status is None else _dense(status, "status", 4, status.dtype, dev),
         _stream(a)) if optr else 0)
     return out
+
+
+def grouped_gemm_16bit_tile_rows(mode, groups, rows_cap, n, k, workspace=True):
+    """Rows of the output tiles (32, 64, 128 or 256) that grouped_gemm_16bit takes for these
+    sizes on the current device.  It goes by rows_cap, the rows of the tensors, however few of
+    them the offsets leave live: pass a view of the rows that can be live."""
+    rows = load_library().grouped_gemm_16bit_tile_rows(mode, groups, rows_cap, n, k, 1 if workspace else 0)
+    if rows == 0:
+        raise ValueError("no 16-bit product of mode %r, %r groups, rows_cap=%r, n=%r, k=%r" % (
+            mode, groups, rows_cap, n, k))
+    return rows
+
+
+def grouped_lora_gemm_16bit_tile_rows(rows_cap, n, k):
+    """As grouped_gemm_16bit_tile_rows, for grouped_lora_gemm_16bit."""
+    rows = load_library().grouped_lora_gemm_16bit_tile_rows(rows_cap, n, k)
+    if rows == 0:
+        raise ValueError("no adapted projection of rows_cap=%r, n=%r, k=%r" % (rows_cap, n, k))
+    return rows
 
 
 def grouped_lora_gemm_16bit_workspace(rows_cap, n, k, rank, device=None):

@@ -550,6 +550,19 @@ bool row_stride_ok(int64_t ld, int64_t cols) {
   return ld >= cols && ld % 8 == 0 && ld <= kMaxRowStride;
 }
 
+// At most this many output tiles of the smallest kind keep a tile's index in 31 bits.
+bool tiles_ok(bool wgrad, int64_t G, int64_t rows_cap, int64_t n, int64_t k) {
+  return (wgrad ? G * ((n + 63) / 64) * ((k + 63) / 64)
+                : ((rows_cap + 15) / 16 + G) * ((n + 63) / 64)) < ((int64_t)1 << 31);
+}
+
+// Whether some call takes these sizes.
+bool sizes_16bit_ok(bool wgrad, int64_t G, int64_t rows_cap, int64_t n, int64_t k) {
+  return G >= 1 && G <= BSG_MAX_GROUPS && rows_cap >= 0 && rows_cap < ((int64_t)1 << 31) &&
+         n > 0 && row_stride_ok(n, n) && k > 0 && row_stride_ok(k, k) &&
+         tiles_ok(wgrad, G, rows_cap, n, k);
+}
+
 int check_16bit_types(const char* fn, int in_dtype, int out_dtype) {
   if (in_dtype != BSG_IN_BF16 && in_dtype != BSG_IN_F16)
     return fail(BSG_ERR_UNSUPPORTED, "%s: in_dtype %d", fn, in_dtype);
@@ -571,6 +584,13 @@ int check_16bit_workspace(const char* fn, const void* workspace, size_t have, si
 }  // namespace
 
 size_t grouped_gemm_16bit_workspace_size(void) { return bsg::gemm_16bit_workspace_bytes(); }
+
+int grouped_gemm_16bit_tile_rows(int mode, int64_t G, int64_t rows_cap, int64_t n, int64_t k,
+                                 int with_workspace) {
+  if (mode != BSG_FPROP_TN && mode != BSG_WGRAD_NT && mode != BSG_DGRAD_NN) return 0;
+  if (!sizes_16bit_ok(mode == BSG_WGRAD_NT, G, rows_cap, n, k)) return 0;
+  return bsg::gemm_16bit_tile_rows(mode, G, rows_cap, n, k, with_workspace != 0);
+}
 
 int grouped_gemm_16bit(int mode, int in_dtype, int64_t G, const void* a, int64_t lda,
                        const void* b, int64_t ldb, int64_t stride_b, const int64_t* offsets,
@@ -604,9 +624,7 @@ int grouped_gemm_16bit(int mode, int in_dtype, int64_t G, const void* a, int64_t
   if (wgrad && G > 1 && (stride_o % 8 != 0 || stride_o < (n - 1) * ldo + k))
     return fail(BSG_ERR_SHAPE, "%s: stride_o=%lld overlaps the groups or is no multiple of 8", fn,
                 (long long)stride_o);
-  const int64_t tiles = wgrad ? G * ((n + 63) / 64) * ((k + 63) / 64)
-                              : ((rows_cap + 15) / 16 + G) * ((n + 63) / 64);
-  if (n >= kMaxTileBytes || k >= kMaxTileBytes || tiles >= ((int64_t)1 << 31))
+  if (!tiles_ok(wgrad, G, rows_cap, n, k))
     return fail(BSG_ERR_SHAPE, "%s: too many output tiles", fn);
   if (!aligned16(a) || !aligned16(b) || !aligned16(out) || !aligned16(c))
     return fail(BSG_ERR_ALIGN, "%s: a, b, c and out must be 16-byte aligned", fn);
@@ -625,6 +643,11 @@ int grouped_gemm_16bit(int mode, int in_dtype, int64_t G, const void* a, int64_t
 size_t grouped_lora_gemm_16bit_workspace_size(int64_t rows_cap, int64_t n, int64_t k, int64_t rank) {
   if (rows_cap < 0 || n < 0 || k < 0 || rank < 0 || rank > BSG_MAX_LORA_RANK) return 0;
   return bsg::lora_gemm_16bit_workspace_bytes(rows_cap, rank);
+}
+
+int grouped_lora_gemm_16bit_tile_rows(int64_t rows_cap, int64_t n, int64_t k) {
+  if (!sizes_16bit_ok(false, 1, rows_cap, n, k)) return 0;
+  return bsg::lora_gemm_16bit_tile_rows(rows_cap, n, k);
 }
 
 int grouped_lora_gemm_16bit(int in_dtype, int64_t G, const void* x, int64_t ldx, const void* w,
@@ -655,7 +678,7 @@ int grouped_lora_gemm_16bit(int in_dtype, int64_t G, const void* x, int64_t ldx,
     return fail(BSG_ERR_SHAPE,
                 "%s: ldx=%lld, ldw=%lld, ldo=%lld must be multiples of 8 in [row length, %lld]", fn,
                 (long long)ldx, (long long)ldw, (long long)ldo, (long long)kMaxRowStride);
-  if (((rows_cap + 15) / 16 + 1) * ((n + 63) / 64) >= ((int64_t)1 << 31))
+  if (!tiles_ok(false, 1, rows_cap, n, k))
     return fail(BSG_ERR_SHAPE, "%s: too many output tiles", fn);
   if (!aligned16(x) || !aligned16(w) || !aligned16(lora_a) || !aligned16(lora_b) || !aligned16(out))
     return fail(BSG_ERR_ALIGN, "%s: x, w, lora_a, lora_b and out must be 16-byte aligned", fn);

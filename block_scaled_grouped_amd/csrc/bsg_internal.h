@@ -269,6 +269,10 @@ hipError_t launch_gemm_16bit(int mode, int f16, int G, const void* a, int64_t ld
 
 size_t lora_gemm_16bit_workspace_bytes(int64_t rows_cap, int64_t r);
 
+// Rows of the output tiles that a call takes (split: with a workspace).
+int gemm_16bit_tile_rows(int mode, int64_t G, int64_t rows_cap, int64_t n, int64_t k, bool split);
+int lora_gemm_16bit_tile_rows(int64_t rows_cap, int64_t n, int64_t k);
+
 hipError_t launch_lora_gemm_16bit(int f16, int G, const void* x, int64_t ldx, const void* w,
                                   int64_t ldw, const void* down, const void* up,
                                   int64_t num_adapters, int64_t r, const int64_t* offsets,

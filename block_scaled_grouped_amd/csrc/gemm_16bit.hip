@@ -214,42 +214,47 @@ constexpr Form kForms[4] = {
     {32, 128, 0.52, 1.5, 4.0}, {64, 128, 0.70, 2.0, 4.5}, {128, 128, 1.14, 3.0, 6.0},
     {256, 256, 1.37, 5.0, 13.0}};
 
-double expected_us(const Form& f, int mode, const Args& p) {
+double expected_us(const Form& f, int mode, int64_t G, int64_t rows_cap, int64_t n, int64_t k,
+                   bool split) {
   const int64_t slots = (f.bm == 256 ? 1 : 2) * (int64_t)device_cu_count();
-  const int64_t ntn = (p.n + f.bn - 1) / f.bn;
+  const int64_t ntn = (n + f.bn - 1) / f.bn;
   int64_t tiles, stages, split_stages;
   if (mode == kWgrad) {
-    tiles = p.G * ((p.n + f.bm - 1) / f.bm) * ((p.k + f.bn - 1) / f.bn);
-    split_stages = (p.rows_cap + kStageK - 1) / kStageK;
-    stages = (p.rows_cap / p.G + kStageK - 1) / kStageK;
+    tiles = G * ((n + f.bm - 1) / f.bm) * ((k + f.bn - 1) / f.bn);
+    split_stages = (rows_cap + kStageK - 1) / kStageK;
+    stages = (rows_cap / G + kStageK - 1) / kStageK;
     if (stages < 1) stages = 1;
   } else {
-    const int64_t groups = mode == kLora ? 1 : p.rows_cap < p.G ? p.rows_cap : p.G;
-    tiles = ((p.rows_cap + f.bm - 1) / f.bm + (groups > 1 ? groups / 2 : 0)) * ntn;
-    split_stages = stages = (p.k + kStageK - 1) / kStageK;
+    const int64_t groups = mode == kLora ? 1 : rows_cap < G ? rows_cap : G;
+    tiles = ((rows_cap + f.bm - 1) / f.bm + (groups > 1 ? groups / 2 : 0)) * ntn;
+    split_stages = stages = (k + kStageK - 1) / kStageK;
   }
   const int64_t full = tiles / slots, left = tiles % slots;
   double us = (double)full * ((double)stages * f.stage_us + f.tile_us);
   if (left > 0) {
-    const int parts =
-        p.ws == nullptr ? 1 : split_parts((int)slots, (int)left, (int)split_stages);
+    const int parts = split ? split_parts((int)slots, (int)left, (int)split_stages) : 1;
     us += (double)((stages + parts - 1) / parts) * f.stage_us + f.tile_us +
           (parts > 1 ? f.reduce_us : 0.0);
   }
   return us;
 }
 
-hipError_t launch_form(int mode, int f16, const Args& p, hipStream_t stream) {
+// Rows of the tiles of the form that a call takes.
+int form_rows(int mode, int64_t G, int64_t rows_cap, int64_t n, int64_t k, bool split) {
   int best = mode == kWgrad ? 2 : 0;  // weight gradients have no forms of fewer rows
-  double us = expected_us(kForms[best], mode, p);
+  double us = expected_us(kForms[best], mode, G, rows_cap, n, k, split);
   for (int i = best + 1; i < 4; ++i) {
-    const double t = expected_us(kForms[i], mode, p);
+    const double t = expected_us(kForms[i], mode, G, rows_cap, n, k, split);
     if (t < us) {
       us = t;
       best = i;
     }
   }
-  const int bm = kForms[best].bm;
+  return kForms[best].bm;
+}
+
+hipError_t launch_form(int mode, int f16, const Args& p, hipStream_t stream) {
+  const int bm = form_rows(mode, p.G, p.rows_cap, p.n, p.k, p.ws != nullptr);
   return bm == 256 ? launch_large(mode, f16, p, stream) : launch_small(mode, f16, bm, p, stream);
 }
 
@@ -258,6 +263,14 @@ hipError_t launch_form(int mode, int f16, const Args& p, hipStream_t stream) {
 size_t gemm_16bit_workspace_bytes() {
   const size_t l = large_workspace_bytes(), s = small_workspace_bytes();
   return l > s ? l : s;
+}
+
+int gemm_16bit_tile_rows(int mode, int64_t G, int64_t rows_cap, int64_t n, int64_t k, bool split) {
+  return form_rows(mode, G, rows_cap, n, k, split);
+}
+
+int lora_gemm_16bit_tile_rows(int64_t rows_cap, int64_t n, int64_t k) {
+  return form_rows(kLora, 1, rows_cap, n, k, true);
 }
 
 hipError_t launch_gemm_16bit(int mode, int f16, int G, const void* a, int64_t lda, const void* b,

@@ -627,8 +627,17 @@ int grouped_gemm_nvfp4_rowscaled_wgrad_ex(int64_t G, const uint8_t* a, const uin
  * Results do not depend on the order in which workgroups run.
  * Errors: BSG_ERR_NULL, BSG_ERR_SHAPE, BSG_ERR_UNSUPPORTED (mode, types),
  * BSG_ERR_ALIGN (a, b, c, out 16-byte), BSG_ERR_WORKSPACE.
+ *
+ * grouped_gemm_16bit_tile_rows: the rows of the output tiles (32, 64, 128 or 256)
+ * that a call of these sizes takes on the current device, with or without a
+ * workspace; 0 for sizes that it refuses.  The group sizes are on the device, so
+ * the choice goes by rows_cap: a buffer whose live rows are a small part of
+ * rows_cap runs with the tiles of a full one.  Where the live rows have a smaller
+ * bound, pass that as rows_cap.
  */
 size_t grouped_gemm_16bit_workspace_size(void);
+int grouped_gemm_16bit_tile_rows(int mode, int64_t G, int64_t rows_cap, int64_t n, int64_t k,
+                                 int with_workspace);
 int grouped_gemm_16bit(int mode, int in_dtype, int64_t G, const void* a, int64_t lda,
                        const void* b, int64_t ldb, int64_t stride_b, const int64_t* offsets,
                        int64_t rows_cap, int64_t n, int64_t k, const void* c, void* out,
@@ -661,8 +670,10 @@ int grouped_gemm_16bit(int mode, int in_dtype, int64_t G, const void* a, int64_t
  *               Calls that may run at the same time need a workspace each.
  * Constraints on n, k and strides and errors as grouped_gemm_16bit.
  * The gradients of the adapters are products of grouped_gemm_16bit.
+ * grouped_lora_gemm_16bit_tile_rows: as grouped_gemm_16bit_tile_rows.
  */
 size_t grouped_lora_gemm_16bit_workspace_size(int64_t rows_cap, int64_t n, int64_t k, int64_t rank);
+int grouped_lora_gemm_16bit_tile_rows(int64_t rows_cap, int64_t n, int64_t k);
 int grouped_lora_gemm_16bit(int in_dtype, int64_t G, const void* x, int64_t ldx, const void* w,
                             int64_t ldw, const void* lora_a, const void* lora_b,
                             int64_t num_adapters, int64_t rank, const int64_t* offsets,
