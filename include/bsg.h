@@ -700,8 +700,9 @@ int grouped_lora_gemm_16bit(int in_dtype, int64_t G, const void* x, int64_t ldx,
  *
  * grad_norm:      norm[0] = sqrt(sum x^2) (float32, optional), sumsq[0] = sum x^2
  *                 (float64, optional; add the ranks' values for a sharded model).
- * clip_grad_norm: dst = src * min(1, max_norm / (norm + 1e-6)), rounded once to
- *                 the tensor's type; norm[0] (optional) the norm before clipping.
+ * clip_grad_norm: dst = src * min(1, max_norm / (norm + 1e-6)); the factor, then
+ *                 the product, are rounded to float32, and a 16-bit gradient's
+ *                 product to its type; norm[0] (optional) the norm before clipping.
  *                 sumsq: a float64 on the device to take for the sum of squares
  *                 (NULL: this call computes it).  In place and within max_norm,
  *                 nothing is written.
