@@ -564,6 +564,8 @@ __device__ __forceinline__ float load_low(const Args& p, int64_t first, int rows
   return f.up;
 }
 
+constexpr int kWaitLoads = 0x0f70;  // s_waitcnt vmcnt(0)
+
 // Adds each row's own low-rank product to a wave's accumulators: for every
 // adapter that occurs in (64 of) the wave's rows one product of the rows' low values
 // with the adapter's rows of `up`, kept for its own rows only.  So what
@@ -675,6 +677,10 @@ __device__ __forceinline__ void add_low_rank(const Args& p, const Tile& t, const
           });
         });
       }
+      // Waits for loads that no block has used.  Left outstanding, the compiler waits for
+      // them where their registers are written again: in the contraction's loop, where that
+      // waits for the copies in flight as well.
+      __builtin_amdgcn_s_waitcnt(kWaitLoads);
     });
   }
 }
