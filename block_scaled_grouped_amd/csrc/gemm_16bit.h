@@ -602,6 +602,12 @@ __device__ __forceinline__ void add_low_rank(const Args& p, const Tile& t, const
       const int row0 = wrow + 16 * i0;
       const int id = lane < 16 * kI ? ids[row0 + lane] : -1;  // of row lane
       uint64_t todo = __ballot(id >= 0);
+      // the next `count` adapters are others' to add
+      const auto pass = [&](int count) {
+        for (; count > 0 && todo != 0; --count)
+          todo &= ~__ballot(id == __builtin_amdgcn_readlane(id, __builtin_ctzll(todo)));
+      };
+      pass(part);
       if (todo == 0) return;
       v4i l[kI][2][kLowValues];  // [block][32 rank columns]
       float factor[kI];          // of a row's products
@@ -612,16 +618,11 @@ __device__ __forceinline__ void add_low_rank(const Args& p, const Tile& t, const
             load_low<F16>(p, t.row0 + row0, t.a_rows - row0, 16 * i + r, k, halves, at, l[i]) *
             (mine >= 0 ? p.scale[mine] : 0.0f);
       }
-      int turn = 0;
       while (todo != 0) {
         const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
         const uint64_t own = __ballot(id == a);
         todo &= ~own;
-        if (nparts > 1) {
-          const bool mine = turn == part;
-          turn = turn + 1 == nparts ? 0 : turn + 1;
-          if (!mine) continue;
-        }
+        pass(nparts - 1);
         const __amdgpu_buffer_rsrc_t up = make_rsrc(
             p.up + ((int64_t)a * p.n + t.col0 + wcol) * rank, cols > 0 ? cols * 2 * rank : 0);
         static_for<NJ / kJ>([&](auto hc) {
