@@ -23,8 +23,12 @@ constexpr int kLowWaves = kLowThreads / 64;
 constexpr int kLowRows = 32;
 constexpr int64_t kFewRows = 1024;  // 32 blocks of rows leave compute units idle
 
-template <bool F16, int NB>  // 16 NB <= 64 rank columns a workgroup
-__global__ __launch_bounds__(kLowThreads, NB == 1 ? 4 : 2) void lora_low_kernel(Args p, const uint16_t* down,
+// NB: 16 NB <= 64 rank columns a workgroup.  DENSE: two workgroups a compute unit, with fewer
+// loads in flight in each.  For all calls of 16 columns, and for few rows, where most
+// workgroups are later turns that have nothing to do (660 rows, rank 32, 25 adapters of fp16:
+// the call in 13.2 us, 15.2 with one workgroup a compute unit).
+template <bool F16, int NB, bool DENSE>
+__global__ __launch_bounds__(kLowThreads, DENSE ? 4 : 2) void lora_low_kernel(Args p, const uint16_t* down,
                                                                int turns) {
   __shared__ int64_t off[kMaxGroups + 1];
   __shared__ int adapters[kMaxGroups];
@@ -86,7 +90,7 @@ __global__ __launch_bounds__(kLowThreads, NB == 1 ? 4 : 2) void lora_low_kernel(
         for (int b = 0; b < NB; ++b) acc[i][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
       }
       // kRuns of the wave's runs are loaded before the first is used
-      constexpr int kRuns = NB == 1 ? 3 : NB == 2 ? 4 : 2;
+      constexpr int kRuns = DENSE ? (NB == 1 ? 3 : NB == 2 ? 2 : 1) : NB == 2 ? 4 : 2;
       const int end = 64 * run1 < k ? 64 * run1 : k;
       for (int k0 = 64 * (run0 + w); k0 < end; k0 += 64 * kLowWaves * kRuns) {
         v4i fx[2 * kRuns][2], fd[2 * kRuns][NB];
@@ -170,8 +174,9 @@ hipError_t launch_low(const Args& p, const uint16_t* down, hipStream_t stream) {
   // the rank columns that share a power of two (fp16, where no parts are left to the second
   // product) are a workgroup's
   static_assert(kLowChunk == 64, "16 * 4 columns");
-  const bool narrow = F16 ? p.low_parts > 1 : p.rows_cap <= kFewRows;
-  const int nb = narrow || p.r <= 16 ? 1 : p.r <= 32 ? 2 : 4;
+  const bool few = p.rows_cap <= kFewRows;
+  const bool narrow = p.r <= 16 || (few && (!F16 || p.low_parts > 1));
+  const int nb = narrow ? 1 : p.r <= 32 ? 2 : 4;
   // as many workgroups share a block's adapters as fill the compute units
   const int64_t blocks = (p.rows_cap + kLowRows - 1) / kLowRows *
                          ((p.r + 16 * nb - 1) / (16 * nb)) * p.low_parts;
@@ -181,11 +186,23 @@ hipError_t launch_low(const Args& p, const uint16_t* down, hipStream_t stream) {
   const int64_t most = p.rows_cap < p.G ? p.rows_cap : p.G;  // adapters that can meet in a block
   if (turns > most) turns = most;
   const int64_t grid = blocks * turns < cap ? blocks * turns : cap;
-  const dim3 gd((unsigned)grid), bd(kLowThreads);
-  const int tn = (int)turns;
-  if (nb == 1) hipLaunchKernelGGL((lora_low_kernel<F16, 1>), gd, bd, 0, stream, p, down, tn);
-  else if (nb == 2) hipLaunchKernelGGL((lora_low_kernel<F16, 2>), gd, bd, 0, stream, p, down, tn);
-  else hipLaunchKernelGGL((lora_low_kernel<F16, 4>), gd, bd, 0, stream, p, down, tn);
+  const auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kLowThreads), 0, stream, p, down,
+                       (int)turns);
+  };
+  bool done = nb == 1;
+  if (done) run(lora_low_kernel<F16, 1, true>);
+  if constexpr (F16) {
+    if (!done && few) {
+      if (nb == 2) run(lora_low_kernel<F16, 2, true>);
+      else run(lora_low_kernel<F16, 4, true>);
+      done = true;
+    }
+  }
+  if (!done) {
+    if (nb == 2) run(lora_low_kernel<F16, 2, false>);
+    else run(lora_low_kernel<F16, 4, false>);
+  }
   return hipGetLastError();
 }
 
