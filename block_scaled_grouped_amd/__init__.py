@@ -23,10 +23,13 @@ BSG_WGRAD_NT_E5M2 = 3
 BSG_OUT_F16 = 2
 BSG_IN_BF16 = 0
 BSG_IN_F16 = 1
+BSG_IN_F32 = 2
 BSG_GRAD_BF16 = 0
 BSG_GRAD_F16 = 1
 BSG_GRAD_F32 = 2
 BSG_MAX_LORA_RANK = 256
+BSG_MAX_TOP_K = 16
+BSG_MAX_INT8_K = 131056
 BSG_MAX_GROUPS = 256
 BSG_COLWISE_PAD = 128
 DEV_NEGATIVE_SIZE = 1
@@ -50,7 +53,12 @@ EXPORTS = ("bsg_last_error", "bsg_version", "group_offsets_i32_to_i64", "grouped
            "grouped_gemm_16bit_workspace_size", "grouped_gemm_16bit_tile_rows", "grouped_gemm_16bit",
            "grouped_lora_gemm_16bit_workspace_size", "grouped_lora_gemm_16bit_tile_rows",
            "grouped_lora_gemm_16bit",
-           "grad_clip_plan_fill", "grad_clip_workspace_size", "grad_norm", "clip_grad_norm")
+           "grad_clip_plan_fill", "grad_clip_workspace_size", "grad_norm", "clip_grad_norm",
+           "moe_router_topk_workspace_size", "moe_router_topk", "moe_router_topk_backward",
+           "grouped_quantize_int8", "grouped_gemm_int8_workspace_size", "grouped_gemm_int8_tile_rows",
+           "grouped_gemm_int8", "grouped_gemm_int8_dynamic_workspace_size",
+           "grouped_gemm_int8_dynamic", "grouped_swiglu_checkpoint_mxfp8",
+           "grouped_swiglu_checkpoint_mxfp8_backward")
 BSG_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 _lib = None
@@ -155,6 +163,33 @@ def load_library(path=LIB_PATH):
     lib.grad_norm.argtypes = [P, I64, P, SZ, P, P, P, P]
     lib.clip_grad_norm.restype = I32
     lib.clip_grad_norm.argtypes = [P, I64, ctypes.c_float, P, P, SZ, P, P, P]
+    lib.moe_router_topk_workspace_size.restype = SZ
+    lib.moe_router_topk_workspace_size.argtypes = [I64, I64]
+    lib.moe_router_topk.restype = I32
+    lib.moe_router_topk.argtypes = [I32, P, I64, I64, I64, I64, P, I32, P, P, P, P, P, P, P, SZ, P, P]
+    lib.moe_router_topk_backward.restype = I32
+    lib.moe_router_topk_backward.argtypes = [I32, P, I64, I64, I64, I64, P, I32, P, P, P, P, P, P, I64,
+                                             P]
+    lib.grouped_quantize_int8.restype = I32
+    lib.grouped_quantize_int8.argtypes = [I32, P, I64, I64, I64, I64, P, P, P, P, P]
+    lib.grouped_gemm_int8_workspace_size.restype = SZ
+    lib.grouped_gemm_int8_workspace_size.argtypes = []
+    lib.grouped_gemm_int8_tile_rows.restype = I32
+    lib.grouped_gemm_int8_tile_rows.argtypes = [I64, I64, I64, I64, I32]
+    lib.grouped_gemm_int8.restype = I32
+    lib.grouped_gemm_int8.argtypes = [I64, P, I64, P, P, I64, I64, P, P, I64, I64, I64, P, I64, I32, P,
+                                      SZ, P, P]
+    lib.grouped_gemm_int8_dynamic_workspace_size.restype = SZ
+    lib.grouped_gemm_int8_dynamic_workspace_size.argtypes = [I64, I64]
+    lib.grouped_gemm_int8_dynamic.restype = I32
+    lib.grouped_gemm_int8_dynamic.argtypes = [I32, I64, P, I64, P, I64, I64, P, P, I64, I64, I64, P,
+                                              I64, I32, P, SZ, P, P]
+    lib.grouped_swiglu_checkpoint_mxfp8.restype = I32
+    lib.grouped_swiglu_checkpoint_mxfp8.argtypes = [I32, P, I64, P, I64, P, I64, I64, P, I64, P, P, P,
+                                                    P]
+    lib.grouped_swiglu_checkpoint_mxfp8_backward.restype = I32
+    lib.grouped_swiglu_checkpoint_mxfp8_backward.argtypes = [I32, P, P, P, P, I64, I64, P, I64, I64, P,
+                                                             I64, P, I64, P, P, P]
     _lib = lib
     return lib
 
@@ -1010,3 +1045,287 @@ def clip_grad_norm(plan, max_norm, sumsq=None, norm=None, status=None):
                                          _ptr(plan.workspace), plan.workspace.numel(), _ptr(norm),
                                          _ptr(status), _stream(plan.table)))
     return norm
+
+
+def _launch(fn, index, *args):
+    """fn(*args, stream) on device `index`, on its current stream; kernels are launched on the
+    device that is current."""
+    import torch
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            _check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
+    else:
+        _check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
+
+
+def _maybe(t, name, nbytes, dtype, index):
+    """_dense for a tensor that may be left out."""
+    return None if t is None else _dense(t, name, nbytes, dtype, index)
+
+
+def _status(t, index):
+    return None if t is None else _dense(t, "status", 4, t.dtype, index)
+
+
+def _router_args(logits, mask, index):
+    """(in_dtype, row stride, tokens, experts, the mask's address)"""
+    import torch
+    codes = {torch.bfloat16: BSG_IN_BF16, torch.float16: BSG_IN_F16, torch.float32: BSG_IN_F32}
+    if logits.dtype not in codes:
+        raise ValueError("logits must be bfloat16, float16 or float32, not %s" % _dtype_name(logits.dtype))
+    ld, _ = _strided(logits, "logits", 2, logits.dtype, index)
+    tokens, experts = logits.shape
+    if mask is not None and mask.dtype not in (torch.bool, torch.uint8):
+        raise ValueError("mask must be bool or uint8, not %s" % _dtype_name(mask.dtype))
+    m = None if mask is None else _dense(mask, "mask", tokens, mask.dtype, index)
+    return codes[logits.dtype], ld, tokens, experts, m
+
+
+def moe_router_topk_workspace(tokens, experts, device=None):
+    """A uint8 device tensor for the `workspace` argument of moe_router_topk, with up to that many
+    tokens and experts.  Calls that may run at the same time need a workspace each."""
+    import torch
+    nbytes = int(load_library().moe_router_topk_workspace_size(tokens, experts))
+    if nbytes == 0:
+        raise ValueError("no workspace for %r tokens and %r experts" % (tokens, experts))
+    return torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+def moe_router_topk(logits, top_k, mask=None, normalize=True, workspace=None, status=None):
+    """Each token's top_k of the experts by its logits [tokens, experts] (bf16, fp16 or float32; rows
+    may be strided), and what balances them.  mask [tokens] (bool or uint8): tokens to route.  Returns
+
+    experts    int32 [tokens, top_k], in descending order (ties: the lowest index first; -1: none)
+    weights    float32 [tokens, top_k]: softmax probabilities; normalize: over the chosen ones' sum
+    counts     int32 [experts]: the sizes that group_offsets_i32_to_i64 takes
+    prob_sums  float32 [experts], live int32 [1]: sums over the tokens that are routed
+    loss       float32 [1]: experts / (top_k live^2) * sum(counts * prob_sums)
+
+    as a dict.  See include/bsg.h."""
+    import torch
+    lib = load_library()
+    dev = _device_index(logits, "logits")
+    code, ld, tokens, E, m = _router_args(logits, mask, dev)
+    if workspace is None:
+        workspace = moe_router_topk_workspace(tokens, max(E, 1), logits.device)
+    out = {"experts": logits.new_empty((tokens, top_k), dtype=torch.int32),
+           "weights": logits.new_empty((tokens, top_k), dtype=torch.float32),
+           "counts": logits.new_empty(E, dtype=torch.int32),
+           "prob_sums": logits.new_empty(E, dtype=torch.float32),
+           "live": logits.new_empty(1, dtype=torch.int32),
+           "loss": logits.new_empty(1, dtype=torch.float32)}
+    _launch(lib.moe_router_topk, dev, code, logits.data_ptr(), ld, tokens, E, top_k, m,
+            1 if normalize else 0, *(t.data_ptr() for t in out.values()),
+            _dense(workspace, "workspace", 0, workspace.dtype, dev), workspace.nbytes,
+            _status(status, dev))
+    return out
+
+
+def moe_router_topk_backward(logits, experts, counts, live, d_weights=None, d_loss=None, mask=None,
+                             normalize=True, out=None):
+    """d_logits of sum(d_weights * weights) + d_loss * loss, with the experts and counts that
+    moe_router_topk gave (counts and live may be sums over ranks).  d_weights float32
+    [tokens, top_k], d_loss float32 [1] on the device; either may be left out.  out: not logits."""
+    import torch
+    lib = load_library()
+    dev = _device_index(logits, "logits")
+    code, ld, tokens, E, m = _router_args(logits, mask, dev)
+    if experts.dim() != 2 or experts.shape[0] != tokens:
+        raise ValueError("experts is %s, the logits have %d rows" % (tuple(experts.shape), tokens))
+    top_k = experts.shape[1]
+    if d_weights is not None and tuple(d_weights.shape) != (tokens, top_k):
+        raise ValueError("d_weights is %s, experts %s" % (tuple(d_weights.shape), (tokens, top_k)))
+    out = _out_or_new(out, (tokens, E), logits.dtype, logits)
+    ldo, _ = _strided(out, "out", 2, logits.dtype, dev)
+    args = (_dense(experts, "experts", 4 * tokens * top_k, torch.int32, dev),
+            _maybe(d_weights, "d_weights", 4 * tokens * top_k, torch.float32, dev),
+            _dense(counts, "counts", 4 * E, torch.int32, dev), _dense(live, "live", 4, torch.int32, dev),
+            _maybe(d_loss, "d_loss", 4, torch.float32, dev), out.data_ptr(), ldo)
+    if tokens:
+        _launch(lib.moe_router_topk_backward, dev, code, logits.data_ptr(), ld, tokens, E, top_k, m,
+                1 if normalize else 0, *args)
+    return out
+
+
+def _in_16bit(t, name):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return BSG_IN_BF16
+    if t.dtype == torch.float16:
+        return BSG_IN_F16
+    raise ValueError("%s must be bfloat16 or float16, not %s" % (name, _dtype_name(t.dtype)))
+
+
+def grouped_quantize_int8(x, offsets=None, data=None, scales=None, status=None):
+    """Rows of x [rows, cols] (bf16 or fp16; rows may be strided) in 8-bit integers with a float32
+    scale each: (data int8 [rows, cols], scales [rows]).  offsets: only rows in
+    [offsets[0], offsets[-1]); None: all.  Weights [G, n, k] go in as G * n rows."""
+    import torch
+    lib = load_library()
+    code, dev = _in_16bit(x, "x"), _device_index(x, "x")
+    ld, _ = _strided(x, "x", 2, x.dtype, dev)
+    rows, cols = x.shape
+    if data is None:
+        data = x.new_empty((rows, cols), dtype=torch.int8)
+    if scales is None:
+        scales = x.new_empty(rows, dtype=torch.float32)
+    args = (_maybe(offsets, "offsets", 16, torch.int64, dev),
+            _dense(data, "data", rows * cols, torch.int8, dev),
+            _dense(scales, "scales", 4 * rows, torch.float32, dev), _status(status, dev))
+    if rows:
+        _launch(lib.grouped_quantize_int8, dev, code, x.data_ptr(), ld, rows, cols,
+                0 if offsets is None else offsets.numel() - 1, *args)
+    return data, scales
+
+
+def _int8_product(rows, k, w, w_scales, offsets, out, out_dtype, default, ref, dev):
+    """Checked arguments that the int8 products share: (out, G, arguments from b to out_dtype)."""
+    import torch
+    codes = {torch.bfloat16: BSG_OUT_BF16, torch.float16: BSG_OUT_F16, torch.float32: BSG_OUT_F32}
+    ldw, stride_w = _strided(w, "w", 3, torch.int8, dev)
+    G, n, wk = w.shape
+    if offsets.numel() - 1 != G or wk != k:
+        raise ValueError("w is %s; %d groups contracting %d are needed" % (
+            tuple(w.shape), offsets.numel() - 1, k))
+    if out_dtype is None:
+        out_dtype = codes.get(out.dtype) if out is not None else default
+    odt = next((d for d, c in codes.items() if c == out_dtype), None)
+    if odt is None:
+        raise ValueError("out_dtype %r is not BSG_OUT_BF16, BSG_OUT_F16 or BSG_OUT_F32" % (out_dtype,))
+    out = _out_or_new(out, (rows, n), odt, ref)
+    ldo, _ = _strided(out, "out", 2, odt, dev)
+    return out, G, (w.data_ptr(), ldw, stride_w,
+                    _dense(w_scales, "w_scales", 4 * G * n, torch.float32, dev),
+                    _dense(offsets, "offsets", 16, torch.int64, dev), rows, n, k, out.data_ptr(), ldo,
+                    out_dtype)
+
+
+def grouped_gemm_int8(a, a_scales, w, w_scales, offsets, out=None, out_dtype=None, workspace=None,
+                      status=None):
+    """Group g's rows of a [rows, k] int8 times w[g]^T (w [G, n, k] int8), each times its row's scale
+    and its channel's: a_scales float32 [rows], w_scales float32 [G, n] -> [rows, n].  out_dtype:
+    BSG_OUT_BF16 (default), BSG_OUT_F16 or BSG_OUT_F32.  workspace: gemm_workspace(), or None
+    (no contraction is split).  See include/bsg.h."""
+    import torch
+    lib = load_library()
+    dev = _device_index(a, "a")
+    lda, _ = _strided(a, "a", 2, torch.int8, dev)
+    rows, k = a.shape
+    out, G, args = _int8_product(rows, k, w, w_scales, offsets, out, out_dtype, BSG_OUT_BF16, a, dev)
+    scales = _dense(a_scales, "a_scales", 4 * rows, torch.float32, dev)
+    ws = (None, 0) if workspace is None else (
+        _dense(workspace, "workspace", 0, workspace.dtype, dev), workspace.nbytes)
+    if rows:
+        _launch(lib.grouped_gemm_int8, dev, G, a.data_ptr(), lda, scales, *args, *ws,
+                _status(status, dev))
+    return out
+
+
+def grouped_gemm_int8_tile_rows(groups, rows_cap, n, k, workspace=True):
+    """As grouped_gemm_16bit_tile_rows, for grouped_gemm_int8 and grouped_gemm_int8_dynamic."""
+    rows = load_library().grouped_gemm_int8_tile_rows(groups, rows_cap, n, k, 1 if workspace else 0)
+    if rows == 0:
+        raise ValueError("no int8 product of %r groups, rows_cap=%r, n=%r, k=%r" % (groups, rows_cap, n, k))
+    return rows
+
+
+def grouped_gemm_int8_dynamic_workspace(rows_cap, k, device=None):
+    """A uint8 device tensor for the `workspace` argument of grouped_gemm_int8_dynamic, with up to
+    rows_cap rows and a contraction of up to k.  Calls that may run at the same time need a
+    workspace each."""
+    import torch
+    nbytes = int(load_library().grouped_gemm_int8_dynamic_workspace_size(rows_cap, k))
+    if nbytes == 0:
+        raise ValueError("no workspace for rows_cap=%r, k=%r" % (rows_cap, k))
+    return torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+def grouped_gemm_int8_dynamic(x, w, w_scales, offsets, out=None, out_dtype=None, workspace=None,
+                              status=None):
+    """grouped_gemm_int8 of 16-bit tokens x [rows, k] (bf16 or fp16; rows may be strided), quantized
+    on the way as grouped_quantize_int8 does.  out_dtype: None for the type of `out` or, without
+    one, of x.  workspace: grouped_gemm_int8_dynamic_workspace(rows, k), or None for a new one
+    (some 67 MB and the tokens' integers a call)."""
+    lib = load_library()
+    code, dev = _in_16bit(x, "x"), _device_index(x, "x")
+    ldx, _ = _strided(x, "x", 2, x.dtype, dev)
+    rows, k = x.shape
+    out, G, args = _int8_product(rows, k, w, w_scales, offsets, out, out_dtype,
+                                 BSG_OUT_F16 if code == BSG_IN_F16 else BSG_OUT_BF16, x, dev)
+    if workspace is None:
+        workspace = grouped_gemm_int8_dynamic_workspace(rows, k, x.device)
+    ws = _dense(workspace, "workspace", 0, workspace.dtype, dev)
+    if rows:
+        _launch(lib.grouped_gemm_int8_dynamic, dev, code, G, x.data_ptr(), ldx, *args, ws,
+                workspace.nbytes, _status(status, dev))
+    return out
+
+
+def grouped_swiglu_checkpoint_mxfp8(h, offsets, row_weights=None, out=None, data=None, scales=None,
+                                    keep=True, status=None):
+    """out = row_weights * silu(g) * u of h = [g | u] ([rows, 2 f], bf16 or fp16; rows may be strided),
+    and h in 8 bits for grouped_swiglu_checkpoint_mxfp8_backward: (out [rows, f], data uint8
+    [rows, 2 f] E4M3 codes, scales uint8 [rows, f / 16] E8M0 bytes).  keep=False: (out, None, None).
+    Only rows in [offsets[0], offsets[-1]).  See include/bsg.h."""
+    import torch
+    lib = load_library()
+    code, dev = _in_16bit(h, "h"), _device_index(h, "h")
+    ldh, _ = _strided(h, "h", 2, h.dtype, dev)
+    rows, f2 = h.shape
+    f = f2 // 2
+    if f2 % 64 != 0 or f2 == 0:
+        raise ValueError("h has %d columns, not two times a multiple of 32" % f2)
+    out = _out_or_new(out, (rows, f), h.dtype, h)
+    ldo, _ = _strided(out, "out", 2, h.dtype, dev)
+    kept = (None, None)
+    if keep:
+        if data is None:
+            data = h.new_empty((rows, f2), dtype=torch.uint8)
+        if scales is None:
+            scales = h.new_empty((rows, f // 16), dtype=torch.uint8)
+        kept = (_dense(data, "data", rows * f2, torch.uint8, dev),
+                _dense(scales, "scales", rows * (f // 16), torch.uint8, dev))
+    else:
+        data = scales = None
+    w = _maybe(row_weights, "row_weights", 4 * rows, torch.float32, dev)
+    off = _dense(offsets, "offsets", 16, torch.int64, dev)
+    if rows:
+        _launch(lib.grouped_swiglu_checkpoint_mxfp8, dev, code, h.data_ptr(), ldh, w,
+                offsets.numel() - 1, off, rows, f, out.data_ptr(), ldo, *kept, _status(status, dev))
+    return out, data, scales
+
+
+def grouped_swiglu_checkpoint_mxfp8_backward(data, scales, d_out, offsets, row_weights=None,
+                                             recompute=False, d_h=None, d_row_weights=None, out=None,
+                                             status=None):
+    """(d_h [rows, 2 f], d_row_weights [rows], out [rows, f]) from what
+    grouped_swiglu_checkpoint_mxfp8 kept and the gradient d_out [rows, f] (bf16 or fp16; rows may be
+    strided) of its output.  d_row_weights: None without row_weights; out (the activation again, for
+    the second product's weight gradient): None unless recompute or given."""
+    import torch
+    lib = load_library()
+    code, dev = _in_16bit(d_out, "d_out"), _device_index(d_out, "d_out")
+    ldd, _ = _strided(d_out, "d_out", 2, d_out.dtype, dev)
+    rows, f = d_out.shape
+    if f % 32 != 0 or f == 0:
+        raise ValueError("d_out has %d columns, not a multiple of 32" % f)
+    d_h = _out_or_new(d_h, (rows, 2 * f), d_out.dtype, d_out, "d_h")
+    ldh, _ = _strided(d_h, "d_h", 2, d_out.dtype, dev)
+    ldo, optr = f, None
+    if recompute or out is not None:
+        out = _out_or_new(out, (rows, f), d_out.dtype, d_out)
+        ldo, _ = _strided(out, "out", 2, d_out.dtype, dev)
+        optr = out.data_ptr()
+    if row_weights is None:
+        d_row_weights = None
+    elif d_row_weights is None:
+        d_row_weights = d_out.new_empty(rows, dtype=torch.float32)
+    args = (_dense(data, "data", rows * 2 * f, torch.uint8, dev),
+            _dense(scales, "scales", rows * (f // 16), torch.uint8, dev),
+            _maybe(row_weights, "row_weights", 4 * rows, torch.float32, dev), d_out.data_ptr(), ldd,
+            offsets.numel() - 1, _dense(offsets, "offsets", 16, torch.int64, dev), rows, f,
+            d_h.data_ptr(), ldh, optr, ldo,
+            _maybe(d_row_weights, "d_row_weights", 4 * rows, torch.float32, dev), _status(status, dev))
+    if rows:
+        _launch(lib.grouped_swiglu_checkpoint_mxfp8_backward, dev, code, *args)
+    return d_h, d_row_weights, out

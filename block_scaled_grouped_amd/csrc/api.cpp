@@ -834,4 +834,298 @@ int clip_grad_norm(const void* plan, int64_t num_chunks, float max_norm, const d
                     fn);
 }
 
+size_t moe_router_topk_workspace_size(int64_t tokens, int64_t E) {
+  if (tokens < 0 || tokens >= ((int64_t)1 << 31) || E < 1 || E > BSG_MAX_GROUPS) return 0;
+  return bsg::router_workspace_bytes(E);
+}
+
+namespace {
+
+size_t in_bytes(int dtype) { return dtype == BSG_IN_F32 ? 4 : 2; }
+
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+int check_router(const char* fn, int in_dtype, const void* logits, int64_t ld, int64_t tokens,
+                 int64_t E, int64_t top_k, int normalize) {
+  if (in_dtype != BSG_IN_BF16 && in_dtype != BSG_IN_F16 && in_dtype != BSG_IN_F32)
+    return fail(BSG_ERR_UNSUPPORTED, "%s: in_dtype %d", fn, in_dtype);
+  if (normalize != 0 && normalize != 1)
+    return fail(BSG_ERR_UNSUPPORTED, "%s: normalize must be 0 or 1", fn);
+  if (tokens < 0 || tokens >= ((int64_t)1 << 31))
+    return fail(BSG_ERR_SHAPE, "%s: tokens=%lld outside [0, 2^31)", fn, (long long)tokens);
+  if (E < 1 || E > BSG_MAX_GROUPS)
+    return fail(BSG_ERR_SHAPE, "%s: E=%lld outside [1, %d]", fn, (long long)E, BSG_MAX_GROUPS);
+  if (top_k < 1 || top_k > E || top_k > BSG_MAX_TOP_K)
+    return fail(BSG_ERR_SHAPE, "%s: top_k=%lld outside [1, min(E, %d)]", fn, (long long)top_k,
+                BSG_MAX_TOP_K);
+  if (ld < E || ld > kMaxRowStride)
+    return fail(BSG_ERR_SHAPE, "%s: row stride %lld outside [E, %lld]", fn, (long long)ld,
+                (long long)kMaxRowStride);
+  if (!aligned_to(logits, in_bytes(in_dtype)))
+    return fail(BSG_ERR_ALIGN, "%s: logits must be aligned to their elements", fn);
+  return BSG_OK;
+}
+
+}  // namespace
+
+int moe_router_topk(int in_dtype, const void* logits, int64_t ld, int64_t tokens, int64_t E,
+                    int64_t top_k, const uint8_t* mask, int normalize, int32_t* experts,
+                    float* weights, int32_t* counts, float* prob_sums, int32_t* live, float* loss,
+                    void* workspace, size_t workspace_bytes, uint32_t* dev_status, void* stream) {
+  const char* fn = "moe_router_topk";
+  if (counts == nullptr || prob_sums == nullptr || live == nullptr || loss == nullptr ||
+      workspace == nullptr || (tokens != 0 && (logits == nullptr || experts == nullptr ||
+                                               weights == nullptr)))
+    return fail(BSG_ERR_NULL, "%s: every buffer but mask and dev_status must be non-NULL", fn);
+  const int c = check_router(fn, in_dtype, logits, ld, tokens, E, top_k, normalize);
+  if (c != BSG_OK) return c;
+  if (!aligned4(experts) || !aligned4(weights) || !aligned4(counts) || !aligned4(prob_sums) ||
+      !aligned4(live) || !aligned4(loss) || !aligned16(workspace))
+    return fail(BSG_ERR_ALIGN, "%s: outputs must be 4-byte and workspace 16-byte aligned", fn);
+  const size_t need = bsg::router_workspace_bytes(E);
+  if (workspace_bytes < need)
+    return fail(BSG_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes,
+                need);
+  return hip_result(bsg::launch_router(in_dtype, logits, ld, tokens, (int)E, (int)top_k, mask,
+                                       normalize, experts, weights, counts, prob_sums, live, loss,
+                                       workspace, dev_status, (hipStream_t)stream),
+                    fn);
+}
+
+int moe_router_topk_backward(int in_dtype, const void* logits, int64_t ld, int64_t tokens,
+                             int64_t E, int64_t top_k, const uint8_t* mask, int normalize,
+                             const int32_t* experts, const float* d_weights,
+                             const int32_t* counts, const int32_t* live, const float* d_loss,
+                             void* d_logits, int64_t ldo, void* stream) {
+  const char* fn = "moe_router_topk_backward";
+  if (logits == nullptr || experts == nullptr || counts == nullptr || live == nullptr ||
+      d_logits == nullptr)
+    return fail(BSG_ERR_NULL, "%s: logits, experts, counts, live and d_logits must be non-NULL", fn);
+  const int c = check_router(fn, in_dtype, logits, ld, tokens, E, top_k, normalize);
+  if (c != BSG_OK) return c;
+  if (ldo < E || ldo > kMaxRowStride)
+    return fail(BSG_ERR_SHAPE, "%s: ldo=%lld outside [E, %lld]", fn, (long long)ldo,
+                (long long)kMaxRowStride);
+  if (!aligned_to(d_logits, in_bytes(in_dtype)) || !aligned4(experts) || !aligned4(d_weights) ||
+      !aligned4(counts) || !aligned4(live) || !aligned4(d_loss))
+    return fail(BSG_ERR_ALIGN, "%s: buffers must be aligned to their elements", fn);
+  return hip_result(bsg::launch_router_backward(in_dtype, logits, ld, tokens, (int)E, (int)top_k,
+                                                mask, normalize, experts, d_weights, counts, live,
+                                                d_loss, d_logits, ldo, (hipStream_t)stream),
+                    fn);
+}
+
+namespace {
+
+bool byte_stride_ok(int64_t ld, int64_t cols) {
+  return ld >= cols && ld % 16 == 0 && ld <= kMaxRowStride;
+}
+
+bool int8_k_ok(int64_t k) { return k > 0 && k % 16 == 0 && k <= BSG_MAX_INT8_K; }
+
+int check_16bit_in(const char* fn, int in_dtype) {
+  if (in_dtype != BSG_IN_BF16 && in_dtype != BSG_IN_F16)
+    return fail(BSG_ERR_UNSUPPORTED, "%s: in_dtype %d", fn, in_dtype);
+  return BSG_OK;
+}
+
+// What the products with integers and with 16-bit tokens share.
+int check_int8_product(const char* fn, int64_t G, const void* b, int64_t ldb, int64_t stride_b,
+                       const void* b_scales, int64_t rows_cap, int64_t n, int64_t k,
+                       const void* out, int64_t ldo, int out_dtype) {
+  if (out_dtype != BSG_OUT_BF16 && out_dtype != BSG_OUT_F16 && out_dtype != BSG_OUT_F32)
+    return fail(BSG_ERR_UNSUPPORTED, "%s: out_dtype %d", fn, out_dtype);
+  if (G < 1 || G > BSG_MAX_GROUPS)
+    return fail(BSG_ERR_SHAPE, "%s: G=%lld outside [1, %d]", fn, (long long)G, BSG_MAX_GROUPS);
+  if (rows_cap < 0 || rows_cap >= ((int64_t)1 << 31) || n <= 0 || n % 8 != 0 || !int8_k_ok(k))
+    return fail(BSG_ERR_SHAPE,
+                "%s: need 0 <= rows_cap < 2^31, n a positive multiple of 8 and k one of 16 up to "
+                "%d (got %lld, %lld, %lld)",
+                fn, BSG_MAX_INT8_K, (long long)rows_cap, (long long)n, (long long)k);
+  if (!byte_stride_ok(ldb, k) || !row_stride_ok(ldo, n))
+    return fail(BSG_ERR_SHAPE, "%s: ldb=%lld (16s) or ldo=%lld (8s) outside [row length, %lld]", fn,
+                (long long)ldb, (long long)ldo, (long long)kMaxRowStride);
+  if (G > 1 && (stride_b % 16 != 0 || stride_b < (n - 1) * ldb + k))
+    return fail(BSG_ERR_SHAPE, "%s: stride_b=%lld overlaps the groups or is no multiple of 16", fn,
+                (long long)stride_b);
+  if (!tiles_ok(false, G, rows_cap, n, k))
+    return fail(BSG_ERR_SHAPE, "%s: too many output tiles", fn);
+  if (!aligned16(b) || !aligned16(out) || !aligned16(b_scales))
+    return fail(BSG_ERR_ALIGN, "%s: b, b_scales and out must be 16-byte aligned", fn);
+  return BSG_OK;
+}
+
+}  // namespace
+
+int grouped_quantize_int8(int in_dtype, const void* x, int64_t ldx, int64_t rows_cap, int64_t cols,
+                          int64_t G, const int64_t* offsets, int8_t* data, float* scales,
+                          uint32_t* dev_status, void* stream) {
+  const char* fn = "grouped_quantize_int8";
+  if (x == nullptr || data == nullptr || scales == nullptr)
+    return fail(BSG_ERR_NULL, "%s: x, data and scales must be non-NULL", fn);
+  const int tc = check_16bit_in(fn, in_dtype);
+  if (tc != BSG_OK) return tc;
+  if (offsets != nullptr && (G < 1 || G > BSG_MAX_GROUPS))
+    return fail(BSG_ERR_SHAPE, "%s: G=%lld outside [1, %d]", fn, (long long)G, BSG_MAX_GROUPS);
+  if (rows_cap < 0 || rows_cap >= ((int64_t)1 << 31) || !int8_k_ok(cols))
+    return fail(BSG_ERR_SHAPE,
+                "%s: need 0 <= rows_cap < 2^31 and cols a positive multiple of 16 up to %d (got "
+                "%lld, %lld)",
+                fn, BSG_MAX_INT8_K, (long long)rows_cap, (long long)cols);
+  if (!row_stride_ok(ldx, cols))
+    return fail(BSG_ERR_SHAPE, "%s: ldx=%lld must be a multiple of 8 in [cols, %lld]", fn,
+                (long long)ldx, (long long)kMaxRowStride);
+  if (!aligned16(x) || !aligned16(data) || !aligned4(scales))
+    return fail(BSG_ERR_ALIGN, "%s: x and data must be 16-byte and scales 4-byte aligned", fn);
+  return hip_result(bsg::launch_quantize_int8(in_dtype == BSG_IN_F16, x, ldx, rows_cap, cols, (int)G,
+                                              offsets, data, scales, dev_status,
+                                              (hipStream_t)stream),
+                    fn);
+}
+
+size_t grouped_gemm_int8_workspace_size(void) { return bsg::gemm_16bit_workspace_bytes(); }
+
+int grouped_gemm_int8_tile_rows(int64_t G, int64_t rows_cap, int64_t n, int64_t k,
+                                int with_workspace) {
+  if (G < 1 || G > BSG_MAX_GROUPS || rows_cap < 0 || rows_cap >= ((int64_t)1 << 31) || n <= 0 ||
+      !row_stride_ok(n, n) || !int8_k_ok(k) || !tiles_ok(false, G, rows_cap, n, k))
+    return 0;
+  return bsg::gemm_int8_tile_rows(G, rows_cap, n, k, with_workspace != 0);
+}
+
+int grouped_gemm_int8(int64_t G, const int8_t* a, int64_t lda, const float* a_scales,
+                      const int8_t* b, int64_t ldb, int64_t stride_b, const float* b_scales,
+                      const int64_t* offsets, int64_t rows_cap, int64_t n, int64_t k, void* out,
+                      int64_t ldo, int out_dtype, void* workspace, size_t workspace_bytes,
+                      uint32_t* dev_status, void* stream) {
+  const char* fn = "grouped_gemm_int8";
+  if (a == nullptr || a_scales == nullptr || b == nullptr || b_scales == nullptr ||
+      offsets == nullptr || out == nullptr)
+    return fail(BSG_ERR_NULL, "%s: operands, scales, offsets and out must be non-NULL", fn);
+  const int c = check_int8_product(fn, G, b, ldb, stride_b, b_scales, rows_cap, n, k, out, ldo,
+                                   out_dtype);
+  if (c != BSG_OK) return c;
+  if (!byte_stride_ok(lda, k))
+    return fail(BSG_ERR_SHAPE, "%s: lda=%lld must be a multiple of 16 in [k, %lld]", fn,
+                (long long)lda, (long long)kMaxRowStride);
+  if (!aligned16(a) || !aligned4(a_scales))
+    return fail(BSG_ERR_ALIGN, "%s: a must be 16-byte and a_scales 4-byte aligned", fn);
+  if (workspace != nullptr) {
+    const int wc = check_16bit_workspace(fn, workspace, workspace_bytes,
+                                         bsg::gemm_16bit_workspace_bytes());
+    if (wc != BSG_OK) return wc;
+  }
+  return hip_result(bsg::launch_gemm_int8((int)G, a, lda, a_scales, b, ldb, stride_b, b_scales,
+                                          offsets, rows_cap, n, k, out, ldo,
+                                          out_dtype == BSG_OUT_F16, out_dtype == BSG_OUT_F32,
+                                          workspace, dev_status, (hipStream_t)stream),
+                    fn);
+}
+
+size_t grouped_gemm_int8_dynamic_workspace_size(int64_t rows_cap, int64_t k) {
+  if (rows_cap < 0 || rows_cap >= ((int64_t)1 << 31) || k < 0 || k > BSG_MAX_INT8_K) return 0;
+  return bsg::gemm_int8_dynamic_workspace_bytes(rows_cap, k);
+}
+
+int grouped_gemm_int8_dynamic(int in_dtype, int64_t G, const void* x, int64_t ldx, const int8_t* b,
+                              int64_t ldb, int64_t stride_b, const float* b_scales,
+                              const int64_t* offsets, int64_t rows_cap, int64_t n, int64_t k,
+                              void* out, int64_t ldo, int out_dtype, void* workspace,
+                              size_t workspace_bytes, uint32_t* dev_status, void* stream) {
+  const char* fn = "grouped_gemm_int8_dynamic";
+  if (x == nullptr || b == nullptr || b_scales == nullptr || offsets == nullptr || out == nullptr ||
+      workspace == nullptr)
+    return fail(BSG_ERR_NULL, "%s: every buffer but dev_status must be non-NULL", fn);
+  const int tc = check_16bit_in(fn, in_dtype);
+  if (tc != BSG_OK) return tc;
+  const int c = check_int8_product(fn, G, b, ldb, stride_b, b_scales, rows_cap, n, k, out, ldo,
+                                   out_dtype);
+  if (c != BSG_OK) return c;
+  if (!row_stride_ok(ldx, k))
+    return fail(BSG_ERR_SHAPE, "%s: ldx=%lld must be a multiple of 8 in [k, %lld]", fn,
+                (long long)ldx, (long long)kMaxRowStride);
+  if (!aligned16(x)) return fail(BSG_ERR_ALIGN, "%s: x must be 16-byte aligned", fn);
+  const int wc = check_16bit_workspace(fn, workspace, workspace_bytes,
+                                       bsg::gemm_int8_dynamic_workspace_bytes(rows_cap, k));
+  if (wc != BSG_OK) return wc;
+  return hip_result(
+      bsg::launch_gemm_int8_dynamic(in_dtype == BSG_IN_F16, (int)G, x, ldx, b, ldb, stride_b,
+                                    b_scales, offsets, rows_cap, n, k, out, ldo,
+                                    out_dtype == BSG_OUT_F16, out_dtype == BSG_OUT_F32, workspace,
+                                    dev_status, (hipStream_t)stream),
+      fn);
+}
+
+namespace {
+
+int check_swiglu(const char* fn, int in_dtype, int64_t G, int64_t rows_cap, int64_t f) {
+  const int tc = check_16bit_in(fn, in_dtype);
+  if (tc != BSG_OK) return tc;
+  if (G < 1 || G > BSG_MAX_GROUPS)
+    return fail(BSG_ERR_SHAPE, "%s: G=%lld outside [1, %d]", fn, (long long)G, BSG_MAX_GROUPS);
+  if (rows_cap < 0 || rows_cap >= ((int64_t)1 << 31) || f <= 0 || f % 32 != 0 ||
+      2 * f > kMaxRowStride)
+    return fail(BSG_ERR_SHAPE,
+                "%s: need 0 <= rows_cap < 2^31 and f a positive multiple of 32 up to %lld (got %lld, "
+                "%lld)",
+                fn, (long long)(kMaxRowStride / 2), (long long)rows_cap, (long long)f);
+  return BSG_OK;
+}
+
+}  // namespace
+
+int grouped_swiglu_checkpoint_mxfp8(int in_dtype, const void* h, int64_t ldh,
+                                    const float* row_weights, int64_t G, const int64_t* offsets,
+                                    int64_t rows_cap, int64_t f, void* out, int64_t ldo,
+                                    uint8_t* data, uint8_t* scales, uint32_t* dev_status,
+                                    void* stream) {
+  const char* fn = "grouped_swiglu_checkpoint_mxfp8";
+  if (h == nullptr || offsets == nullptr || out == nullptr)
+    return fail(BSG_ERR_NULL, "%s: h, offsets and out must be non-NULL", fn);
+  if ((data == nullptr) != (scales == nullptr))
+    return fail(BSG_ERR_NULL, "%s: data and scales go together", fn);
+  const int c = check_swiglu(fn, in_dtype, G, rows_cap, f);
+  if (c != BSG_OK) return c;
+  if (!row_stride_ok(ldh, 2 * f) || !row_stride_ok(ldo, f))
+    return fail(BSG_ERR_SHAPE, "%s: ldh=%lld, ldo=%lld must be multiples of 8 in [row length, %lld]",
+                fn, (long long)ldh, (long long)ldo, (long long)kMaxRowStride);
+  if (!aligned16(h) || !aligned16(out) || !aligned16(data) || !aligned4(row_weights))
+    return fail(BSG_ERR_ALIGN, "%s: h, out and data must be 16-byte and row_weights 4-byte aligned",
+                fn);
+  return hip_result(bsg::launch_swiglu_checkpoint(in_dtype == BSG_IN_F16, h, ldh, row_weights,
+                                                  (int)G, offsets, rows_cap, f, out, ldo, data,
+                                                  scales, dev_status, (hipStream_t)stream),
+                    fn);
+}
+
+int grouped_swiglu_checkpoint_mxfp8_backward(int in_dtype, const uint8_t* data,
+                                             const uint8_t* scales, const float* row_weights,
+                                             const void* d_out, int64_t ldd, int64_t G,
+                                             const int64_t* offsets, int64_t rows_cap, int64_t f,
+                                             void* d_h, int64_t ldh, void* out, int64_t ldo,
+                                             float* d_row_weights, uint32_t* dev_status,
+                                             void* stream) {
+  const char* fn = "grouped_swiglu_checkpoint_mxfp8_backward";
+  if (data == nullptr || scales == nullptr || d_out == nullptr || offsets == nullptr ||
+      d_h == nullptr)
+    return fail(BSG_ERR_NULL, "%s: data, scales, d_out, offsets and d_h must be non-NULL", fn);
+  const int c = check_swiglu(fn, in_dtype, G, rows_cap, f);
+  if (c != BSG_OK) return c;
+  if (!row_stride_ok(ldd, f) || !row_stride_ok(ldh, 2 * f) ||
+      (out != nullptr && !row_stride_ok(ldo, f)))
+    return fail(BSG_ERR_SHAPE,
+                "%s: ldd=%lld, ldh=%lld, ldo=%lld must be multiples of 8 in [row length, %lld]", fn,
+                (long long)ldd, (long long)ldh, (long long)ldo, (long long)kMaxRowStride);
+  if (!aligned16(data) || !aligned16(d_out) || !aligned16(d_h) || !aligned16(out) ||
+      !aligned4(row_weights) || !aligned4(d_row_weights))
+    return fail(BSG_ERR_ALIGN, "%s: 16-bit tensors and data must be 16-byte aligned, float32 ones "
+                "4-byte", fn);
+  return hip_result(
+      bsg::launch_swiglu_checkpoint_backward(in_dtype == BSG_IN_F16, data, scales, row_weights,
+                                             d_out, ldd, (int)G, offsets, rows_cap, f, d_h, ldh,
+                                             out, ldo, d_row_weights, dev_status,
+                                             (hipStream_t)stream),
+      fn);
+}
+
 }  // extern "C"

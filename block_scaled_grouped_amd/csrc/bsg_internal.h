@@ -297,6 +297,57 @@ hipError_t launch_clip_grad_norm(const GradChunk* plan, int64_t num_chunks, floa
                                  const double* sumsq, double* partials, float* norm,
                                  uint32_t* status, hipStream_t stream);
 
+// Workspace of a router's forward pass over E experts.
+size_t router_workspace_bytes(int64_t E);
+
+// dtype: 0 bf16, 1 fp16, 2 float32 (bsg_in_dtype); ld in elements.
+hipError_t launch_router(int dtype, const void* logits, int64_t ld, int64_t tokens, int E, int k,
+                         const uint8_t* mask, int normalize, int32_t* experts, float* weights,
+                         int32_t* counts, float* prob_sums, int32_t* live, float* loss, void* ws,
+                         uint32_t* status, hipStream_t stream);
+
+hipError_t launch_router_backward(int dtype, const void* logits, int64_t ld, int64_t tokens, int E,
+                                  int k, const uint8_t* mask, int normalize, const int32_t* experts,
+                                  const float* d_weights, const int32_t* counts,
+                                  const int32_t* live, const float* d_loss, void* out, int64_t ldo,
+                                  hipStream_t stream);
+
+// offsets null: all rows.
+hipError_t launch_quantize_int8(int f16, const void* x, int64_t ldx, int64_t rows_cap, int64_t cols,
+                                int G, const int64_t* offsets, int8_t* data, float* scales,
+                                uint32_t* status, hipStream_t stream);
+
+// f16: the type of a 16-bit output.  Strides in elements.  ws: of gemm_16bit_workspace_bytes()
+// or null.
+hipError_t launch_gemm_int8(int G, const int8_t* a, int64_t lda, const float* a_scales,
+                            const int8_t* b, int64_t ldb, int64_t stride_b, const float* b_scales,
+                            const int64_t* offsets, int64_t rows_cap, int64_t n, int64_t k,
+                            void* out, int64_t ldo, int f16, int out_f32, void* ws,
+                            uint32_t* status, hipStream_t stream);
+
+// The workspace of 16-bit tokens' calls holds their integers and scales too.
+size_t gemm_int8_dynamic_workspace_bytes(int64_t rows_cap, int64_t k);
+
+hipError_t launch_gemm_int8_dynamic(int in_f16, int G, const void* x, int64_t ldx, const int8_t* b,
+                                    int64_t ldb, int64_t stride_b, const float* b_scales,
+                                    const int64_t* offsets, int64_t rows_cap, int64_t n, int64_t k,
+                                    void* out, int64_t ldo, int f16, int out_f32, void* ws,
+                                    uint32_t* status, hipStream_t stream);
+
+int gemm_int8_tile_rows(int64_t G, int64_t rows_cap, int64_t n, int64_t k, bool split);
+
+// data and scales null: nothing is kept.
+hipError_t launch_swiglu_checkpoint(int f16, const void* h, int64_t ldh, const float* w, int G,
+                                    const int64_t* offsets, int64_t rows_cap, int64_t f, void* y,
+                                    int64_t ldy, uint8_t* data, uint8_t* scales, uint32_t* status,
+                                    hipStream_t stream);
+
+hipError_t launch_swiglu_checkpoint_backward(int f16, const uint8_t* data, const uint8_t* scales,
+                                             const float* w, const void* dy, int64_t lddy, int G,
+                                             const int64_t* offsets, int64_t rows_cap, int64_t f,
+                                             void* dh, int64_t lddh, void* y, int64_t ldy,
+                                             float* dw, uint32_t* status, hipStream_t stream);
+
 int device_cu_count();
 
 }  // namespace bsg

@@ -56,7 +56,7 @@ constexpr int kLowParts = 4;             // of the adapters' first product, wher
 constexpr int kLowValues = 3;            // 16-bit values that carry a sum of it to the second
 constexpr int kLowChunk = 64;            // rank columns that share a row's power of two
 
-enum Mode { kFprop = 0, kWgrad = 1, kDgrad = 2, kLora = 3 };
+enum Mode { kFprop = 0, kWgrad = 1, kDgrad = 2, kLora = 3, kInt8 = 4 };
 template <int MODE> constexpr bool kColsA = MODE == kWgrad;
 template <int MODE> constexpr bool kColsB = MODE == kWgrad || MODE == kDgrad;
 
@@ -114,6 +114,9 @@ struct Args {
   const uint16_t* up;      // [adapters, n, r]
   const int32_t* adapter;  // [G], negative: none
   int num_adapters, r;
+  // INT8
+  const float* a_scales;   // [rows_cap]
+  const float* b_scales;   // [G, n]
 };
 
 struct Sched {
@@ -129,8 +132,8 @@ struct Tile {
   int a_rows, b_rows;  // live rows (those past them read as zeros)
   int kl;              // contraction length
   int64_t out_off;     // bytes from out (and c) to the tile's first element
-  int64_t row0;        // LORA: first row
-  int64_t col0;        // LORA: first column
+  int64_t row0;        // LORA, INT8: first row
+  int64_t col0;        // LORA: first column; INT8: of all groups' columns
 };
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -249,7 +252,7 @@ __device__ __forceinline__ Tile find_tile(const Args& p, const Sched& sm, int ti
     t.kl = (int)p.k;
     t.out_off = ((first + r0) * p.ldo + n0) * esz;
     t.row0 = first + r0;
-    t.col0 = n0;
+    t.col0 = MODE == kInt8 ? g * p.n + n0 : n0;
   }
   t.lda = p.lda;
   t.ldb = p.ldb;
@@ -425,6 +428,15 @@ __device__ __forceinline__ v4f mfma16(const v4i& x, const v4i& y, const v4f& acc
   else
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x),
                                                    __builtin_bit_cast(v8bf, y), acc, 0, 0, 0);
+}
+
+template <int MODE, bool F16>
+__device__ __forceinline__ v4f mfma_step(const v4i& x, const v4i& y, const v4f& acc) {
+  if constexpr (MODE == kInt8)
+    return __builtin_bit_cast(
+        v4f, __builtin_amdgcn_mfma_i32_16x16x64_i8(x, y, __builtin_bit_cast(v4i, acc), 0, 0, 0));
+  else
+    return mfma16<F16>(x, y, acc);
 }
 
 // ---------------------------------------------------------------- adapters
@@ -701,6 +713,8 @@ struct OutTile {
   char* out;
   const char* c;  // or null
   int ldo, rows, cols;
+  const float* a_scales;  // INT8: of the tile's rows
+  const float* b_scales;  // INT8: of its columns
 };
 
 // This lane's byte offset of a block's columns 4 q + [0, 4) in an output tile: a
@@ -761,7 +775,9 @@ __device__ __forceinline__ void store_pair(const v4f& y0, const v4f& y1, __amdgp
 // A wave's MI x NJ blocks, the first at (wrow, wcol) of the tile, two at a time: the
 // accumulators are copied out right before their stores.  The addend, if there is
 // one, is added in float32 before the one rounding, and read a row of blocks ahead.
-template <bool F16, bool F32, bool ADD, int MI, int NJ>
+// INT8: a sum becomes a float32 number (one rounding), is multiplied by its row's scale,
+// then by its column's.
+template <int MODE, bool F16, bool F32, bool ADD, int MI, int NJ>
 __device__ __forceinline__ void store_rows(const v4f (&acc)[MI][NJ], const OutTile& o, int wrow,
                                            int wcol, int lane) {
   static_assert(NJ % 2 == 0, "blocks are stored in pairs");
@@ -771,6 +787,20 @@ __device__ __forceinline__ void store_rows(const v4f (&acc)[MI][NJ], const OutTi
   const __amdgpu_buffer_rsrc_t ro = make_rsrc(o.out, (int64_t)o.rows * o.ldo * esz);
   const __amdgpu_buffer_rsrc_t rc = make_rsrc(o.c, ADD ? (int64_t)o.rows * o.ldo * esz : 0);
   const int q = lane >> 4, row = wrow + (lane & 15);
+  v4f cscale[NJ];
+  float rscale[MI];
+  if constexpr (MODE == kInt8) {
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(o.a_scales, (int64_t)o.rows * 4);
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(o.b_scales, (int64_t)o.cols * 4);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      cscale[j] = __builtin_bit_cast(
+          v4f, __builtin_amdgcn_raw_buffer_load_b128(rb, 4 * (wcol + 16 * j + 4 * q), 0, 0));
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+      rscale[i] = __builtin_bit_cast(
+          float, __builtin_amdgcn_raw_buffer_load_b32(ra, 4 * (row + 16 * i), 0, 0));
+  }
   Addend<F32> c[2][NJ];
   if constexpr (ADD) {
 #pragma unroll
@@ -792,6 +822,14 @@ __device__ __forceinline__ void store_rows(const v4f (&acc)[MI][NJ], const OutTi
       fence();
       v4f y0 = acc[i][j], y1 = acc[i][j + 1];
       asm volatile("" : "+v"(y0), "+v"(y1));
+      if constexpr (MODE == kInt8) {
+        const v4i s0 = __builtin_bit_cast(v4i, y0), s1 = __builtin_bit_cast(v4i, y1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y0[e] = ((float)s0[e] * rscale[i]) * cscale[j][e];
+          y1[e] = ((float)s1[e] * rscale[i]) * cscale[j + 1][e];
+        }
+      }
       if constexpr (ADD) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -805,15 +843,15 @@ __device__ __forceinline__ void store_rows(const v4f (&acc)[MI][NJ], const OutTi
   }
 }
 
-template <bool F16, int MI, int NJ>
+template <int MODE, bool F16, int MI, int NJ>
 __device__ __forceinline__ void store_blocks(const v4f (&acc)[MI][NJ], const OutTile& o,
                                              int out_f32, int wrow, int wcol, int lane) {
-  if (o.c != nullptr) {
-    if (out_f32) store_rows<F16, true, true>(acc, o, wrow, wcol, lane);
-    else store_rows<F16, false, true>(acc, o, wrow, wcol, lane);
+  if (MODE != kInt8 && o.c != nullptr) {
+    if (out_f32) store_rows<MODE, F16, true, true>(acc, o, wrow, wcol, lane);
+    else store_rows<MODE, F16, false, true>(acc, o, wrow, wcol, lane);
   } else {
-    if (out_f32) store_rows<F16, true, false>(acc, o, wrow, wcol, lane);
-    else store_rows<F16, false, false>(acc, o, wrow, wcol, lane);
+    if (out_f32) store_rows<MODE, F16, true, false>(acc, o, wrow, wcol, lane);
+    else store_rows<MODE, F16, false, false>(acc, o, wrow, wcol, lane);
   }
 }
 
@@ -835,8 +873,8 @@ constexpr int kMaxSplitTiles = (int)((kWsHeader - 64) / 32);
 
 struct SplitRecord {
   int64_t out_off;
-  int32_t rows, cols, pad0, pad1;
-  int64_t pad2;
+  int32_t rows, cols;
+  int64_t row0, col0;  // INT8
 };
 static_assert(sizeof(SplitRecord) == 32, "records fill the header");
 
@@ -916,12 +954,17 @@ __device__ __forceinline__ Work take_work(const Args& p, const Rounds& r, int ro
   return k;
 }
 
+template <int MODE>
 __device__ __forceinline__ void write_split_record(char* ws, int slot, int nsplit, const Tile& t) {
   if (threadIdx.x == 0) {
     SplitRecord* rec = reinterpret_cast<SplitRecord*>(ws + 64) + slot / nsplit;
     rec->out_off = t.out_off;
     rec->rows = t.a_rows;
     rec->cols = t.b_rows;
+    if constexpr (MODE == kInt8) {
+      rec->row0 = t.row0;
+      rec->col0 = t.col0;
+    }
   }
 }
 
@@ -956,10 +999,12 @@ __device__ __forceinline__ void store_part(float* __restrict__ part, const v4f (
 }
 
 // The second step of a split: wave by wave one pair of blocks of a split tile.
-template <bool F16, int BM, int BN, int WN, int MI, int NJ>
+template <bool I8, bool F16, int BM, int BN, int WN, int MI, int NJ>
 __global__ __launch_bounds__(kThreads) void split_reduce_kernel(const char* __restrict__ ws,
                                                                 char* out, const char* c,
-                                                                int64_t ldo, int out_f32) {
+                                                                int64_t ldo, int out_f32,
+                                                                const float* a_scales,
+                                                                const float* b_scales) {
   constexpr int kUnits = BM * BN / 512;
   const int32_t* hdr = reinterpret_cast<const int32_t*>(ws);
   const int nl = hdr[0], nsplit = hdr[1];
@@ -985,7 +1030,12 @@ __global__ __launch_bounds__(kThreads) void split_reduce_kernel(const char* __re
         for (int b = 0; b < 2; ++b) {
           const v4f v = *reinterpret_cast<const v4f*>(src + (int64_t)s * (BM * BN) + 256 * b);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[0][b][e] += v[e];
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (I8)
+              y[0][b][e] = __int_as_float(__float_as_int(y[0][b][e]) + __float_as_int(v[e]));
+            else
+              y[0][b][e] += v[e];
+          }
         }
       }
     }
@@ -995,7 +1045,9 @@ __global__ __launch_bounds__(kThreads) void split_reduce_kernel(const char* __re
     o.ldo = (int)ldo;
     o.rows = rec.rows;
     o.cols = rec.cols;
-    store_blocks<F16, 1, 2>(y, o, out_f32, wrow, wcol, lane);
+    o.a_scales = I8 ? a_scales + rec.row0 : nullptr;
+    o.b_scales = I8 ? b_scales + rec.col0 : nullptr;
+    store_blocks<I8 ? kInt8 : kFprop, F16, 1, 2>(y, o, out_f32, wrow, wcol, lane);
   }
 }
 
@@ -1027,6 +1079,7 @@ int prepare_launch(Args& p, int slots) {
   return grid;
 }
 
+template <int MODE>
 __device__ __forceinline__ OutTile out_tile(const Args& p, const Tile& t) {
   OutTile o;
   o.out = p.out + t.out_off;
@@ -1034,6 +1087,8 @@ __device__ __forceinline__ OutTile out_tile(const Args& p, const Tile& t) {
   o.ldo = (int)p.ldo;
   o.rows = t.a_rows;
   o.cols = t.b_rows;
+  o.a_scales = MODE == kInt8 ? p.a_scales + t.row0 : nullptr;
+  o.b_scales = MODE == kInt8 ? p.b_scales + t.col0 : nullptr;
   return o;
 }
 
@@ -1041,8 +1096,13 @@ __device__ __forceinline__ OutTile out_tile(const Args& p, const Tile& t) {
 
 hipError_t launch_large(int mode, int f16, const Args& p, hipStream_t stream);
 hipError_t launch_small(int mode, int f16, int bm, const Args& p, hipStream_t stream);
+hipError_t launch_large_int8(int f16, const Args& p, hipStream_t stream);
+hipError_t launch_small_int8(int f16, int bm, const Args& p, hipStream_t stream);
 size_t large_workspace_bytes();
 size_t small_workspace_bytes();
+
+// Rows of the tiles of the form that a call takes.
+int form_rows(int mode, int64_t G, int64_t rows_cap, int64_t n, int64_t k, bool split);
 
 }  // namespace g16
 }  // namespace bsg

@@ -256,6 +256,15 @@ double expected_us(const Form& f, int mode, int64_t G, int64_t rows_cap, int64_t
   return us;
 }
 
+hipError_t launch_form(int mode, int f16, const Args& p, hipStream_t stream) {
+  const int bm = form_rows(mode, p.G, p.rows_cap, p.n, p.k, p.ws != nullptr);
+  return bm == 256 ? launch_large(mode, f16, p, stream) : launch_small(mode, f16, bm, p, stream);
+}
+
+}  // namespace
+
+namespace g16 {
+
 // Rows of the tiles of the form that a call takes.
 int form_rows(int mode, int64_t G, int64_t rows_cap, int64_t n, int64_t k, bool split) {
   int best = mode == kWgrad ? 2 : 0;  // weight gradients have no forms of fewer rows
@@ -270,12 +279,7 @@ int form_rows(int mode, int64_t G, int64_t rows_cap, int64_t n, int64_t k, bool 
   return kForms[best].bm;
 }
 
-hipError_t launch_form(int mode, int f16, const Args& p, hipStream_t stream) {
-  const int bm = form_rows(mode, p.G, p.rows_cap, p.n, p.k, p.ws != nullptr);
-  return bm == 256 ? launch_large(mode, f16, p, stream) : launch_small(mode, f16, bm, p, stream);
-}
-
-}  // namespace
+}  // namespace g16
 
 size_t gemm_16bit_workspace_bytes() {
   const size_t l = large_workspace_bytes(), s = small_workspace_bytes();

@@ -1,0 +1,633 @@
+// The router of a mixture of experts: each token's top k experts, their weights, the
+// tokens of each expert and a loss that balances them; and the gradient of the logits.
+//
+// With l the logits of a token that is routed (live), n the live tokens:
+//   p_e = exp(l_e - max l) / sum_i exp(l_i - max l)
+//   the k largest logits, ties to the lowest index; -inf and NaN are never chosen
+//   w_j = p_{e_j}, or, normalized, p_{e_j} / sum_i p_{e_i}
+//   c_e = how often e is chosen, S_e = sum of p_e over the live tokens
+//   loss = E / (k n^2) * sum_e c_e S_e
+// and backwards, with b_e = dloss * E c_e / (k n^2) (the counts are constants):
+//   unnormalized  a_e = b_e + sum_j dw_j [e_j = e],  dl_e = p_e (a_e - sum_i p_i a_i)
+//   normalized    dl_e = p_e (b_e - sum_i p_i b_i) + sum_j [e_j = e] w_j (dw_j - sum_i w_i dw_i)
+//
+// 16 lanes take a token, lane i the experts EPL i .. EPL i + EPL - 1, so that a wave
+// holds four tokens and reductions are lane moves within a row of 16 (DPP).
+//
+// The largest are found on 32-bit keys: the logit's bits, ordered as integers, with the
+// lowest eight replaced by 255 - index.  Keys differ, so the next largest below M is the
+// one with the largest key - M (unsigned: those at or above M come out smallest), which
+// takes a subtraction and half a three-way maximum each, and no search for an index.
+// A 16-bit logit has its bits above those eight.  A float32 one may share them with the
+// next in order: where that happens among a token's k + 1 largest the wave does it again,
+// on whole values.
+#include "bsg_internal.h"
+
+namespace bsg {
+
+namespace {
+
+constexpr int kLanes = 16;           // of a token
+constexpr int kMaxExperts = 256;
+constexpr int kFwdThreads = 1024;
+constexpr int kFwdTokens = kFwdThreads / kLanes;
+constexpr int kFwdWaves = kFwdThreads / 64;
+constexpr int kFwdBlocks = 256;      // at most
+constexpr int64_t kOneBlock = 256;   // tokens that one workgroup takes alone
+constexpr int kBwdThreads = 256;
+constexpr int kBwdTokens = kBwdThreads / kLanes;
+
+typedef __attribute__((address_space(1))) const char gchar;
+
+// ---------------------------------------------------------------- 16 lanes
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+
+// f over the 16 lanes, the same bits in all of them: f is commutative.
+template <typename F>
+__device__ __forceinline__ uint32_t reduce16(uint32_t v, F f) {
+  v = f(v, dpp<kXor1>(v));
+  v = f(v, dpp<kXor2>(v));
+  v = f(v, dpp<kHalfMirror>(v));
+  return f(v, dpp<kMirror>(v));
+}
+__device__ __forceinline__ uint32_t max16u(uint32_t v) {
+  return reduce16(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+__device__ __forceinline__ uint32_t min16u(uint32_t v) {
+  return reduce16(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+__device__ __forceinline__ float max16(float v) {
+  return __uint_as_float(reduce16(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+__device__ __forceinline__ float sum16(float v) {
+  return __uint_as_float(reduce16(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+// The 16 bits of a ballot that are this lane's token's.
+__device__ __forceinline__ uint32_t ballot16(bool b, int lane) {
+  return (uint32_t)(__ballot(b) >> (lane & 48)) & 0xffffu;
+}
+
+// ---------------------------------------------------------------- values
+
+// exp(x) for x <= 0 (or NaN), to float32's last bits: 2^y with y = x log2(e) in two parts,
+// the second to first order.
+__device__ __forceinline__ float exp_le0(float x) {
+  x = x < -150.0f ? -150.0f : x;
+  const float hi = 1.44269502162933349609375f, lo = 1.92596299112661746887e-8f;
+  const float y = x * hi;
+  const float rest = fmaf(x, lo, fmaf(x, hi, -y));
+  const float e = __builtin_amdgcn_exp2f(y);
+  return fmaf(e, rest * 0.693147182464599609375f, e);
+}
+
+// DT 0: bf16, 1: fp16, 2: float32.
+template <int DT> constexpr int kBytes = DT == 2 ? 4 : 2;
+template <int DT>
+__device__ __forceinline__ float decode16(uint32_t bits) {
+  if constexpr (DT == 1) return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+  return __uint_as_float(bits << 16);
+}
+template <int DT>
+__device__ __forceinline__ float load_one(const char* row, int e) {
+  const gchar* at = (const gchar*)(row) + (int64_t)e * kBytes<DT>;
+  if constexpr (DT == 2) return *reinterpret_cast<const __attribute__((address_space(1))) float*>(at);
+  return decode16<DT>(*reinterpret_cast<const __attribute__((address_space(1))) uint16_t*>(at));
+}
+
+// A row is aligned to its elements only; the hardware takes wide loads and stores at any.
+typedef v4i v4i_any __attribute__((aligned(2)));
+typedef v2i v2i_any __attribute__((aligned(2)));
+typedef int int_any __attribute__((aligned(2)));
+
+// Elements e0 .. e0 + EPL - 1 of a row of E; those past it are -inf.
+template <int DT, int EPL>
+__device__ __forceinline__ void load_row(const char* row, int e0, int E, float (&v)[EPL]) {
+  constexpr int bytes = EPL * kBytes<DT>;
+  if (e0 + EPL <= E) {
+    uint32_t w[(bytes + 3) / 4];
+    const gchar* at = (const gchar*)(row) + (int64_t)e0 * kBytes<DT>;
+    if constexpr (bytes >= 16) {
+#pragma unroll
+      for (int i = 0; i < bytes / 16; ++i) {
+        const v4i q = *reinterpret_cast<const __attribute__((address_space(1))) v4i_any*>(at + 16 * i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[4 * i + j] = (uint32_t)q[j];
+      }
+    } else if constexpr (bytes == 8) {
+      const v2i q = *reinterpret_cast<const __attribute__((address_space(1))) v2i_any*>(at);
+      w[0] = (uint32_t)q[0];
+      w[1] = (uint32_t)q[1];
+    } else if constexpr (bytes == 4) {
+      w[0] = (uint32_t)*reinterpret_cast<const __attribute__((address_space(1))) int_any*>(at);
+    } else {
+      w[0] = *reinterpret_cast<const __attribute__((address_space(1))) uint16_t*>(at);
+    }
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      if constexpr (DT == 2) v[j] = __uint_as_float(w[j]);
+      else v[j] = decode16<DT>((w[j >> 1] >> (16 * (j & 1))) & 0xffffu);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) v[j] = e0 + j < E ? load_one<DT>(row, e0 + j) : -INFINITY;
+  }
+}
+
+template <int DT, int EPL>
+__device__ __forceinline__ void store_row(char* row, int e0, int E, const float (&v)[EPL]) {
+  constexpr int words = DT == 2 ? EPL : (EPL + 1) / 2;
+  uint32_t w[words];
+#pragma unroll
+  for (int j = 0; j < words; ++j) {
+    if constexpr (DT == 2) w[j] = __float_as_uint(v[j]);
+    else w[j] = pack16<DT == 1>(v[2 * j], 2 * j + 1 < EPL ? v[(2 * j + 1) % EPL] : 0.0f);
+  }
+  typedef __attribute__((address_space(1))) char gout;
+  gout* at = (gout*)(row) + (int64_t)e0 * kBytes<DT>;
+  constexpr int bytes = EPL * kBytes<DT>;
+  if (e0 + EPL <= E) {
+    if constexpr (bytes >= 16) {
+#pragma unroll
+      for (int i = 0; i < bytes / 16; ++i)
+        *reinterpret_cast<__attribute__((address_space(1))) v4i_any*>(at + 16 * i) =
+            v4i{(int)w[4 * i], (int)w[4 * i + 1], (int)w[4 * i + 2], (int)w[4 * i + 3]};
+    } else if constexpr (bytes == 8) {
+      *reinterpret_cast<__attribute__((address_space(1))) v2i_any*>(at) = v2i{(int)w[0], (int)w[1]};
+    } else if constexpr (bytes == 4) {
+      *reinterpret_cast<__attribute__((address_space(1))) int_any*>(at) = (int)w[0];
+    } else {
+      *reinterpret_cast<__attribute__((address_space(1))) uint16_t*>(at) = (uint16_t)w[0];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      if (e0 + j >= E) continue;
+      if constexpr (DT == 2)
+        *reinterpret_cast<__attribute__((address_space(1))) uint32_t*>(at + 4 * j) = w[j];
+      else
+        *reinterpret_cast<__attribute__((address_space(1))) uint16_t*>(at + 2 * j) =
+            (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+    }
+  }
+}
+
+// A logit's bits ordered as unsigned integers; 0 for what is never chosen.  -0 orders as 0.
+__device__ __forceinline__ uint32_t order(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  const uint32_t o = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  return v > -INFINITY ? o : 0u;  // false for a NaN
+}
+
+template <int N>
+__device__ __forceinline__ uint32_t max_of(const uint32_t (&v)[N]) {
+  uint32_t m = v[0];
+#pragma unroll
+  for (int j = 1; j < N; ++j) m = m > v[j] ? m : v[j];
+  return m;
+}
+
+// This lane's of a token's k chosen experts (lane j: the j-th; -1: none).
+template <int DT, int EPL>
+__device__ __forceinline__ int choose(const float (&v)[EPL], int e0, int E, int k, int lane) {
+  const int slot = lane & (kLanes - 1);
+  uint32_t key[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const uint32_t o = order(v[j]);
+    key[j] = o != 0 ? (o & ~255u) | (uint32_t)(255 - (e0 + j)) : 0u;
+  }
+  uint32_t m = max16u(max_of(key));
+  int chosen = slot == 0 && m != 0 ? 255 - (int)(m & 255u) : -1;
+  bool close = false;
+  // float32: one more than is chosen, which shows whether the last is next to another
+  const int rounds = DT == 2 && k < E ? k + 1 : k;
+  for (int r = 1; r < rounds; ++r) {
+    uint32_t d[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) d[j] = key[j] - m;
+    const uint32_t next = m != 0 ? max16u(max_of(d)) + m : 0u;
+    if (DT == 2) close |= next != 0 && ((next ^ m) >> 8) == 0;
+    m = next;
+    if (slot == r && r < k && m != 0) chosen = 255 - (int)(m & 255u);
+  }
+  if (DT == 2 && __any(close)) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) key[j] = order(v[j]);
+    chosen = -1;
+    for (int r = 0; r < k; ++r) {
+      m = max16u(max_of(key));
+      uint32_t at = 0xffffu;
+#pragma unroll
+      for (int j = EPL - 1; j >= 0; --j) at = key[j] == m ? (uint32_t)(e0 + j) : at;
+      at = min16u(at);
+      if (slot == r && m != 0) chosen = (int)at;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) key[j] = (uint32_t)(e0 + j) == at ? 0u : key[j];
+    }
+  }
+  return chosen;
+}
+
+// ---------------------------------------------------------------- forward
+
+struct Fwd {
+  const char* logits;
+  int64_t ld, tokens;  // ld in bytes
+  const uint8_t* mask;
+  int E, k, normalize;
+  int32_t* experts;
+  float* weights;
+  int32_t* counts;
+  float* prob_sums;
+  int32_t* live;
+  float* loss;
+  uint32_t* status;
+  // workspace: of each workgroup S_e [E] and c_e [E] and its live tokens; then for the
+  // second kernel c_e S_e [E] and a count of its workgroups
+  float* part_sums;
+  int32_t* part_counts;
+  int32_t* part_live;
+  double* products;
+  uint32_t* done;
+};
+
+// Sum over lanes of a wave, in one order.
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+
+// loss from sum_e c_e S_e
+__device__ __forceinline__ float balance_loss(double products, int E, int k, int live) {
+  if (live == 0) return 0.0f;
+  return (float)(products * E / ((double)k * live * live));
+}
+
+// Every workgroup takes 64 tokens at a time; what it sums over tokens stays in registers
+// (a lane's experts are the same for all of its tokens) and is added up in one order at
+// the end.  Alone, it writes the results itself.
+template <int DT, int EPL>
+__global__ __launch_bounds__(kFwdThreads) void router_kernel(Fwd p) {
+  __shared__ float sums[kFwdWaves][kLanes * EPL];
+  __shared__ int32_t hist[kMaxExperts];
+  __shared__ int32_t live_of[kFwdWaves];
+  __shared__ double products[kMaxExperts / 64];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int slot = lane & (kLanes - 1), e0 = EPL * slot;
+  const int E = p.E, k = p.k;
+  if (tid < kMaxExperts) hist[tid] = 0;
+  if (blockIdx.x == 0 && tid == 0) *p.done = 0;
+  __syncthreads();
+  float acc[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) acc[j] = 0.0f;
+  int live_tokens = 0;
+  bool bad = false;
+  for (int64_t base = (int64_t)blockIdx.x * kFwdTokens; base < p.tokens;
+       base += (int64_t)gridDim.x * kFwdTokens) {
+    const int64_t t = base + w * (64 / kLanes) + (lane >> 4);
+    const bool here = t < p.tokens;
+    const char* row = p.logits + t * p.ld;
+    bool live = here && (p.mask == nullptr || p.mask[t] != 0);
+    float v[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) v[j] = -INFINITY;
+    if (live) load_row<DT, EPL>(row, e0, E, v);
+    bool any = false;
+    float m = v[0];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      any |= !(v[j] == -INFINITY);
+      m = fmaxf(m, v[j]);
+    }
+    m = max16(m);
+    live = ballot16(any, lane) != 0;
+    float ex[EPL], s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      ex[j] = exp_le0(v[j] - m);
+      s += v[j] == -INFINITY ? 0.0f : ex[j];
+    }
+    s = sum16(s);
+    bad |= live && !(s < INFINITY);
+    const float inv = 1.0f / s;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      acc[j] += !live || (v[j] == -INFINITY && s < INFINITY) ? 0.0f : ex[j] * inv;
+    live_tokens += live ? 1 : 0;
+    const int e = choose<DT, EPL>(v, e0, E, k, lane);
+    float weight = 0.0f;
+    if (e >= 0) weight = exp_le0(load_one<DT>(row, e) - m) * inv;
+    if (p.normalize) {
+      const float all = sum16(weight);
+      weight = e >= 0 ? weight / all : 0.0f;
+    }
+    if (here && slot < k) {
+      p.experts[t * k + slot] = e;
+      p.weights[t * k + slot] = weight;
+      if (e >= 0) atomicAdd(&hist[e], 1);
+    }
+  }
+  if (__any(bad) && lane == 0) dev_status_or(p.status, kDevNonFinite);
+  // the wave's four tokens, then the waves
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    acc[j] += __shfl_xor(acc[j], 16, 64);
+    acc[j] += __shfl_xor(acc[j], 32, 64);
+    if (lane < kLanes) sums[w][e0 + j] = acc[j];
+  }
+  live_tokens += __shfl_xor(live_tokens, 16, 64);
+  live_tokens += __shfl_xor(live_tokens, 32, 64);
+  if (lane == 0) live_of[w] = live_tokens;
+  __syncthreads();
+  int live = 0;
+#pragma unroll
+  for (int i = 0; i < kFwdWaves; ++i) live += live_of[i];
+  float sum = 0.0f;
+  if (tid < E) {
+#pragma unroll
+    for (int i = 0; i < kFwdWaves; ++i) sum += sums[i][tid];
+  }
+  if (gridDim.x > 1) {
+    if (tid < E) {
+      p.part_sums[(int64_t)blockIdx.x * E + tid] = sum;
+      p.part_counts[(int64_t)blockIdx.x * E + tid] = hist[tid];
+    }
+    if (tid == 0) p.part_live[blockIdx.x] = live;
+    return;
+  }
+  if (tid < kMaxExperts) {
+    const double c = wave_sum(tid < E ? (double)hist[tid] * sum : 0.0);
+    if (lane == 0) products[w] = c;
+    if (tid < E) {
+      p.counts[tid] = hist[tid];
+      p.prob_sums[tid] = sum;
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    *p.live = live;
+    *p.loss = balance_loss(products[0] + products[1] + products[2] + products[3], E, k, live);
+  }
+}
+
+// Adds up the workgroups' sums: 16 experts a workgroup, 16 threads an expert.  The last
+// workgroup to end adds up the loss.
+constexpr int kFinishThreads = 256;
+
+__global__ __launch_bounds__(kFinishThreads) void router_finish_kernel(Fwd p, int parts) {
+  __shared__ double sums[16][17];
+  __shared__ int32_t counts[16][17];
+  __shared__ bool last;
+  __shared__ double waves[kFinishThreads / 64];
+  __shared__ int32_t lives[kFinishThreads / 64];
+  const int tid = threadIdx.x, e = tid & 15, i = tid >> 4;
+  const int expert = (int)blockIdx.x * 16 + e;
+  double s = 0.0;
+  int32_t c = 0;
+  if (expert < p.E) {
+#pragma unroll 8
+    for (int b = i; b < parts; b += 16) {
+      s += (double)p.part_sums[(int64_t)b * p.E + expert];
+      c += p.part_counts[(int64_t)b * p.E + expert];
+    }
+  }
+  sums[i][e] = s;
+  counts[i][e] = c;
+  __syncthreads();
+  if (i == 0 && expert < p.E) {
+#pragma unroll
+    for (int j = 1; j < 16; ++j) {
+      s += sums[j][e];
+      c += counts[j][e];
+    }
+    p.counts[expert] = c;
+    p.prob_sums[expert] = (float)s;
+    __hip_atomic_store(p.products + expert, (double)c * s, __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __threadfence();
+  __syncthreads();
+  if (tid == 0)
+    last = __hip_atomic_fetch_add(p.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+           gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  double all = tid < p.E ? __hip_atomic_load(p.products + tid, __ATOMIC_RELAXED,
+                                             __HIP_MEMORY_SCOPE_AGENT)
+                         : 0.0;
+  int live = tid < parts ? p.part_live[tid] : 0;
+  all = wave_sum(all);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) live += __shfl_xor(live, d, 64);
+  if ((tid & 63) == 0) {
+    waves[tid >> 6] = all;
+    lives[tid >> 6] = live;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    live = lives[0] + lives[1] + lives[2] + lives[3];
+    *p.live = live;
+    *p.loss = balance_loss(waves[0] + waves[1] + waves[2] + waves[3], p.E, p.k, live);
+  }
+}
+static_assert(kFwdBlocks <= kFinishThreads && kMaxExperts <= kFinishThreads, "a thread each");
+
+// ---------------------------------------------------------------- backward
+
+struct Bwd {
+  const char* logits;
+  int64_t ld, tokens;
+  const uint8_t* mask;
+  int E, k, normalize;
+  const int32_t* experts;
+  const float* d_weights;  // or null
+  const int32_t* counts;
+  const int32_t* live;
+  const float* d_loss;     // or null
+  char* out;
+  int64_t ldo;
+};
+
+// What the slots add goes to the experts' lanes through LDS: a row of E floats a token,
+// zeros but for the slots, which are cleared again after they were read.
+template <int DT, int EPL>
+__global__ __launch_bounds__(kBwdThreads) void router_backward_kernel(Bwd p) {
+  __shared__ __attribute__((aligned(16))) float slots[kBwdTokens][kLanes * EPL];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int slot = lane & (kLanes - 1), e0 = EPL * slot;
+  const int E = p.E, k = p.k;
+  float* mine = slots[tid >> 4];
+  float b[EPL];
+  const int n = p.d_loss != nullptr ? *p.live : 0;
+  const float f = n > 0 ? (float)((double)*p.d_loss * E / ((double)k * n * n)) : 0.0f;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    mine[e0 + j] = 0.0f;
+    b[j] = f != 0.0f && e0 + j < E ? f * (float)p.counts[e0 + j] : 0.0f;
+  }
+  for (int64_t base = (int64_t)blockIdx.x * kBwdTokens; base < p.tokens;
+       base += (int64_t)gridDim.x * kBwdTokens) {
+    const int64_t t = base + (tid >> 4);
+    const bool here = t < p.tokens;
+    const char* row = p.logits + t * p.ld;
+    bool live = here && (p.mask == nullptr || p.mask[t] != 0);
+    float v[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) v[j] = -INFINITY;
+    if (live) load_row<DT, EPL>(row, e0, E, v);
+    int e = -1;
+    float dw = 0.0f;
+    if (live && slot < k && p.d_weights != nullptr) {
+      e = p.experts[t * k + slot];
+      if (e < 0 || e >= E) e = -1;
+      if (e >= 0) dw = p.d_weights[t * k + slot];
+    }
+    bool any = false;
+    float m = v[0];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      any |= !(v[j] == -INFINITY);
+      m = fmaxf(m, v[j]);
+    }
+    m = max16(m);
+    live = ballot16(any, lane) != 0;
+    float prob[EPL], s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      prob[j] = exp_le0(v[j] - m);
+      s += v[j] == -INFINITY ? 0.0f : prob[j];
+    }
+    s = sum16(s);
+    const float inv = 1.0f / s;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      prob[j] = v[j] == -INFINITY && s < INFINITY ? 0.0f : prob[j] * inv;
+    float add = dw;
+    if (p.normalize) {
+      float weight = e >= 0 ? exp_le0(load_one<DT>(row, e) - m) * inv : 0.0f;
+      const float all = sum16(weight);
+      weight = e >= 0 ? weight / all : 0.0f;
+      add = weight * (dw - sum16(e >= 0 ? weight * dw : 0.0f));
+    }
+    if (e >= 0) atomicAdd(&mine[e], add);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    float a[EPL], dot = 0.0f, given[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) given[j] = mine[e0 + j];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (e >= 0) mine[e] = 0.0f;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      a[j] = p.normalize ? b[j] : b[j] + given[j];
+      dot += prob[j] * a[j];
+    }
+    dot = sum16(dot);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      const float d = prob[j] * (a[j] - dot) + (p.normalize ? given[j] : 0.0f);
+      a[j] = live ? d : 0.0f;
+    }
+    if (here) store_row<DT, EPL>(p.out + t * p.ldo, e0, E, a);
+  }
+}
+
+// f<DT, EPL> for a type and a number of experts.
+template <int DT, typename F>
+hipError_t by_experts(int E, F f) {
+  if (E <= 16) return f(std::integral_constant<int, DT>{}, std::integral_constant<int, 1>{});
+  if (E <= 32) return f(std::integral_constant<int, DT>{}, std::integral_constant<int, 2>{});
+  if (E <= 64) return f(std::integral_constant<int, DT>{}, std::integral_constant<int, 4>{});
+  if (E <= 128) return f(std::integral_constant<int, DT>{}, std::integral_constant<int, 8>{});
+  return f(std::integral_constant<int, DT>{}, std::integral_constant<int, 16>{});
+}
+template <typename F>
+hipError_t by_type(int dtype, int E, F f) {
+  if (dtype == 0) return by_experts<0>(E, f);
+  if (dtype == 1) return by_experts<1>(E, f);
+  return by_experts<2>(E, f);
+}
+
+int element_bytes(int dtype) { return dtype == 2 ? 4 : 2; }
+
+}  // namespace
+
+// The same for every number of tokens, and more for more experts.
+size_t router_workspace_bytes(int64_t E) {
+  return 64 + 4 * (size_t)kFwdBlocks + 8 * (size_t)E + 8 * (size_t)kFwdBlocks * (size_t)E;
+}
+
+hipError_t launch_router(int dtype, const void* logits, int64_t ld, int64_t tokens, int E, int k,
+                         const uint8_t* mask, int normalize, int32_t* experts, float* weights,
+                         int32_t* counts, float* prob_sums, int32_t* live, float* loss, void* ws,
+                         uint32_t* status, hipStream_t stream) {
+  Fwd p{};
+  p.logits = static_cast<const char*>(logits);
+  p.ld = ld * element_bytes(dtype);
+  p.tokens = tokens;
+  p.mask = mask;
+  p.E = E; p.k = k; p.normalize = normalize;
+  p.experts = experts; p.weights = weights; p.counts = counts; p.prob_sums = prob_sums;
+  p.live = live; p.loss = loss; p.status = status;
+  char* at = static_cast<char*>(ws);
+  p.done = reinterpret_cast<uint32_t*>(at);
+  at += 64;
+  p.products = reinterpret_cast<double*>(at);
+  at += 8 * (size_t)E;
+  p.part_live = reinterpret_cast<int32_t*>(at);
+  at += 4 * (size_t)kFwdBlocks;
+  p.part_sums = reinterpret_cast<float*>(at);
+  at += 4 * (size_t)kFwdBlocks * (size_t)E;
+  p.part_counts = reinterpret_cast<int32_t*>(at);
+  const int64_t want = (tokens + kFwdTokens - 1) / kFwdTokens;
+  const int blocks = tokens <= kOneBlock ? 1 : (int)(want < kFwdBlocks ? want : kFwdBlocks);
+  const hipError_t e = by_type(dtype, E, [&](auto dt, auto epl) {
+    hipLaunchKernelGGL((router_kernel<decltype(dt)::value, decltype(epl)::value>), dim3(blocks),
+                       dim3(kFwdThreads), 0, stream, p);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess || blocks == 1) return e;
+  hipLaunchKernelGGL(router_finish_kernel, dim3((E + 15) / 16), dim3(kFinishThreads), 0, stream, p,
+                     blocks);
+  return hipGetLastError();
+}
+
+hipError_t launch_router_backward(int dtype, const void* logits, int64_t ld, int64_t tokens, int E,
+                                  int k, const uint8_t* mask, int normalize, const int32_t* experts,
+                                  const float* d_weights, const int32_t* counts,
+                                  const int32_t* live, const float* d_loss, void* out, int64_t ldo,
+                                  hipStream_t stream) {
+  if (tokens == 0) return hipSuccess;
+  Bwd p{};
+  p.logits = static_cast<const char*>(logits);
+  p.ld = ld * element_bytes(dtype);
+  p.tokens = tokens;
+  p.mask = mask;
+  p.E = E; p.k = k; p.normalize = normalize;
+  p.experts = experts; p.d_weights = d_weights; p.counts = counts; p.live = live;
+  p.d_loss = d_loss;
+  p.out = static_cast<char*>(out);
+  p.ldo = ldo * element_bytes(dtype);
+  const int64_t want = (tokens + kBwdTokens - 1) / kBwdTokens;
+  const int64_t cap = 8 * (int64_t)device_cu_count();
+  const unsigned blocks = (unsigned)(want < cap ? want : cap);
+  return by_type(dtype, E, [&](auto dt, auto epl) {
+    hipLaunchKernelGGL((router_backward_kernel<decltype(dt)::value, decltype(epl)::value>),
+                       dim3(blocks), dim3(kBwdThreads), 0, stream, p);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace bsg

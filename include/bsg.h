@@ -48,7 +48,9 @@ typedef enum {
 #define BSG_DEV_OVER_CAPACITY 2u   /* offsets ran past the buffer capacity; clamped */
 #define BSG_DEV_BAD_PADDING   4u   /* padded offsets not multiples of 128 or smaller than
                                       the live sizes; that group was skipped */
-#define BSG_DEV_NONFINITE     8u   /* a global gradient norm is infinite or NaN */
+#define BSG_DEV_NONFINITE     8u   /* a global gradient norm is infinite or NaN; a row to be routed,
+                                      quantized to int8 or kept in 8 bits holds an infinity
+                                      or a NaN */
 #define BSG_DEV_BAD_ADAPTER   16u  /* an adapter index >= num_adapters was treated as none */
 
 typedef enum {
@@ -58,12 +60,14 @@ typedef enum {
   BSG_WGRAD_NT_E5M2 = 3
 } bsg_gemm_mode;
 typedef enum { BSG_OUT_BF16 = 0, BSG_OUT_F32 = 1, BSG_OUT_F16 = 2 } bsg_out_dtype; /* F16: 16-bit GEMMs */
-typedef enum { BSG_IN_BF16 = 0, BSG_IN_F16 = 1 } bsg_in_dtype;
+typedef enum { BSG_IN_BF16 = 0, BSG_IN_F16 = 1, BSG_IN_F32 = 2 } bsg_in_dtype; /* F32: the router's logits */
 typedef enum { BSG_GRAD_BF16 = 0, BSG_GRAD_F16 = 1, BSG_GRAD_F32 = 2 } bsg_grad_dtype;
 
 #define BSG_MAX_GROUPS 256
 #define BSG_COLWISE_PAD 128
 #define BSG_MAX_LORA_RANK 256
+#define BSG_MAX_TOP_K 16
+#define BSG_MAX_INT8_K 131056  /* longest contraction whose sums fit 32 bits, in 16s */
 
 /* Thread-local message of the last failing call on this thread ("" if none). */
 const char* bsg_last_error(void);
@@ -723,6 +727,179 @@ int grad_norm(const void* plan, int64_t num_chunks, void* workspace, size_t work
 int clip_grad_norm(const void* plan, int64_t num_chunks, float max_norm, const double* sumsq,
                    void* workspace, size_t workspace_bytes, float* norm, uint32_t* dev_status,
                    void* stream);
+
+/*
+ * The router of a mixture of experts, in front of the grouped products: each token's
+ * top k experts and their weights, the tokens of each expert (the sizes that
+ * group_offsets_i32_to_i64 takes), and a loss that balances them.
+ *
+ * A token is live if its mask is not 0 and a logit of it is above -inf; n of them are.
+ *   p_e  = exp(l_e) / sum_i exp(l_i) of a live token's logits l
+ *   experts: the k largest logits, ties to the lowest index; a logit of -inf or NaN is
+ *            never chosen (a slot without an expert: -1, with weight 0)
+ *   weights: p of the chosen; normalize 1: over the sum of the chosen
+ *   counts[e] = slots that hold e, prob_sums[e] = sum of p_e over the live tokens
+ *   loss = E / (top_k n^2) * sum_e counts[e] prob_sums[e]  (0 without a live token):
+ *          E times the sum of an expert's share of the slots times its mean probability,
+ *          1 where both are even.
+ * Tokens that are not live get -1 and 0.  A live token with a NaN or +inf has p NaN (the
+ * formula's), which reaches its weights, prob_sums and loss; *dev_status gets
+ * BSG_DEV_NONFINITE.
+ *
+ *   in_dtype    BSG_IN_BF16, BSG_IN_F16 or BSG_IN_F32.
+ *   logits      [tokens, E], ld >= E elements between rows, aligned to its elements.
+ *   tokens      0 <= tokens < 2^31; 1 <= E <= BSG_MAX_GROUPS;
+ *               1 <= top_k <= min(E, BSG_MAX_TOP_K).
+ *   mask        [tokens] bytes or NULL (all tokens).
+ *   experts     [tokens, top_k] int32, in descending order of the logits;
+ *   weights     [tokens, top_k] float32.
+ *   counts      [E] int32, prob_sums [E], live [1] int32 (n), loss [1].
+ *   workspace   moe_router_topk_workspace_size(tokens, E) bytes, 16-byte aligned.  The
+ *               size never decreases in either.  Calls that may run at the same time
+ *               need a workspace each; its contents on entry do not matter.
+ * Sums of probabilities are taken in a fixed order.  One launch for up to 256 tokens, else
+ * two.
+ *
+ * moe_router_topk_backward: d_logits [tokens, E] (the logits' type, ldo) of
+ *   sum(d_weights * weights) + d_loss * loss
+ * with experts and counts as constants.  With b_e = d_loss E counts[e] / (top_k live^2):
+ *   normalize 0: a_e = b_e + d_weights of e's slot; d_e = p_e (a_e - sum_i p_i a_i)
+ *   normalize 1: d_e = p_e (b_e - sum_i p_i b_i), and w_j (dw_j - sum_i w_i dw_i) in slot
+ *                j's expert
+ * in float32, rounded once; 0 for tokens that are not live.  d_weights or d_loss may be
+ * NULL (zeros).  experts is what the forward pass wrote (indexes outside [0, E) are
+ * slots without one, whose d_weights are not read); counts and live may hold sums over several calls or
+ * ranks: the loss is then that of all their tokens, E / (top_k live^2) * sum_e counts[e]
+ * prob_sums[e] with prob_sums added up too.  Not in place.
+ * Errors: BSG_ERR_NULL, BSG_ERR_SHAPE, BSG_ERR_UNSUPPORTED (type, normalize),
+ * BSG_ERR_ALIGN (elements; workspace), BSG_ERR_WORKSPACE.
+ */
+size_t moe_router_topk_workspace_size(int64_t tokens, int64_t E);
+int moe_router_topk(int in_dtype, const void* logits, int64_t ld, int64_t tokens, int64_t E,
+                    int64_t top_k, const uint8_t* mask, int normalize, int32_t* experts,
+                    float* weights, int32_t* counts, float* prob_sums, int32_t* live, float* loss,
+                    void* workspace, size_t workspace_bytes, uint32_t* dev_status, void* stream);
+int moe_router_topk_backward(int in_dtype, const void* logits, int64_t ld, int64_t tokens,
+                             int64_t E, int64_t top_k, const uint8_t* mask, int normalize,
+                             const int32_t* experts, const float* d_weights,
+                             const int32_t* counts, const int32_t* live, const float* d_loss,
+                             void* d_logits, int64_t ldo, void* stream);
+
+/*
+ * grouped_quantize_int8
+ *
+ * Rows in 8-bit integers with a scale each, for tokens (a row of activations) and for
+ * channels (a row of an expert's [n, k] weights):
+ *   scales[r] = float32(max_i |x[r, i]| / 127)
+ *   data[r, i] = the integer nearest to x[r, i] / scales[r] (the exact quotient), ties to
+ *                even, in [-127, 127]
+ * A row of zeros has scale 0.  A row that holds an infinity or a NaN has scale NaN and
+ * data 0, and sets BSG_DEV_NONFINITE.
+ *
+ *   x           [rows_cap, cols] of in_dtype (BSG_IN_BF16, BSG_IN_F16), ldx elements
+ *               between rows (a multiple of 8, at most 2^20); cols a multiple of 16, at
+ *               most BSG_MAX_INT8_K.
+ *   offsets     [G+1] int64: rows outside [offsets[0], offsets[G]) are neither read nor
+ *               written.  NULL: all rows_cap rows (G is not looked at).
+ *   data        [rows_cap, cols] int8, scales [rows_cap] float32.
+ * Errors: BSG_ERR_NULL, BSG_ERR_SHAPE, BSG_ERR_UNSUPPORTED (in_dtype), BSG_ERR_ALIGN (x and
+ * data 16-byte, scales 4-byte).
+ */
+int grouped_quantize_int8(int in_dtype, const void* x, int64_t ldx, int64_t rows_cap, int64_t cols,
+                          int64_t G, const int64_t* offsets, int8_t* data, float* scales,
+                          uint32_t* dev_status, void* stream);
+
+/*
+ * grouped_gemm_int8 / grouped_gemm_int8_dynamic
+ *
+ * The grouped product of 8-bit integers with a scale for each token and each channel, in
+ * one launch over all groups:
+ *   Y[r, j] = (float32(sum_i A[r, i] B[g, j, i]) * a_scales[r]) * b_scales[g, j]
+ * for r in [offsets[g], offsets[g+1]).  The sums are exact integers; the result is rounded
+ * once more, to out's type.
+ *
+ *   a           [rows_cap, k] int8, a_scales [rows_cap] float32 (grouped_quantize_int8 of the
+ *               tokens; any value of a byte is taken, -128 too)
+ *   b           [G, n, k] int8, b_scales [G, n] float32 (grouped_quantize_int8 of the
+ *               weights as G * n rows)
+ *   lda, ldb    bytes between rows (multiples of 16, at most 2^20); stride_b: bytes
+ *               between groups' matrices (a multiple of 16).
+ *   offsets     [G+1] int64 live row offsets; rows outside are neither read nor written.
+ *   n           a multiple of 8; k a multiple of 16, at most BSG_MAX_INT8_K.
+ *   out         [rows_cap, n] of out_dtype (BSG_OUT_BF16, BSG_OUT_F16, BSG_OUT_F32), ldo
+ *               elements between rows (a multiple of 8).
+ *   workspace   grouped_gemm_int8_workspace_size() bytes, 256-byte aligned, or NULL: as for
+ *               grouped_gemm_16bit.  Splitting a contraction does not change a result.
+ * One group is a projection that all rows share.
+ *
+ * grouped_gemm_int8_dynamic takes the tokens in 16 bits (x [rows_cap, k] of in_dtype, ldx
+ * elements between rows) and quantizes them on the way: the result is that of
+ * grouped_quantize_int8 and grouped_gemm_int8, bit for bit.  Its workspace is not
+ * optional: grouped_gemm_int8_dynamic_workspace_size(rows_cap, k) bytes, which never decrease
+ * in either argument, so one serves calls of up to that many rows and columns.  It
+ * says BSG_DEV_NONFINITE as grouped_quantize_int8 does.
+ * Calls that may run at the same time need a workspace each.
+ * Errors: BSG_ERR_NULL, BSG_ERR_SHAPE, BSG_ERR_UNSUPPORTED (types), BSG_ERR_ALIGN (a, x, b, out
+ * and b_scales 16-byte, a_scales 4-byte), BSG_ERR_WORKSPACE.
+ *
+ * grouped_gemm_int8_tile_rows: as grouped_gemm_16bit_tile_rows, for both.
+ */
+size_t grouped_gemm_int8_workspace_size(void);
+int grouped_gemm_int8_tile_rows(int64_t G, int64_t rows_cap, int64_t n, int64_t k,
+                                int with_workspace);
+int grouped_gemm_int8(int64_t G, const int8_t* a, int64_t lda, const float* a_scales,
+                      const int8_t* b, int64_t ldb, int64_t stride_b, const float* b_scales,
+                      const int64_t* offsets, int64_t rows_cap, int64_t n, int64_t k, void* out,
+                      int64_t ldo, int out_dtype, void* workspace, size_t workspace_bytes,
+                      uint32_t* dev_status, void* stream);
+size_t grouped_gemm_int8_dynamic_workspace_size(int64_t rows_cap, int64_t k);
+int grouped_gemm_int8_dynamic(int in_dtype, int64_t G, const void* x, int64_t ldx, const int8_t* b,
+                              int64_t ldb, int64_t stride_b, const float* b_scales,
+                              const int64_t* offsets, int64_t rows_cap, int64_t n, int64_t k,
+                              void* out, int64_t ldo, int out_dtype, void* workspace,
+                              size_t workspace_bytes, uint32_t* dev_status, void* stream);
+
+/*
+ * grouped_swiglu_checkpoint_mxfp8 / grouped_swiglu_checkpoint_mxfp8_backward
+ *
+ * The gated activation between an expert's two products, which keeps its input in 8 bits
+ * for the backward pass.  With h = [g | u] (the first product's output, f columns each),
+ * w the row's weight (row_weights, e.g. the router's, or 1) and s = 1 / (1 + exp(-g)):
+ *   out = w g s u                          (float32, rounded once)
+ *   data, scales: h as grouped_quantize_mxfp8 quantizes rows (E4M3 elements, an E8M0 byte
+ *                 for each 32; infinities and NaN saturate, and set BSG_DEV_NONFINITE)
+ * and backwards, g and u being the kept values (element times 2^(byte - 127)):
+ *   d_h = [d_out w u s (1 + g (1 - s)) | d_out w g s]
+ *   d_row_weights[r] = sum_j d_out g s u   (float32, in a fixed order)
+ *   out = w g s u again, for the second product's weight gradient
+ *
+ *   in_dtype    BSG_IN_BF16 or BSG_IN_F16: of h, out, d_out and d_h.
+ *   f           a multiple of 32, at most 2^19.
+ *   h, d_h      [rows_cap, 2 f], ldh; out, d_out [rows_cap, f], ldo, ldd: elements between
+ *               rows (multiples of 8, at most 2^20).
+ *   offsets     [G+1] int64: rows outside [offsets[0], offsets[G]) are neither read nor
+ *               written.
+ *   row_weights [rows_cap] float32 or NULL.
+ *   data        [rows_cap, 2 f] bytes, scales [rows_cap, f / 16] bytes, row by row.  Both
+ *               NULL in the forward pass: nothing is kept (serving).
+ *   d_row_weights [rows_cap] float32 or NULL (not computed); out may be NULL in the
+ *               backward pass.
+ * In 8 bits the kept form takes 33/64 of h's bytes.  d_out and d_h, h and out must not overlap.
+ * Errors: BSG_ERR_NULL, BSG_ERR_SHAPE, BSG_ERR_UNSUPPORTED (in_dtype), BSG_ERR_ALIGN (16-bit
+ * tensors and data 16-byte, float32 ones 4-byte).
+ */
+int grouped_swiglu_checkpoint_mxfp8(int in_dtype, const void* h, int64_t ldh,
+                                    const float* row_weights, int64_t G, const int64_t* offsets,
+                                    int64_t rows_cap, int64_t f, void* out, int64_t ldo,
+                                    uint8_t* data, uint8_t* scales, uint32_t* dev_status,
+                                    void* stream);
+int grouped_swiglu_checkpoint_mxfp8_backward(int in_dtype, const uint8_t* data,
+                                             const uint8_t* scales, const float* row_weights,
+                                             const void* d_out, int64_t ldd, int64_t G,
+                                             const int64_t* offsets, int64_t rows_cap, int64_t f,
+                                             void* d_h, int64_t ldh, void* out, int64_t ldo,
+                                             float* d_row_weights, uint32_t* dev_status,
+                                             void* stream);
 
 #ifdef __cplusplus
 }
