@@ -246,6 +246,11 @@ def _i64():
     return torch.int64
 
 
+def _i8():
+    import torch
+    return torch.int8
+
+
 def _f32():
     import torch
     return torch.float32
@@ -1058,9 +1063,32 @@ def _launch(fn, index, *args):
         _check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
 
 
+_makers = {}
+
+
+def _maker(index, dtype):
+    """new_empty of a tensor of that type on device `index`: a call of it without a type takes half a
+    microsecond less than one with a type, which is a good part of a small call."""
+    make = _makers.get((index, dtype))
+    if make is None:
+        import torch
+        make = torch.empty(0, dtype=dtype, device=torch.device("cuda", index)).new_empty
+        _makers[index, dtype] = make
+    return make
+
+
 def _maybe(t, name, nbytes, dtype, index):
     """_dense for a tensor that may be left out."""
     return None if t is None else _dense(t, name, nbytes, dtype, index)
+
+
+def _output(t, rows, cols, dtype, index, name="out"):
+    """(tensor [rows, cols], row stride): a new one, or the given one after its checks."""
+    if t is None:
+        return _maker(index, dtype)(rows, cols), cols
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError("%s is %s; the call writes %s" % (name, tuple(t.shape), (rows, cols)))
+    return t, _strided(t, name, 2, dtype, index)[0]
 
 
 def _status(t, index):
@@ -1108,12 +1136,9 @@ def moe_router_topk(logits, top_k, mask=None, normalize=True, workspace=None, st
     code, ld, tokens, E, m = _router_args(logits, mask, dev)
     if workspace is None:
         workspace = moe_router_topk_workspace(tokens, max(E, 1), logits.device)
-    out = {"experts": logits.new_empty((tokens, top_k), dtype=torch.int32),
-           "weights": logits.new_empty((tokens, top_k), dtype=torch.float32),
-           "counts": logits.new_empty(E, dtype=torch.int32),
-           "prob_sums": logits.new_empty(E, dtype=torch.float32),
-           "live": logits.new_empty(1, dtype=torch.int32),
-           "loss": logits.new_empty(1, dtype=torch.float32)}
+    ints, floats = _maker(dev, torch.int32), _maker(dev, torch.float32)
+    out = {"experts": ints(tokens, top_k), "weights": floats(tokens, top_k), "counts": ints(E),
+           "prob_sums": floats(E), "live": ints(1), "loss": floats(1)}
     _launch(lib.moe_router_topk, dev, code, logits.data_ptr(), ld, tokens, E, top_k, m,
             1 if normalize else 0, *(t.data_ptr() for t in out.values()),
             _dense(workspace, "workspace", 0, workspace.dtype, dev), workspace.nbytes,
@@ -1135,8 +1160,7 @@ def moe_router_topk_backward(logits, experts, counts, live, d_weights=None, d_lo
     top_k = experts.shape[1]
     if d_weights is not None and tuple(d_weights.shape) != (tokens, top_k):
         raise ValueError("d_weights is %s, experts %s" % (tuple(d_weights.shape), (tokens, top_k)))
-    out = _out_or_new(out, (tokens, E), logits.dtype, logits)
-    ldo, _ = _strided(out, "out", 2, logits.dtype, dev)
+    out, ldo = _output(out, tokens, E, logits.dtype, dev)
     args = (_dense(experts, "experts", 4 * tokens * top_k, torch.int32, dev),
             _maybe(d_weights, "d_weights", 4 * tokens * top_k, torch.float32, dev),
             _dense(counts, "counts", 4 * E, torch.int32, dev), _dense(live, "live", 4, torch.int32, dev),
@@ -1166,9 +1190,9 @@ def grouped_quantize_int8(x, offsets=None, data=None, scales=None, status=None):
     ld, _ = _strided(x, "x", 2, x.dtype, dev)
     rows, cols = x.shape
     if data is None:
-        data = x.new_empty((rows, cols), dtype=torch.int8)
+        data = _maker(dev, torch.int8)(rows, cols)
     if scales is None:
-        scales = x.new_empty(rows, dtype=torch.float32)
+        scales = _maker(dev, torch.float32)(rows)
     args = (_maybe(offsets, "offsets", 16, torch.int64, dev),
             _dense(data, "data", rows * cols, torch.int8, dev),
             _dense(scales, "scales", 4 * rows, torch.float32, dev), _status(status, dev))
@@ -1178,25 +1202,35 @@ def grouped_quantize_int8(x, offsets=None, data=None, scales=None, status=None):
     return data, scales
 
 
-def _int8_product(rows, k, w, w_scales, offsets, out, out_dtype, default, ref, dev):
+_out_type_of = {}
+
+
+def _out_types():
+    if not _out_type_of:
+        import torch
+        _out_type_of.update({BSG_OUT_BF16: torch.bfloat16, BSG_OUT_F16: torch.float16,
+                             BSG_OUT_F32: torch.float32})
+    return _out_type_of
+
+
+def _int8_product(rows, k, w, w_scales, offsets, out, out_dtype, default, dev):
     """Checked arguments that the int8 products share: (out, G, arguments from b to out_dtype)."""
-    import torch
-    codes = {torch.bfloat16: BSG_OUT_BF16, torch.float16: BSG_OUT_F16, torch.float32: BSG_OUT_F32}
-    ldw, stride_w = _strided(w, "w", 3, torch.int8, dev)
+    types = _out_types()
+    ldw, stride_w = _strided(w, "w", 3, _i8(), dev)
     G, n, wk = w.shape
     if offsets.numel() - 1 != G or wk != k:
         raise ValueError("w is %s; %d groups contracting %d are needed" % (
             tuple(w.shape), offsets.numel() - 1, k))
     if out_dtype is None:
-        out_dtype = codes.get(out.dtype) if out is not None else default
-    odt = next((d for d, c in codes.items() if c == out_dtype), None)
+        out_dtype = default if out is None else next(
+            (c for c, d in types.items() if d == out.dtype), None)
+    odt = types.get(out_dtype)
     if odt is None:
         raise ValueError("out_dtype %r is not BSG_OUT_BF16, BSG_OUT_F16 or BSG_OUT_F32" % (out_dtype,))
-    out = _out_or_new(out, (rows, n), odt, ref)
-    ldo, _ = _strided(out, "out", 2, odt, dev)
+    out, ldo = _output(out, rows, n, odt, dev)
     return out, G, (w.data_ptr(), ldw, stride_w,
-                    _dense(w_scales, "w_scales", 4 * G * n, torch.float32, dev),
-                    _dense(offsets, "offsets", 16, torch.int64, dev), rows, n, k, out.data_ptr(), ldo,
+                    _dense(w_scales, "w_scales", 4 * G * n, _f32(), dev),
+                    _dense(offsets, "offsets", 16, _i64(), dev), rows, n, k, out.data_ptr(), ldo,
                     out_dtype)
 
 
@@ -1211,7 +1245,7 @@ def grouped_gemm_int8(a, a_scales, w, w_scales, offsets, out=None, out_dtype=Non
     dev = _device_index(a, "a")
     lda, _ = _strided(a, "a", 2, torch.int8, dev)
     rows, k = a.shape
-    out, G, args = _int8_product(rows, k, w, w_scales, offsets, out, out_dtype, BSG_OUT_BF16, a, dev)
+    out, G, args = _int8_product(rows, k, w, w_scales, offsets, out, out_dtype, BSG_OUT_BF16, dev)
     scales = _dense(a_scales, "a_scales", 4 * rows, torch.float32, dev)
     ws = (None, 0) if workspace is None else (
         _dense(workspace, "workspace", 0, workspace.dtype, dev), workspace.nbytes)
@@ -1251,7 +1285,7 @@ def grouped_gemm_int8_dynamic(x, w, w_scales, offsets, out=None, out_dtype=None,
     ldx, _ = _strided(x, "x", 2, x.dtype, dev)
     rows, k = x.shape
     out, G, args = _int8_product(rows, k, w, w_scales, offsets, out, out_dtype,
-                                 BSG_OUT_F16 if code == BSG_IN_F16 else BSG_OUT_BF16, x, dev)
+                                 BSG_OUT_F16 if code == BSG_IN_F16 else BSG_OUT_BF16, dev)
     if workspace is None:
         workspace = grouped_gemm_int8_dynamic_workspace(rows, k, x.device)
     ws = _dense(workspace, "workspace", 0, workspace.dtype, dev)
@@ -1275,14 +1309,13 @@ def grouped_swiglu_checkpoint_mxfp8(h, offsets, row_weights=None, out=None, data
     f = f2 // 2
     if f2 % 64 != 0 or f2 == 0:
         raise ValueError("h has %d columns, not two times a multiple of 32" % f2)
-    out = _out_or_new(out, (rows, f), h.dtype, h)
-    ldo, _ = _strided(out, "out", 2, h.dtype, dev)
+    out, ldo = _output(out, rows, f, h.dtype, dev)
     kept = (None, None)
     if keep:
         if data is None:
-            data = h.new_empty((rows, f2), dtype=torch.uint8)
+            data = _maker(dev, torch.uint8)(rows, f2)
         if scales is None:
-            scales = h.new_empty((rows, f // 16), dtype=torch.uint8)
+            scales = _maker(dev, torch.uint8)(rows, f // 16)
         kept = (_dense(data, "data", rows * f2, torch.uint8, dev),
                 _dense(scales, "scales", rows * (f // 16), torch.uint8, dev))
     else:
@@ -1309,17 +1342,15 @@ def grouped_swiglu_checkpoint_mxfp8_backward(data, scales, d_out, offsets, row_w
     rows, f = d_out.shape
     if f % 32 != 0 or f == 0:
         raise ValueError("d_out has %d columns, not a multiple of 32" % f)
-    d_h = _out_or_new(d_h, (rows, 2 * f), d_out.dtype, d_out, "d_h")
-    ldh, _ = _strided(d_h, "d_h", 2, d_out.dtype, dev)
+    d_h, ldh = _output(d_h, rows, 2 * f, d_out.dtype, dev, "d_h")
     ldo, optr = f, None
     if recompute or out is not None:
-        out = _out_or_new(out, (rows, f), d_out.dtype, d_out)
-        ldo, _ = _strided(out, "out", 2, d_out.dtype, dev)
+        out, ldo = _output(out, rows, f, d_out.dtype, dev)
         optr = out.data_ptr()
     if row_weights is None:
         d_row_weights = None
     elif d_row_weights is None:
-        d_row_weights = d_out.new_empty(rows, dtype=torch.float32)
+        d_row_weights = _maker(dev, torch.float32)(rows)
     args = (_dense(data, "data", rows * 2 * f, torch.uint8, dev),
             _dense(scales, "scales", rows * (f // 16), torch.uint8, dev),
             _maybe(row_weights, "row_weights", 4 * rows, torch.float32, dev), d_out.data_ptr(), ldd,

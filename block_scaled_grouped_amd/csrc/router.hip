@@ -11,8 +11,9 @@
 //   unnormalized  a_e = b_e + sum_j dw_j [e_j = e],  dl_e = p_e (a_e - sum_i p_i a_i)
 //   normalized    dl_e = p_e (b_e - sum_i p_i b_i) + sum_j [e_j = e] w_j (dw_j - sum_i w_i dw_i)
 //
-// 16 lanes take a token, lane i the experts EPL i .. EPL i + EPL - 1, so that a wave
-// holds four tokens and reductions are lane moves within a row of 16 (DPP).
+// 16 lanes take a token, EPL experts each, so that a wave holds four tokens and reductions
+// are lane moves within a row of 16 (DPP).  A lane's experts are runs of 16 bytes, 16 lanes
+// apart: a load of the wave covers whole lines of its four rows.
 //
 // The largest are found on 32-bit keys: the logit's bits, ordered as integers, with the
 // lowest eight replaced by 255 - index.  Keys differ, so the next largest below M is the
@@ -21,6 +22,8 @@
 // A 16-bit logit has its bits above those eight.  A float32 one may share them with the
 // next in order: where that happens among a token's k + 1 largest the wave does it again,
 // on whole values.
+#include <type_traits>
+
 #include "bsg_internal.h"
 
 namespace bsg {
@@ -71,22 +74,12 @@ __device__ __forceinline__ float sum16(float v) {
     return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
   }));
 }
-// The 16 bits of a ballot that are this lane's token's.
-__device__ __forceinline__ uint32_t ballot16(bool b, int lane) {
-  return (uint32_t)(__ballot(b) >> (lane & 48)) & 0xffffu;
-}
 
 // ---------------------------------------------------------------- values
 
-// exp(x) for x <= 0 (or NaN), to float32's last bits: 2^y with y = x log2(e) in two parts,
-// the second to first order.
+// exp(x) for x <= 0 or NaN: the product's rounding is |x| 2^-24 of the result.
 __device__ __forceinline__ float exp_le0(float x) {
-  x = x < -150.0f ? -150.0f : x;
-  const float hi = 1.44269502162933349609375f, lo = 1.92596299112661746887e-8f;
-  const float y = x * hi;
-  const float rest = fmaf(x, lo, fmaf(x, hi, -y));
-  const float e = __builtin_amdgcn_exp2f(y);
-  return fmaf(e, rest * 0.693147182464599609375f, e);
+  return __builtin_amdgcn_exp2f(x * 1.44269502162933349609375f);
 }
 
 // DT 0: bf16, 1: fp16, 2: float32.
@@ -103,88 +96,107 @@ __device__ __forceinline__ float load_one(const char* row, int e) {
   return decode16<DT>(*reinterpret_cast<const __attribute__((address_space(1))) uint16_t*>(at));
 }
 
+// A lane's experts: runs of kRun, a run of the 16 lanes after the other.
+template <int DT, int EPL> constexpr int kRun = EPL < 16 / kBytes<DT> ? EPL : 16 / kBytes<DT>;
+template <int DT, int EPL>
+__device__ __forceinline__ int expert_of(int slot, int j) {
+  constexpr int R = kRun<DT, EPL>;
+  return R * (slot + kLanes * (j / R)) + j % R;
+}
+
 // A row is aligned to its elements only; the hardware takes wide loads and stores at any.
 typedef v4i v4i_any __attribute__((aligned(2)));
 typedef v2i v2i_any __attribute__((aligned(2)));
 typedef int int_any __attribute__((aligned(2)));
+#define BSG_GLOBAL __attribute__((address_space(1)))
 
-// Elements e0 .. e0 + EPL - 1 of a row of E; those past it are -inf.
-template <int DT, int EPL>
-__device__ __forceinline__ void load_row(const char* row, int e0, int E, float (&v)[EPL]) {
-  constexpr int bytes = EPL * kBytes<DT>;
-  if (e0 + EPL <= E) {
+// A lane's logits; those past the last expert are -inf.  RUNS: the experts are whole runs;
+// else they come one by one.
+template <int DT, int EPL, bool RUNS>
+__device__ __forceinline__ void load_row(const char* row, int slot, int E, float (&v)[EPL]) {
+  constexpr int R = kRun<DT, EPL>, bytes = R * kBytes<DT>;
+  if constexpr (!RUNS) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      const int e = expert_of<DT, EPL>(slot, j);
+      const float x = load_one<DT>(row, e < E ? e : E - 1);
+      v[j] = e < E ? x : -INFINITY;
+    }
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < EPL / R; ++c) {
+    const int e0 = R * (slot + kLanes * c);
+    float* out = v + R * c;
     uint32_t w[(bytes + 3) / 4];
-    const gchar* at = (const gchar*)(row) + (int64_t)e0 * kBytes<DT>;
-    if constexpr (bytes >= 16) {
+    const gchar* at = (const gchar*)(row) + (int64_t)(e0 < E ? e0 : 0) * kBytes<DT>;
+    if constexpr (bytes == 16) {
+      const v4i q = *reinterpret_cast<const BSG_GLOBAL v4i_any*>(at);
 #pragma unroll
-      for (int i = 0; i < bytes / 16; ++i) {
-        const v4i q = *reinterpret_cast<const __attribute__((address_space(1))) v4i_any*>(at + 16 * i);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[4 * i + j] = (uint32_t)q[j];
-      }
+      for (int j = 0; j < 4; ++j) w[j] = (uint32_t)q[j];
     } else if constexpr (bytes == 8) {
-      const v2i q = *reinterpret_cast<const __attribute__((address_space(1))) v2i_any*>(at);
+      const v2i q = *reinterpret_cast<const BSG_GLOBAL v2i_any*>(at);
       w[0] = (uint32_t)q[0];
       w[1] = (uint32_t)q[1];
     } else if constexpr (bytes == 4) {
-      w[0] = (uint32_t)*reinterpret_cast<const __attribute__((address_space(1))) int_any*>(at);
+      w[0] = (uint32_t)*reinterpret_cast<const BSG_GLOBAL int_any*>(at);
     } else {
-      w[0] = *reinterpret_cast<const __attribute__((address_space(1))) uint16_t*>(at);
+      w[0] = *reinterpret_cast<const BSG_GLOBAL uint16_t*>(at);
     }
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      if constexpr (DT == 2) v[j] = __uint_as_float(w[j]);
-      else v[j] = decode16<DT>((w[j >> 1] >> (16 * (j & 1))) & 0xffffu);
+    for (int j = 0; j < R; ++j) {
+      float x;
+      if constexpr (DT == 2) x = __uint_as_float(w[j]);
+      else x = decode16<DT>((w[j >> 1] >> (16 * (j & 1))) & 0xffffu);
+      out[j] = e0 < E ? x : -INFINITY;
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) v[j] = e0 + j < E ? load_one<DT>(row, e0 + j) : -INFINITY;
   }
 }
 
-template <int DT, int EPL>
-__device__ __forceinline__ void store_row(char* row, int e0, int E, const float (&v)[EPL]) {
-  constexpr int words = DT == 2 ? EPL : (EPL + 1) / 2;
-  uint32_t w[words];
+template <int DT, int EPL, bool RUNS>
+__device__ __forceinline__ void store_row(char* row, int slot, int E, const float (&v)[EPL]) {
+  constexpr int R = kRun<DT, EPL>, bytes = R * kBytes<DT>, words = (bytes + 3) / 4;
 #pragma unroll
-  for (int j = 0; j < words; ++j) {
-    if constexpr (DT == 2) w[j] = __float_as_uint(v[j]);
-    else w[j] = pack16<DT == 1>(v[2 * j], 2 * j + 1 < EPL ? v[(2 * j + 1) % EPL] : 0.0f);
-  }
-  typedef __attribute__((address_space(1))) char gout;
-  gout* at = (gout*)(row) + (int64_t)e0 * kBytes<DT>;
-  constexpr int bytes = EPL * kBytes<DT>;
-  if (e0 + EPL <= E) {
-    if constexpr (bytes >= 16) {
+  for (int c = 0; c < EPL / R; ++c) {
+    const int e0 = R * (slot + kLanes * c);
+    const float* in = v + R * c;
+    uint32_t w[words];
 #pragma unroll
-      for (int i = 0; i < bytes / 16; ++i)
-        *reinterpret_cast<__attribute__((address_space(1))) v4i_any*>(at + 16 * i) =
-            v4i{(int)w[4 * i], (int)w[4 * i + 1], (int)w[4 * i + 2], (int)w[4 * i + 3]};
-    } else if constexpr (bytes == 8) {
-      *reinterpret_cast<__attribute__((address_space(1))) v2i_any*>(at) = v2i{(int)w[0], (int)w[1]};
-    } else if constexpr (bytes == 4) {
-      *reinterpret_cast<__attribute__((address_space(1))) int_any*>(at) = (int)w[0];
-    } else {
-      *reinterpret_cast<__attribute__((address_space(1))) uint16_t*>(at) = (uint16_t)w[0];
+    for (int j = 0; j < words; ++j) {
+      if constexpr (DT == 2) w[j] = __float_as_uint(in[j]);
+      else w[j] = pack16<DT == 1>(in[2 * j], R > 1 ? in[(2 * j + 1) % R] : 0.0f);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      if (e0 + j >= E) continue;
-      if constexpr (DT == 2)
-        *reinterpret_cast<__attribute__((address_space(1))) uint32_t*>(at + 4 * j) = w[j];
+    BSG_GLOBAL char* at = (BSG_GLOBAL char*)(row) + (int64_t)e0 * kBytes<DT>;
+    if constexpr (RUNS) {
+      if (e0 >= E) continue;
+      if constexpr (bytes == 16)
+        *reinterpret_cast<BSG_GLOBAL v4i_any*>(at) = v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+      else if constexpr (bytes == 8)
+        *reinterpret_cast<BSG_GLOBAL v2i_any*>(at) = v2i{(int)w[0], (int)w[1]};
+      else if constexpr (bytes == 4)
+        *reinterpret_cast<BSG_GLOBAL int_any*>(at) = (int)w[0];
       else
-        *reinterpret_cast<__attribute__((address_space(1))) uint16_t*>(at + 2 * j) =
-            (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+        *reinterpret_cast<BSG_GLOBAL uint16_t*>(at) = (uint16_t)w[0];
+    } else {
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        if (e0 + j >= E) continue;
+        if constexpr (DT == 2)
+          *reinterpret_cast<BSG_GLOBAL uint32_t*>(at + 4 * j) = w[j];
+        else
+          *reinterpret_cast<BSG_GLOBAL uint16_t*>(at + 2 * j) =
+              (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+      }
     }
   }
 }
 
-// A logit's bits ordered as unsigned integers; 0 for what is never chosen.  -0 orders as 0.
+// A logit's bits ordered as unsigned integers, -0 as 0 and a NaN as -inf.  What is below
+// kOpen is not to be chosen.
+constexpr uint32_t kOpen = 0x00800000u;  // of the lowest finite number
 __device__ __forceinline__ uint32_t order(float v) {
-  const uint32_t u = __float_as_uint(v + 0.0f);
-  const uint32_t o = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-  return v > -INFINITY ? o : 0u;  // false for a NaN
+  const uint32_t u = __float_as_uint(fmaxf(v + 0.0f, -INFINITY));
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 template <int N>
@@ -196,45 +208,108 @@ __device__ __forceinline__ uint32_t max_of(const uint32_t (&v)[N]) {
 }
 
 // This lane's of a token's k chosen experts (lane j: the j-th; -1: none).
+//
+// A round takes the largest of the token's keys.  Each lane holds its own kHeads largest in
+// order, so that a round is a maximum over 16 lanes and a step of the winner's list.  A lane
+// that used up its list before the last round may have missed a key: of 256 experts' 9
+// largest that happens to 2 % of the tokens, and all rounds are done again on all keys (as
+// they are at once where more than kFewRounds are asked for).
+constexpr int kHeads = 4, kFewRounds = 9, kRoundsAtOnce = 3;
+
 template <int DT, int EPL>
-__device__ __forceinline__ int choose(const float (&v)[EPL], int e0, int E, int k, int lane) {
-  const int slot = lane & (kLanes - 1);
-  uint32_t key[EPL];
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const uint32_t o = order(v[j]);
-    key[j] = o != 0 ? (o & ~255u) | (uint32_t)(255 - (e0 + j)) : 0u;
-  }
-  uint32_t m = max16u(max_of(key));
-  int chosen = slot == 0 && m != 0 ? 255 - (int)(m & 255u) : -1;
-  bool close = false;
+__device__ __forceinline__ int choose(const float (&v)[EPL], int slot, int E, int k) {
+  constexpr int H = EPL < kHeads ? EPL : kHeads;
   // float32: one more than is chosen, which shows whether the last is next to another
   const int rounds = DT == 2 && k < E ? k + 1 : k;
-  for (int r = 1; r < rounds; ++r) {
+  uint32_t key[EPL], mine = 0, m = 0;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j)
+    key[j] = (order(v[j]) & ~255u) | (uint32_t)(255 - expert_of<DT, EPL>(slot, j));
+  const auto below = [&](uint32_t top) {  // the largest key below `top`
     uint32_t d[EPL];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) d[j] = key[j] - m;
-    const uint32_t next = m != 0 ? max16u(max_of(d)) + m : 0u;
-    if (DT == 2) close |= next != 0 && ((next ^ m) >> 8) == 0;
-    m = next;
-    if (slot == r && r < k && m != 0) chosen = 255 - (int)(m & 255u);
+    for (int j = 0; j < EPL; ++j) d[j] = key[j] - top;
+    return max_of(d) + top;
+  };
+  bool all = EPL > H && rounds > kFewRounds;
+  if (!all) {
+    uint32_t head[H];
+    bool won = false;
+    head[0] = max_of(key);
+#pragma unroll
+    for (int i = 1; i < H; ++i) head[i] = below(head[i - 1]);
+    for (int r0 = 0; r0 < rounds; r0 += kRoundsAtOnce) {
+#pragma unroll
+      for (int r = 0; r < kRoundsAtOnce; ++r) {
+        if (r0 + r == rounds) break;
+        m = max16u(head[0]);
+        mine = slot == r0 + r ? m : mine;
+        won = head[0] == m;
+#pragma unroll
+        for (int i = 0; i < H; ++i) head[i] = won ? (i + 1 < H ? head[(i + 1) % H] : 0u) : head[i];
+      }
+    }
+    all = EPL > H && __any(head[0] == 0 && !won);
   }
-  if (DT == 2 && __any(close)) {
+  if (EPL > H && all) {
+    m = max16u(max_of(key));
+    mine = m;
+    for (int r = 1; r < rounds; ++r) {
+      m = max16u(below(m));
+      mine = slot == r ? m : mine;
+    }
+  }
+  int chosen = slot < k && mine >= kOpen ? 255 - (int)(mine & 255u) : -1;
+  if constexpr (DT == 2) {
+    // neighbours in the order, the last round's (in m) next to lane k - 1's
+    const uint32_t after = dpp<0x101>(mine);  // of lane + 1, which has to be active
+    const uint32_t next = slot == k - 1 ? (rounds > k ? m : 0u) : after;
+    if (__any(slot < k && next >= kOpen && (next ^ mine) < 256u)) {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) key[j] = order(v[j]);
-    chosen = -1;
-    for (int r = 0; r < k; ++r) {
-      m = max16u(max_of(key));
-      uint32_t at = 0xffffu;
+      for (int j = 0; j < EPL; ++j) key[j] = order(v[j]);
+      chosen = -1;
+      for (int r = 0; r < k; ++r) {
+        m = max16u(max_of(key));
+        uint32_t at = 0xffffu;
 #pragma unroll
-      for (int j = EPL - 1; j >= 0; --j) at = key[j] == m ? (uint32_t)(e0 + j) : at;
-      at = min16u(at);
-      if (slot == r && m != 0) chosen = (int)at;
+        for (int j = EPL - 1; j >= 0; --j)
+          at = key[j] == m ? (uint32_t)expert_of<DT, EPL>(slot, j) : at;
+        at = min16u(at);
+        if (slot == r && m >= kOpen) chosen = (int)at;
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) key[j] = (uint32_t)(e0 + j) == at ? 0u : key[j];
+        for (int j = 0; j < EPL; ++j)
+          key[j] = (uint32_t)expert_of<DT, EPL>(slot, j) == at ? 0u : key[j];
+      }
     }
   }
   return chosen;
+}
+
+// A token's softmax: exp(l - max) in ex, what they have to be multiplied by, and whether it is
+// live.  Without an open expert the sum of the exponentials is 0 (max stands for 0 then), with
+// a NaN or +inf it is NaN.
+struct Softmax {
+  float max, sum, inv;
+  bool live;
+};
+template <int EPL>
+__device__ __forceinline__ Softmax softmax(const float (&v)[EPL], float (&ex)[EPL]) {
+  Softmax r;
+  float m = v[0];
+#pragma unroll
+  for (int j = 1; j < EPL; ++j) m = fmaxf(m, v[j]);
+  m = max16(m);
+  r.max = m > -INFINITY ? m : 0.0f;
+  r.sum = 0.0f;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    ex[j] = exp_le0(v[j] - r.max);
+    r.sum += ex[j];
+  }
+  r.sum = sum16(r.sum);
+  r.live = !(r.sum == 0.0f);
+  r.inv = r.live ? 1.0f / r.sum : 0.0f;
+  return r;
 }
 
 // ---------------------------------------------------------------- forward
@@ -251,10 +326,9 @@ struct Fwd {
   int32_t* live;
   float* loss;
   uint32_t* status;
-  // workspace: of each workgroup S_e [E] and c_e [E] and its live tokens; then for the
+  // workspace: of each workgroup (S_e, c_e) [E] and its live tokens; then for the
   // second kernel c_e S_e [E] and a count of its workgroups
-  float* part_sums;
-  int32_t* part_counts;
+  v2i* parts;
   int32_t* part_live;
   double* products;
   uint32_t* done;
@@ -273,17 +347,24 @@ __device__ __forceinline__ float balance_loss(double products, int E, int k, int
   return (float)(products * E / ((double)k * live * live));
 }
 
-// Every workgroup takes 64 tokens at a time; what it sums over tokens stays in registers
-// (a lane's experts are the same for all of its tokens) and is added up in one order at
-// the end.  Alone, it writes the results itself.
-template <int DT, int EPL>
+// Orders a wave's LDS accesses before and after (they complete in that order by themselves).
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// Every workgroup takes 64 tokens at a time, and reads the next 64 ahead; what it sums over
+// tokens stays in registers (a lane's experts are the same for all of its tokens) and is
+// added up in one order at the end.  Alone, it writes the results itself.
+template <int DT, int EPL, bool RUNS>
 __global__ __launch_bounds__(kFwdThreads) void router_kernel(Fwd p) {
-  __shared__ float sums[kFwdWaves][kLanes * EPL];
+  // exponentials of the tokens at hand; at the end the waves' sums
+  __shared__ __attribute__((aligned(16))) float rows[kFwdTokens][kLanes * EPL];
+  float(*sums)[kLanes * EPL] = rows;
   __shared__ int32_t hist[kMaxExperts];
   __shared__ int32_t live_of[kFwdWaves];
   __shared__ double products[kMaxExperts / 64];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int slot = lane & (kLanes - 1), e0 = EPL * slot;
+  int slot = lane & (kLanes - 1);
   const int E = p.E, k = p.k;
   if (tid < kMaxExperts) hist[tid] = 0;
   if (blockIdx.x == 0 && tid == 0) *p.done = 0;
@@ -293,58 +374,55 @@ __global__ __launch_bounds__(kFwdThreads) void router_kernel(Fwd p) {
   for (int j = 0; j < EPL; ++j) acc[j] = 0.0f;
   int live_tokens = 0;
   bool bad = false;
+  float* mine = rows[tid >> 4];
+  const int64_t stride = (int64_t)gridDim.x * kFwdTokens;
+  int64_t t = (int64_t)blockIdx.x * kFwdTokens + (tid >> 4);
+  float next[EPL];
+  const auto load = [&](int64_t token) {
+    const bool routed = token < p.tokens && (p.mask == nullptr || p.mask[token] != 0);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) next[j] = -INFINITY;
+    if (routed) load_row<DT, EPL, RUNS>(p.logits + token * p.ld, slot, E, next);
+  };
+  load(t);
   for (int64_t base = (int64_t)blockIdx.x * kFwdTokens; base < p.tokens;
-       base += (int64_t)gridDim.x * kFwdTokens) {
-    const int64_t t = base + w * (64 / kLanes) + (lane >> 4);
-    const bool here = t < p.tokens;
-    const char* row = p.logits + t * p.ld;
-    bool live = here && (p.mask == nullptr || p.mask[t] != 0);
-    float v[EPL];
+       base += stride, t += stride) {
+    // opaque: keeps what every expert's index gives from being held over the loop
+    asm volatile("" : "+v"(slot));
+    float v[EPL], ex[EPL];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) v[j] = -INFINITY;
-    if (live) load_row<DT, EPL>(row, e0, E, v);
-    bool any = false;
-    float m = v[0];
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      any |= !(v[j] == -INFINITY);
-      m = fmaxf(m, v[j]);
-    }
-    m = max16(m);
-    live = ballot16(any, lane) != 0;
-    float ex[EPL], s = 0.0f;
+    for (int j = 0; j < EPL; ++j) v[j] = next[j];
+    if (base + stride < p.tokens) load(t + stride);
+    const Softmax sm = softmax(v, ex);
+    bad |= sm.live && !(sm.sum < INFINITY);
+    wave_fence();
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-      ex[j] = exp_le0(v[j] - m);
-      s += v[j] == -INFINITY ? 0.0f : ex[j];
+      acc[j] = fmaf(ex[j], sm.inv, acc[j]);
+      mine[expert_of<DT, EPL>(slot, j)] = ex[j];
     }
-    s = sum16(s);
-    bad |= live && !(s < INFINITY);
-    const float inv = 1.0f / s;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      acc[j] += !live || (v[j] == -INFINITY && s < INFINITY) ? 0.0f : ex[j] * inv;
-    live_tokens += live ? 1 : 0;
-    const int e = choose<DT, EPL>(v, e0, E, k, lane);
-    float weight = 0.0f;
-    if (e >= 0) weight = exp_le0(load_one<DT>(row, e) - m) * inv;
+    wave_fence();
+    live_tokens += sm.live ? 1 : 0;
+    const int e = choose<DT, EPL>(v, slot, E, k);
+    float weight = e >= 0 ? mine[e] * sm.inv : 0.0f;
     if (p.normalize) {
       const float all = sum16(weight);
       weight = e >= 0 ? weight / all : 0.0f;
     }
-    if (here && slot < k) {
+    if (t < p.tokens && slot < k) {
       p.experts[t * k + slot] = e;
       p.weights[t * k + slot] = weight;
       if (e >= 0) atomicAdd(&hist[e], 1);
     }
   }
+  __syncthreads();
   if (__any(bad) && lane == 0) dev_status_or(p.status, kDevNonFinite);
   // the wave's four tokens, then the waves
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     acc[j] += __shfl_xor(acc[j], 16, 64);
     acc[j] += __shfl_xor(acc[j], 32, 64);
-    if (lane < kLanes) sums[w][e0 + j] = acc[j];
+    if (lane < kLanes) sums[w][expert_of<DT, EPL>(slot, j)] = acc[j];
   }
   live_tokens += __shfl_xor(live_tokens, 16, 64);
   live_tokens += __shfl_xor(live_tokens, 32, 64);
@@ -359,10 +437,7 @@ __global__ __launch_bounds__(kFwdThreads) void router_kernel(Fwd p) {
     for (int i = 0; i < kFwdWaves; ++i) sum += sums[i][tid];
   }
   if (gridDim.x > 1) {
-    if (tid < E) {
-      p.part_sums[(int64_t)blockIdx.x * E + tid] = sum;
-      p.part_counts[(int64_t)blockIdx.x * E + tid] = hist[tid];
-    }
+    if (tid < E) p.parts[(int64_t)blockIdx.x * E + tid] = v2i{__float_as_int(sum), hist[tid]};
     if (tid == 0) p.part_live[blockIdx.x] = live;
     return;
   }
@@ -398,8 +473,10 @@ __global__ __launch_bounds__(kFinishThreads) void router_finish_kernel(Fwd p, in
   if (expert < p.E) {
 #pragma unroll 8
     for (int b = i; b < parts; b += 16) {
-      s += (double)p.part_sums[(int64_t)b * p.E + expert];
-      c += p.part_counts[(int64_t)b * p.E + expert];
+      const v2i v = p.parts[(int64_t)b * p.E + expert];
+      const int bits = v[0];
+      s += (double)__int_as_float(bits);
+      c += v[1];
     }
   }
   sums[i][e] = s;
@@ -427,7 +504,8 @@ __global__ __launch_bounds__(kFinishThreads) void router_finish_kernel(Fwd p, in
   double all = tid < p.E ? __hip_atomic_load(p.products + tid, __ATOMIC_RELAXED,
                                              __HIP_MEMORY_SCOPE_AGENT)
                          : 0.0;
-  int live = tid < parts ? p.part_live[tid] : 0;
+  int live = 0;
+  for (int b = tid; b < parts; b += kFinishThreads) live += p.part_live[b];
   all = wave_sum(all);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) live += __shfl_xor(live, d, 64);
@@ -442,7 +520,7 @@ __global__ __launch_bounds__(kFinishThreads) void router_finish_kernel(Fwd p, in
     *p.loss = balance_loss(waves[0] + waves[1] + waves[2] + waves[3], p.E, p.k, live);
   }
 }
-static_assert(kFwdBlocks <= kFinishThreads && kMaxExperts <= kFinishThreads, "a thread each");
+static_assert(kMaxExperts <= kFinishThreads, "a thread each");
 
 // ---------------------------------------------------------------- backward
 
@@ -462,11 +540,12 @@ struct Bwd {
 
 // What the slots add goes to the experts' lanes through LDS: a row of E floats a token,
 // zeros but for the slots, which are cleared again after they were read.
-template <int DT, int EPL>
+template <int DT, int EPL, bool RUNS>
 __global__ __launch_bounds__(kBwdThreads) void router_backward_kernel(Bwd p) {
   __shared__ __attribute__((aligned(16))) float slots[kBwdTokens][kLanes * EPL];
+  __shared__ __attribute__((aligned(16))) float probs[kBwdTokens][kLanes * EPL];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int slot = lane & (kLanes - 1), e0 = EPL * slot;
+  const int slot = lane & (kLanes - 1);
   const int E = p.E, k = p.k;
   float* mine = slots[tid >> 4];
   float b[EPL];
@@ -474,61 +553,48 @@ __global__ __launch_bounds__(kBwdThreads) void router_backward_kernel(Bwd p) {
   const float f = n > 0 ? (float)((double)*p.d_loss * E / ((double)k * n * n)) : 0.0f;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
-    mine[e0 + j] = 0.0f;
-    b[j] = f != 0.0f && e0 + j < E ? f * (float)p.counts[e0 + j] : 0.0f;
+    const int e = expert_of<DT, EPL>(slot, j);
+    mine[e] = 0.0f;
+    b[j] = f != 0.0f && e < E ? f * (float)p.counts[e] : 0.0f;
   }
   for (int64_t base = (int64_t)blockIdx.x * kBwdTokens; base < p.tokens;
        base += (int64_t)gridDim.x * kBwdTokens) {
     const int64_t t = base + (tid >> 4);
     const bool here = t < p.tokens;
     const char* row = p.logits + t * p.ld;
-    bool live = here && (p.mask == nullptr || p.mask[t] != 0);
-    float v[EPL];
+    const bool routed = here && (p.mask == nullptr || p.mask[t] != 0);
+    float v[EPL], prob[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) v[j] = -INFINITY;
-    if (live) load_row<DT, EPL>(row, e0, E, v);
+    if (routed) load_row<DT, EPL, RUNS>(row, slot, E, v);
     int e = -1;
     float dw = 0.0f;
-    if (live && slot < k && p.d_weights != nullptr) {
+    if (routed && slot < k && p.d_weights != nullptr) {
       e = p.experts[t * k + slot];
       if (e < 0 || e >= E) e = -1;
       if (e >= 0) dw = p.d_weights[t * k + slot];
     }
-    bool any = false;
-    float m = v[0];
+    const Softmax sm = softmax(v, prob);
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      any |= !(v[j] == -INFINITY);
-      m = fmaxf(m, v[j]);
-    }
-    m = max16(m);
-    live = ballot16(any, lane) != 0;
-    float prob[EPL], s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      prob[j] = exp_le0(v[j] - m);
-      s += v[j] == -INFINITY ? 0.0f : prob[j];
-    }
-    s = sum16(s);
-    const float inv = 1.0f / s;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      prob[j] = v[j] == -INFINITY && s < INFINITY ? 0.0f : prob[j] * inv;
+    for (int j = 0; j < EPL; ++j) prob[j] *= sm.inv;
     float add = dw;
     if (p.normalize) {
-      float weight = e >= 0 ? exp_le0(load_one<DT>(row, e) - m) * inv : 0.0f;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) probs[tid >> 4][expert_of<DT, EPL>(slot, j)] = prob[j];
+      wave_fence();
+      float weight = e >= 0 ? probs[tid >> 4][e] : 0.0f;
       const float all = sum16(weight);
       weight = e >= 0 ? weight / all : 0.0f;
       add = weight * (dw - sum16(e >= 0 ? weight * dw : 0.0f));
     }
     if (e >= 0) atomicAdd(&mine[e], add);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    wave_fence();
     float a[EPL], dot = 0.0f, given[EPL];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) given[j] = mine[e0 + j];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    for (int j = 0; j < EPL; ++j) given[j] = mine[expert_of<DT, EPL>(slot, j)];
+    wave_fence();
     if (e >= 0) mine[e] = 0.0f;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    wave_fence();
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
       a[j] = p.normalize ? b[j] : b[j] + given[j];
@@ -538,20 +604,28 @@ __global__ __launch_bounds__(kBwdThreads) void router_backward_kernel(Bwd p) {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
       const float d = prob[j] * (a[j] - dot) + (p.normalize ? given[j] : 0.0f);
-      a[j] = live ? d : 0.0f;
+      a[j] = sm.live ? d : 0.0f;
     }
-    if (here) store_row<DT, EPL>(p.out + t * p.ldo, e0, E, a);
+    if (here) store_row<DT, EPL, RUNS>(p.out + t * p.ldo, slot, E, a);
   }
 }
 
-// f<DT, EPL> for a type and a number of experts.
+// f<DT, EPL, RUNS> for a type and a number of experts.
+template <int DT, int EPL, typename F>
+hipError_t by_runs(int E, F f) {
+  const std::integral_constant<int, DT> dt;
+  const std::integral_constant<int, EPL> epl;
+  if constexpr (EPL > 1)
+    if (E % kRun<DT, EPL> != 0) return f(dt, epl, std::false_type{});
+  return f(dt, epl, std::true_type{});
+}
 template <int DT, typename F>
 hipError_t by_experts(int E, F f) {
-  if (E <= 16) return f(std::integral_constant<int, DT>{}, std::integral_constant<int, 1>{});
-  if (E <= 32) return f(std::integral_constant<int, DT>{}, std::integral_constant<int, 2>{});
-  if (E <= 64) return f(std::integral_constant<int, DT>{}, std::integral_constant<int, 4>{});
-  if (E <= 128) return f(std::integral_constant<int, DT>{}, std::integral_constant<int, 8>{});
-  return f(std::integral_constant<int, DT>{}, std::integral_constant<int, 16>{});
+  if (E <= 16) return by_runs<DT, 1>(E, f);
+  if (E <= 32) return by_runs<DT, 2>(E, f);
+  if (E <= 64) return by_runs<DT, 4>(E, f);
+  if (E <= 128) return by_runs<DT, 8>(E, f);
+  return by_runs<DT, 16>(E, f);
 }
 template <typename F>
 hipError_t by_type(int dtype, int E, F f) {
@@ -588,13 +662,11 @@ hipError_t launch_router(int dtype, const void* logits, int64_t ld, int64_t toke
   at += 8 * (size_t)E;
   p.part_live = reinterpret_cast<int32_t*>(at);
   at += 4 * (size_t)kFwdBlocks;
-  p.part_sums = reinterpret_cast<float*>(at);
-  at += 4 * (size_t)kFwdBlocks * (size_t)E;
-  p.part_counts = reinterpret_cast<int32_t*>(at);
+  p.parts = reinterpret_cast<v2i*>(at);
   const int64_t want = (tokens + kFwdTokens - 1) / kFwdTokens;
   const int blocks = tokens <= kOneBlock ? 1 : (int)(want < kFwdBlocks ? want : kFwdBlocks);
-  const hipError_t e = by_type(dtype, E, [&](auto dt, auto epl) {
-    hipLaunchKernelGGL((router_kernel<decltype(dt)::value, decltype(epl)::value>), dim3(blocks),
+  const hipError_t e = by_type(dtype, E, [&](auto dt, auto epl, auto runs) {
+    hipLaunchKernelGGL((router_kernel<decltype(dt)::value, decltype(epl)::value, decltype(runs)::value>), dim3(blocks),
                        dim3(kFwdThreads), 0, stream, p);
     return hipGetLastError();
   });
@@ -623,8 +695,8 @@ hipError_t launch_router_backward(int dtype, const void* logits, int64_t ld, int
   const int64_t want = (tokens + kBwdTokens - 1) / kBwdTokens;
   const int64_t cap = 8 * (int64_t)device_cu_count();
   const unsigned blocks = (unsigned)(want < cap ? want : cap);
-  return by_type(dtype, E, [&](auto dt, auto epl) {
-    hipLaunchKernelGGL((router_backward_kernel<decltype(dt)::value, decltype(epl)::value>),
+  return by_type(dtype, E, [&](auto dt, auto epl, auto runs) {
+    hipLaunchKernelGGL((router_backward_kernel<decltype(dt)::value, decltype(epl)::value, decltype(runs)::value>),
                        dim3(blocks), dim3(kBwdThreads), 0, stream, p);
     return hipGetLastError();
   });
