@@ -21,6 +21,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 KERNEL_SOURCES = ["offsets.hip", "quantize_mxfp8.hip", "quantize_nvfp4.hip", "gemm_mxfp8.hip",
                   "gemm_nvfp4.hip", "gemm_16bit.hip",
                   "gemm_16bit_large.hip", "gemm_16bit_small.hip", "grad_clip.hip", "gemm_int8.hip",
+                  "gemm_int8_few.hip",
                   "quantize_int8.hip", "router.hip", "swiglu_checkpoint.hip"]
 HOST_SOURCES = ["api.cpp"]
 

@@ -336,6 +336,15 @@ hipError_t launch_gemm_int8_dynamic(int in_f16, int G, const void* x, int64_t ld
 
 int gemm_int8_tile_rows(int64_t G, int64_t rows_cap, int64_t n, int64_t k, bool split);
 
+// The form of few rows.  tokens: x holds 16-bit tokens (a_scales is not read), at most 8 rows and
+// kFewTokenBytes integers of them; else integers.
+constexpr int64_t kFewTokenBytes = 8192;
+hipError_t launch_gemm_int8_few(int tokens, int in_f16, int G, const void* x, int64_t ldx,
+                                const float* a_scales, const int8_t* b, int64_t ldb,
+                                int64_t stride_b, const float* b_scales, const int64_t* offsets,
+                                int64_t rows_cap, int64_t n, int64_t k, void* out, int64_t ldo,
+                                int f16, int out_f32, uint32_t* status, hipStream_t stream);
+
 // data and scales null: nothing is kept.
 hipError_t launch_swiglu_checkpoint(int f16, const void* h, int64_t ldh, const float* w, int G,
                                     const int64_t* offsets, int64_t rows_cap, int64_t f, void* y,

@@ -34,8 +34,22 @@ hipError_t launch_small_int8(int f16, int bm, const Args& p, hipStream_t stream)
 
 }  // namespace g16
 
+namespace {
+
+// Whether the form of few rows runs.  It reads a group's weights once for 16 rows, the 32-row
+// tiles once for 32, at a lower rate and with a second step for split contractions.  us, few
+// rows and 32-row tiles, n x k 4096 x 4096: 16 rows of one group 9.7 and 14.2, 32 of eight 29.1
+// and 29.9, 64 of eight 30.5 and 30.3, 128 of eight 36 and 32; 2048 x 7168: 64 of 64 107 and
+// 118, 256 of 64 155 and 155.  Group sizes are on the device, and all rows may be one group's:
+// the second bound keeps that case's price down.
+bool few_rows(int64_t G, int64_t rows_cap) {
+  return rows_cap <= 16 || (rows_cap <= 4 * G && rows_cap <= 256);
+}
+
+}  // namespace
+
 int gemm_int8_tile_rows(int64_t G, int64_t rows_cap, int64_t n, int64_t k, bool split) {
-  return form_rows(kInt8, G, rows_cap, n, k / 2, split);
+  return few_rows(G, rows_cap) ? 16 : form_rows(kInt8, G, rows_cap, n, k / 2, split);
 }
 
 hipError_t launch_gemm_int8(int G, const int8_t* a, int64_t lda, const float* a_scales,
@@ -43,6 +57,9 @@ hipError_t launch_gemm_int8(int G, const int8_t* a, int64_t lda, const float* a_
                             const int64_t* offsets, int64_t rows_cap, int64_t n, int64_t k,
                             void* out, int64_t ldo, int f16, int out_f32, void* ws,
                             uint32_t* status, hipStream_t stream) {
+  if (few_rows(G, rows_cap))
+    return launch_gemm_int8_few(0, 0, G, a, lda, a_scales, b, ldb, stride_b, b_scales, offsets,
+                                rows_cap, n, k, out, ldo, f16, out_f32, status, stream);
   Args p{};
   p.a = reinterpret_cast<const uint16_t*>(a);
   p.b = reinterpret_cast<const uint16_t*>(b);
@@ -72,6 +89,11 @@ hipError_t launch_gemm_int8_dynamic(int in_f16, int G, const void* x, int64_t ld
                                     const int64_t* offsets, int64_t rows_cap, int64_t n, int64_t k,
                                     void* out, int64_t ldo, int f16, int out_f32, void* ws,
                                     uint32_t* status, hipStream_t stream) {
+  // a workgroup quantizes up to kFewTokenBytes of tokens faster than a launch of their own
+  // takes (4096 columns: 1 row 9.6 and 12.5 us, 4 rows 19 and 15)
+  if (rows_cap <= 8 && rows_cap * k <= kFewTokenBytes)
+    return launch_gemm_int8_few(1, in_f16, G, x, ldx, nullptr, b, ldb, stride_b, b_scales, offsets,
+                                rows_cap, n, k, out, ldo, f16, out_f32, status, stream);
   char* at = static_cast<char*>(ws) + gemm_16bit_workspace_bytes();
   float* scales = reinterpret_cast<float*>(at);
   int8_t* data = reinterpret_cast<int8_t*>(at + align256(4 * rows_cap));

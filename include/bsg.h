@@ -842,7 +842,8 @@ int grouped_quantize_int8(int in_dtype, const void* x, int64_t ldx, int64_t rows
  * Errors: BSG_ERR_NULL, BSG_ERR_SHAPE, BSG_ERR_UNSUPPORTED (types), BSG_ERR_ALIGN (a, x, b, out
  * and b_scales 16-byte, a_scales 4-byte), BSG_ERR_WORKSPACE.
  *
- * grouped_gemm_int8_tile_rows: as grouped_gemm_16bit_tile_rows, for both.
+ * grouped_gemm_int8_tile_rows: as grouped_gemm_16bit_tile_rows, for both; 16 is the form of
+ * few rows, which takes no workspace.
  */
 size_t grouped_gemm_int8_workspace_size(void);
 int grouped_gemm_int8_tile_rows(int64_t G, int64_t rows_cap, int64_t n, int64_t k,
