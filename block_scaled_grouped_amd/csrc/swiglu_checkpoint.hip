@@ -12,7 +12,10 @@
 // and y again, for the second product's weight gradient.
 //
 // HBM bound: forward 8 bytes and 1/16 an element of y, backward 10 and 1/16 (8 without y).
-// A wave takes 512 columns of both halves, a lane 8 of each: 16-byte loads and stores.
+// A wave takes 512 columns of both halves, a lane 8 of each: 16-byte loads and stores, and
+// the next 512 columns' loads before these are worked on.  A workgroup takes some whole rows, so
+// that one XCD's L2 holds the lines of their scale bytes, of which a wave writes 16 bytes at a
+// time, and its waves take the rows' chunks of 512 in turn.
 #include "bsg_internal.h"
 #include "mx_convert.h"
 
@@ -20,8 +23,8 @@ namespace bsg {
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kChunk = 512;  // columns of a wave
+constexpr int kMaxThreads = 1024;
 
 // g s(g) and s(g).  The exponential's error is under 2^-16 of an s below 2^-64, which
 // rounding to 16 bits hides, and 2^-22 around 1.
@@ -94,6 +97,50 @@ __device__ __forceinline__ Rows live_rows(const int64_t* offsets, int G, int64_t
   return r;
 }
 
+// A wave's chunks of its workgroup's rows: every waves-th of them, row after row.
+struct Walk {
+  int64_t row, last;
+  int c, unit;             // chunk of the row, and of the workgroup's rows
+  int chunks, waves, dr, dc;
+  __device__ __forceinline__ void init(const Rows& rows, int n, int rows_each) {
+    unit = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    waves = (int)(blockDim.x >> 6);
+    chunks = n;
+    dr = waves / n;
+    dc = waves - dr * n;
+    const int64_t first = rows.first + (int64_t)blockIdx.x * rows_each;
+    last = first + rows_each < rows.last ? first + rows_each : rows.last;
+    const int r = unit / n;
+    row = first + r;
+    c = unit - r * n;
+  }
+  __device__ __forceinline__ bool here() const { return row < last; }
+  __device__ __forceinline__ void next() {
+    unit += waves;
+    row += dr;
+    c += dc;
+    if (c >= chunks) {
+      c -= chunks;
+      ++row;
+    }
+  }
+};
+
+// STREAM: past the caches, for outputs that the last-level cache cannot hold for the next
+// reader (16384 x 14336, forward and backward, with 16 waves a row: 332 -> 308 and 414 -> 396
+// us; 32000 x 2080, whose outputs it can hold, backward: 85 -> 92 us).
+template <bool STREAM, typename T>
+__device__ __forceinline__ void store(void* to, const T& v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<T*>(to));
+  else *reinterpret_cast<T*>(to) = v;
+}
+
+template <bool F16, bool STREAM>
+__device__ __forceinline__ void store8(uint16_t* to, const float (&v)[8]) {
+  store<STREAM>(to, v4i{(int)pack16<F16>(v[0], v[1]), (int)pack16<F16>(v[2], v[3]),
+                        (int)pack16<F16>(v[4], v[5]), (int)pack16<F16>(v[6], v[7])});
+}
+
 struct Fwd {
   const uint16_t* h;
   int64_t ldh;
@@ -105,36 +152,46 @@ struct Fwd {
   uint8_t* data;
   uint8_t* scales;
   uint32_t* status;
-  int G;
+  int G, rows_each;
 };
 
-template <bool F16, bool KEEP>
-__global__ __launch_bounds__(kThreads) void swiglu_kernel(Fwd p) {
+template <bool F16, bool KEEP, bool STREAM>
+__global__ __launch_bounds__(kMaxThreads) void swiglu_kernel(Fwd p) {
   const Rows rows = live_rows(p.offsets, p.G, p.rows_cap, p.status);
   const int lane = threadIdx.x & 63;
-  const int f = (int)p.f, chunks = (f + kChunk - 1) / kChunk;
-  const int64_t units = (rows.last - rows.first) * chunks;
-  const int64_t stride = (int64_t)gridDim.x * (kThreads / 64);
-  for (int64_t unit = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); unit < units;
-       unit += stride) {
-    const int64_t row = rows.first + unit / chunks;
-    const int col = (int)(unit % chunks) * kChunk + 8 * lane;
-    const bool here = col < f;  // of four lanes or none: f is a multiple of 32
-    v4i g = v4i{0, 0, 0, 0}, u = v4i{0, 0, 0, 0};
-    if (here) {
-      const uint16_t* src = p.h + row * p.ldh + col;
-      g = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(src));
-      u = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(src + f));
+  const int f = (int)p.f;
+  Walk at;
+  at.init(rows, (f + kChunk - 1) / kChunk, p.rows_each);
+  v4i next_g, next_u;
+  float next_w = 1.0f;
+  const auto load = [&]() {
+    next_g = next_u = v4i{0, 0, 0, 0};
+    if (!at.here()) return;
+    const int col = at.c * kChunk + 8 * lane;
+    if (col < f) {  // of four lanes or none: f is a multiple of 32
+      const uint16_t* src = p.h + at.row * p.ldh + col;
+      next_g = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(src));
+      next_u = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(src + f));
     }
-    const float w = p.w != nullptr ? p.w[row] : 1.0f;
+    if (p.w != nullptr) next_w = p.w[at.row];
+  };
+  load();
+  while (at.here()) {
+    const v4i g = next_g, u = next_u;
+    const float w = next_w;
+    const int64_t row = at.row;
+    const int col = at.c * kChunk + 8 * lane;
+    const bool here = col < f;
+    at.next();
+    load();
     if constexpr (KEEP) {
       const uint32_t ag = block_amax(g), au = block_amax(u);
       const uint32_t bg = scale_byte<F16>(ag), bu = scale_byte<F16>(au);
       const v2i qg = codes8<F16>(g, bg), qu = codes8<F16>(u, bu);
       if (here) {
         uint8_t* dst = p.data + row * 2 * p.f + col;
-        *reinterpret_cast<v2i*>(dst) = qg;
-        *reinterpret_cast<v2i*>(dst + f) = qu;
+        store<true>(dst, qg);  // not read before the backward pass
+        store<true>(dst + f, qu);
         if ((lane & 3) == 0) {
           uint8_t* sc = p.scales + row * (p.f / 16) + col / 32;
           sc[0] = (uint8_t)bg;
@@ -150,10 +207,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_kernel(Fwd p) {
       const float x = elem<F16>(g, e);
       y[e] = w * (x * sigmoid(x)) * elem<F16>(u, e);
     }
-    if (here)
-      *reinterpret_cast<v4i*>(p.y + row * p.ldy + col) =
-          v4i{(int)pack16<F16>(y[0], y[1]), (int)pack16<F16>(y[2], y[3]),
-              (int)pack16<F16>(y[4], y[5]), (int)pack16<F16>(y[6], y[7])};
+    if (here) store8<F16, STREAM>(p.y + row * p.ldy + col, y);
   }
 }
 
@@ -171,7 +225,7 @@ struct Bwd {
   int64_t ldy;
   float* dw;
   uint32_t* status;
-  int G;
+  int G, rows_each;
 };
 
 // 8 kept values of a half.
@@ -188,104 +242,131 @@ __device__ __forceinline__ void decode8(const v2i& q, uint32_t byte, float (&v)[
   }
 }
 
-// One wave's 512 columns of a row; returns its share of dw.
-template <bool F16>
-__device__ __forceinline__ float backward_chunk(const Bwd& p, int64_t row, int col, float w) {
-  const int f = (int)p.f;
-  float dw = 0.0f;
-  if (col < f) {
-    const uint8_t* src = p.data + row * 2 * p.f + col;
-    const v2i qg = __builtin_nontemporal_load(reinterpret_cast<const v2i*>(src));
-    const v2i qu = __builtin_nontemporal_load(reinterpret_cast<const v2i*>(src + f));
-    const uint8_t* sc = p.scales + row * (p.f / 16) + col / 32;
-    const uint32_t bg = sc[0], bu = sc[f / 32];
-    const v4i d = __builtin_nontemporal_load(
-        reinterpret_cast<const v4i*>(p.dy + row * p.lddy + col));
-    float g[8], u[8], dg[8], du[8], y[8];
-    decode8(qg, bg, g);
-    decode8(qu, bu, u);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float s = sigmoid(g[e]), act = g[e] * s, dy = elem<F16>(d, e);
-      dw += dy * act * u[e];
-      const float dyw = dy * w;
-      du[e] = dyw * act;
-      dg[e] = dyw * u[e] * (s * fmaf(g[e], 1.0f - s, 1.0f));
-      y[e] = w * act * u[e];
-    }
-    const auto store = [&](uint16_t* at, const float (&v)[8]) {
-      *reinterpret_cast<v4i*>(at) =
-          v4i{(int)pack16<F16>(v[0], v[1]), (int)pack16<F16>(v[2], v[3]),
-              (int)pack16<F16>(v[4], v[5]), (int)pack16<F16>(v[6], v[7])};
-    };
-    store(p.dh + row * p.lddh + col, dg);
-    store(p.dh + row * p.lddh + f + col, du);
-    if (p.y != nullptr) store(p.y + row * p.ldy + col, y);
-  }
-  return dw;
-}
+// ROWSUM: dw of the rows, added up in one order: a lane's terms of a chunk, the lanes, and when
+// the rows are done their chunks.
+constexpr int kMaxUnits = 2048;  // of a workgroup, with ROWSUM
 
-// ROWSUM: a workgroup of WPR waves a row adds up dw in one order; else every wave takes
-// the next 512 columns wherever they lie.
-template <bool F16, bool ROWSUM, int WPR>
-__global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(Bwd p) {
+template <bool F16, bool ROWSUM, bool STREAM>
+__global__ __launch_bounds__(kMaxThreads) void swiglu_backward_kernel(Bwd p) {
+  __shared__ float part[ROWSUM ? kMaxUnits : 1];
   const Rows rows = live_rows(p.offsets, p.G, p.rows_cap, p.status);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int f = (int)p.f, chunks = (f + kChunk - 1) / kChunk;
-  if constexpr (!ROWSUM) {
-    const int64_t units = (rows.last - rows.first) * chunks;
-    const int64_t stride = (int64_t)gridDim.x * (kThreads / 64);
-    for (int64_t unit = (int64_t)blockIdx.x * (kThreads / 64) + wave; unit < units;
-         unit += stride) {
-      const int64_t row = rows.first + unit / chunks;
-      backward_chunk<F16>(p, row, (int)(unit % chunks) * kChunk + 8 * lane,
-                          p.w != nullptr ? p.w[row] : 1.0f);
+  const int lane = threadIdx.x & 63;
+  const int f = (int)p.f;
+  Walk at;
+  at.init(rows, (f + kChunk - 1) / kChunk, p.rows_each);
+  struct Kept {
+    v2i g, u;
+    v4i dy;
+    uint32_t bg, bu;
+    float w;
+  } next;
+  next.w = 1.0f;
+  const auto load = [&]() {
+    if (!at.here()) return;
+    const int col = at.c * kChunk + 8 * lane;
+    if (col < f) {
+      const uint8_t* src = p.data + at.row * 2 * p.f + col;
+      next.g = __builtin_nontemporal_load(reinterpret_cast<const v2i*>(src));
+      next.u = __builtin_nontemporal_load(reinterpret_cast<const v2i*>(src + f));
+      const uint8_t* sc = p.scales + at.row * (p.f / 16) + col / 32;
+      next.bg = sc[0];
+      next.bu = sc[f / 32];
+      next.dy = __builtin_nontemporal_load(
+          reinterpret_cast<const v4i*>(p.dy + at.row * p.lddy + col));
     }
-  } else {
-    constexpr int kRows = kThreads / 64 / WPR;
-    __shared__ float part[2][kThreads / 64];
-    const int64_t count = rows.last - rows.first;
-    int turn = 0;
-    for (int64_t r = (int64_t)blockIdx.x * kRows; r < count; r += (int64_t)gridDim.x * kRows) {
-      const int64_t row = rows.first + r + wave / WPR;
-      float dw = 0.0f;
-      if (row < rows.last) {
-        const float w = p.w != nullptr ? p.w[row] : 1.0f;
-        for (int c = wave % WPR; c < chunks; c += WPR)
-          dw += backward_chunk<F16>(p, row, c * kChunk + 8 * lane, w);
+    if (p.w != nullptr) next.w = p.w[at.row];
+  };
+  load();
+  while (at.here()) {
+    const Kept k = next;
+    const int64_t row = at.row;
+    const int col = at.c * kChunk + 8 * lane, unit = at.unit;
+    at.next();
+    load();
+    float dw = 0.0f;
+    if (col < f) {
+      float g[8], u[8], dg[8], du[8], y[8];
+      decode8(k.g, k.bg, g);
+      decode8(k.u, k.bu, u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float s = sigmoid(g[e]), act = g[e] * s, dy = elem<F16>(k.dy, e);
+        if constexpr (ROWSUM) dw += dy * act * u[e];
+        const float dyw = dy * k.w;
+        du[e] = dyw * act;
+        dg[e] = dyw * u[e] * (s * fmaf(g[e], 1.0f - s, 1.0f));
+        y[e] = k.w * act * u[e];
       }
+      store8<F16, STREAM>(p.dh + row * p.lddh + col, dg);
+      store8<F16, STREAM>(p.dh + row * p.lddh + f + col, du);
+      if (p.y != nullptr) store8<F16, STREAM>(p.y + row * p.ldy + col, y);
+    }
+    if constexpr (ROWSUM) {
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) dw += __shfl_xor(dw, d, 64);
-      if constexpr (WPR > 1) {
-        if (lane == 0) part[turn][wave] = dw;
-        __syncthreads();
-        dw = 0.0f;
+      if (lane == 0) part[unit] = dw;
+    }
+  }
+  if constexpr (ROWSUM) {
+    __syncthreads();
+    const int64_t first = rows.first + (int64_t)blockIdx.x * p.rows_each;
+    for (int r = (int)(threadIdx.x >> 6); first + r < at.last; r += at.waves) {
+      float dw = 0.0f;
+      for (int c = lane; c < at.chunks; c += 64) dw += part[r * at.chunks + c];
 #pragma unroll
-        for (int i = 0; i < WPR; ++i) dw += part[turn][wave / WPR * WPR + i];
-        turn ^= 1;  // the next row's parts go elsewhere: one barrier a row
-      }
-      if (lane == 0 && wave % WPR == 0 && row < rows.last) p.dw[row] = dw;
+      for (int d = 1; d < 64; d <<= 1) dw += __shfl_xor(dw, d, 64);
+      if (lane == 0) p.dw[first + r] = dw;
     }
   }
 }
 
-unsigned grid_for(int64_t workgroups) {
-  const int64_t cap = 32 * (int64_t)device_cu_count();
-  return (unsigned)(workgroups < cap ? workgroups : cap);
+// Workgroups of 16 waves where there is work for the chip in them (4 where not), and as many
+// rows in each as give a wave some kRounds chunks.  16384 x 14336, forward and backward, and
+// 32000 x 2080 backward, us: 16 waves and 2 chunks each 306, 391 and 83, 3 chunks 307, 392 and
+// 82 (6.2, 6.0 and 6.5 TB/s), 5 chunks 323, 402 and 84, 8 chunks 344, 431 and 86; 4 waves 348,
+// 441 and 87.
+constexpr int64_t kRounds = 3;
+
+struct Shape {
+  int rows_each;
+  unsigned grid, block;
+};
+Shape shape_of(int64_t rows_cap, int64_t f) {
+  const int64_t chunks = (f + kChunk - 1) / kChunk, units = rows_cap * chunks;
+  const int64_t slots = 32 * (int64_t)device_cu_count();  // waves on the chip
+  const int64_t waves = units >= slots || chunks > 4 ? 16 : 4;
+  int64_t rounds = units / slots;
+  rounds = rounds < 1 ? 1 : rounds > kRounds ? kRounds : rounds;
+  int64_t each = waves * rounds / chunks;
+  if (each < 1) each = 1;
+  if (each * chunks > kMaxUnits) each = kMaxUnits / chunks;
+  // a launch has fewer than 2^32 threads
+  const int64_t least = (rows_cap + ((int64_t)1 << 20) - 1) >> 20;
+  if (each < least) each = least;
+  return {(int)each, (unsigned)((rows_cap + each - 1) / each), (unsigned)(64 * waves)};
 }
 
-template <bool F16>
+constexpr int64_t kCacheBytes = (int64_t)256 << 20;  // of the last level
+
+template <typename K, typename P>
+hipError_t run(K kernel, P p, hipStream_t stream) {
+  const Shape s = shape_of(p.rows_cap, p.f);
+  p.rows_each = s.rows_each;
+  hipLaunchKernelGGL(kernel, dim3(s.grid), dim3(s.block), 0, stream, p);
+  return hipGetLastError();
+}
+
+template <bool F16, bool KEEP>
+hipError_t launch_forward(const Fwd& p, hipStream_t stream) {
+  if (2 * p.rows_cap * p.f > kCacheBytes) return run(swiglu_kernel<F16, KEEP, true>, p, stream);
+  return run(swiglu_kernel<F16, KEEP, false>, p, stream);
+}
+
+template <bool F16, bool ROWSUM>
 hipError_t launch_backward(const Bwd& p, hipStream_t stream) {
-  const int64_t chunks = (p.f + kChunk - 1) / kChunk;
-  const auto run = [&](auto kernel, int64_t workgroups) {
-    hipLaunchKernelGGL(kernel, dim3(grid_for(workgroups)), dim3(kThreads), 0, stream, p);
-    return hipGetLastError();
-  };
-  if (p.dw == nullptr)
-    return run(swiglu_backward_kernel<F16, false, 1>, (p.rows_cap * chunks + 3) / 4);
-  if (chunks == 1) return run(swiglu_backward_kernel<F16, true, 1>, (p.rows_cap + 3) / 4);
-  if (chunks == 2) return run(swiglu_backward_kernel<F16, true, 2>, (p.rows_cap + 1) / 2);
-  return run(swiglu_backward_kernel<F16, true, 4>, p.rows_cap);
+  if ((p.y != nullptr ? 6 : 4) * p.rows_cap * p.f > 2 * kCacheBytes)
+    return run(swiglu_backward_kernel<F16, ROWSUM, true>, p, stream);
+  return run(swiglu_backward_kernel<F16, ROWSUM, false>, p, stream);
 }
 
 }  // namespace
@@ -296,14 +377,10 @@ hipError_t launch_swiglu_checkpoint(int f16, const void* h, int64_t ldh, const f
                                     hipStream_t stream) {
   if (rows_cap == 0) return hipSuccess;
   const Fwd p{static_cast<const uint16_t*>(h), ldh, w, offsets, rows_cap, f,
-              static_cast<uint16_t*>(y), ldy, data, scales, status, G};
-  const dim3 grid(grid_for((rows_cap * ((f + kChunk - 1) / kChunk) + 3) / 4));
-  const auto run = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, p);
-    return hipGetLastError();
-  };
-  if (data != nullptr) return f16 ? run(swiglu_kernel<true, true>) : run(swiglu_kernel<false, true>);
-  return f16 ? run(swiglu_kernel<true, false>) : run(swiglu_kernel<false, false>);
+              static_cast<uint16_t*>(y), ldy, data, scales, status, G, 0};
+  if (data != nullptr)
+    return f16 ? launch_forward<true, true>(p, stream) : launch_forward<false, true>(p, stream);
+  return f16 ? launch_forward<true, false>(p, stream) : launch_forward<false, false>(p, stream);
 }
 
 hipError_t launch_swiglu_checkpoint_backward(int f16, const uint8_t* data, const uint8_t* scales,
@@ -313,8 +390,10 @@ hipError_t launch_swiglu_checkpoint_backward(int f16, const uint8_t* data, const
                                              float* dw, uint32_t* status, hipStream_t stream) {
   if (rows_cap == 0) return hipSuccess;
   const Bwd p{data, scales, w, static_cast<const uint16_t*>(dy), lddy, offsets, rows_cap, f,
-              static_cast<uint16_t*>(dh), lddh, static_cast<uint16_t*>(y), ldy, dw, status, G};
-  return f16 ? launch_backward<true>(p, stream) : launch_backward<false>(p, stream);
+              static_cast<uint16_t*>(dh), lddh, static_cast<uint16_t*>(y), ldy, dw, status, G, 0};
+  if (dw != nullptr)
+    return f16 ? launch_backward<true, true>(p, stream) : launch_backward<false, true>(p, stream);
+  return f16 ? launch_backward<true, false>(p, stream) : launch_backward<false, false>(p, stream);
 }
 
 }  // namespace bsg
