@@ -109,13 +109,18 @@ __device__ __forceinline__ void mfma(const Half& a, const Half& b, v4f (&acc)[8]
 // Wait states before the accumulators of a run are read by vector instructions.
 __device__ __forceinline__ void mfma_drain() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
+template <int MODE>
+__device__ __forceinline__ void aim_at_tile(Copies<MODE>& c, const Tile& t, int w, int lane) {
+  c.a.init(t.a, t.lda, t.a_rows, t.kl, w, lane);
+  c.b.init(t.b, t.ldb, t.b_rows, t.kl, w, lane);
+  c.stages = uni((t.kl + kStageK - 1) / kStageK);
+}
+
 // Begins a tile: the copies of its first two stages, into the two buffers.
 template <int MODE>
 __device__ __forceinline__ void begin_tile(Copies<MODE>& c, uint32_t lds, const Tile& t, int w,
                                            int lane) {
-  c.a.init(t.a, t.lda, t.a_rows, t.kl, w, lane);
-  c.b.init(t.b, t.ldb, t.b_rows, t.kl, w, lane);
-  c.stages = uni((t.kl + kStageK - 1) / kStageK);
+  aim_at_tile(c, t, w, lane);
   if (c.stages == 0) return;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
@@ -129,8 +134,9 @@ __device__ __forceinline__ void begin_tile(Copies<MODE>& c, uint32_t lds, const 
 }
 
 // A tile's contraction, begun by begin_tile.  stored: the epilogue of the tile before
-// came after those copies, with at least kEpilogueStores stores.
-constexpr int kEpilogueStores = 32;
+// came after those copies, with at least kEpilogueStores stores (INT8: between them, 16 after
+// the first stage's).
+template <int MODE> constexpr int kEpilogueStores = MODE == kInt8 ? 16 : 32;
 
 template <int MODE, bool F16>
 __device__ __forceinline__ void contract(Copies<MODE>& c, uint32_t lds, int w, int lane,
@@ -146,7 +152,7 @@ __device__ __forceinline__ void contract(Copies<MODE>& c, uint32_t lds, int w, i
   fa.init(lds, (w >> 1) * 128, lane);
   fb.init(lds + kTileBytes, (w & 1) * 128, lane);
   c.lds = uni(lds + w * 1024);
-  if (stored) wait_and_barrier<kCopies + kEpilogueStores>();
+  if (stored) wait_and_barrier<kCopies + kEpilogueStores<MODE>>();
   else wait_and_barrier<kCopies>();
   Half a0, b0, a1, b1;
   static_for<16>([&](auto q) { read_frag<MODE, 0, decltype(q)::value>(fa, fb, a0, b0); });
@@ -193,13 +199,63 @@ __device__ __forceinline__ void contract(Copies<MODE>& c, uint32_t lds, int w, i
   fence();
 }
 
-// A tile's copies are begun before the epilogue of the one before it, so that they
-// arrive while that one's stores go out.
+// INT8: a tile's output, with the 32 copies of the next tile's first two stages (`more`) between
+// its 32 pairs of blocks: copies and stores keep the memory path busy where the vector units
+// alone would (a contraction is half as long as a 16-bit one's, and the end of a tile, copies and
+// then stores, took 13 000 of its 87 000 cycles at k = 4096).  scales: of the tile's rows, then
+// of its columns, in LDS.
+template <bool F16, bool F32>
+__device__ __forceinline__ void store_int8(const v4f (&acc)[8][8], const OutTile& o,
+                                           const float* scales, int wrow, int wcol, int w,
+                                           int lane, Copies<kInt8>& c, uint32_t lds, bool more) {
+  constexpr int esz = F32 ? 4 : 2;
+  int ldo = o.ldo;
+  asm volatile("" : "+s"(ldo));  // keeps all the store offsets from being hoisted
+  const __amdgpu_buffer_rsrc_t ro = make_rsrc(o.out, (int64_t)o.rows * o.ldo * esz);
+  const int q = lane >> 4, row = wrow + (lane & 15);
+  v4f cscale[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    cscale[j] = *reinterpret_cast<const v4f*>(scales + BM + wcol + 16 * j + 4 * q);
+  static_for<8>([&](auto ic) {
+    constexpr int i = decltype(ic)::value;
+    const float rscale = scales[row + 16 * i];
+    static_for<4>([&](auto jc) {
+      constexpr int j = 2 * decltype(jc)::value, P = 4 * i + decltype(jc)::value;
+      int voff = 0;
+      fence();
+      if (more) {
+        if constexpr (P % kCopies == 0) {
+          constexpr int S = P / kCopies;
+          c.lds = uni(lds + S * kBufBytes + w * 1024);
+          c.begin(S);
+        }
+        voff = c.template copy_begin<P % kCopies>();
+      }
+      fence();
+      v4f y0 = acc[i][j], y1 = acc[i][j + 1];
+      asm volatile("" : "+v"(y0), "+v"(y1));
+      const v4i s0 = __builtin_bit_cast(v4i, y0), s1 = __builtin_bit_cast(v4i, y1);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y0[e] = ((float)s0[e] * rscale) * cscale[j][e];
+        y1[e] = ((float)s1[e] * rscale) * cscale[j + 1][e];
+      }
+      if (more) c.template copy_end<P % kCopies>(voff);
+      store_pair<F32, F16>(y0, y1, ro, ldo, row + 16 * i, wcol + 16 * j, q, o.cols);
+      fence();
+    });
+  });
+}
+
+// A tile's copies are begun before the epilogue of the one before it (INT8: in it), so that
+// they arrive while that one's stores go out.
 template <int MODE, bool F16>
 __global__ __launch_bounds__(kThreads) void large_kernel(Args p) {
   __shared__ __attribute__((aligned(16))) uint8_t ring[2 * kBufBytes];
   __shared__ Sched sm;
   __shared__ int ids[MODE == kLora ? BM : 1];
+  __shared__ __attribute__((aligned(16))) float scales[MODE == kInt8 ? BM + BN : 4];
   const uint32_t lds = lds_offset(ring);
   const int total = count_tiles<MODE, BM, BN>(p, sm);
   const Rounds rounds = plan_rounds<MODE, false>(p, total);
@@ -227,7 +283,17 @@ __global__ __launch_bounds__(kThreads) void large_kernel(Args p) {
         asm volatile("" : "+a"(acc[i][j]));
       }
     if constexpr (MODE == kLora) tile_adapters<BM>(p, sm, t, ids);
+    float rscale = 0.0f, cscale = 0.0f;
+    if constexpr (MODE == kInt8) {
+      // a row and a column a thread; they arrive during the contraction
+      if (tid < t.a_rows) rscale = p.a_scales[t.row0 + tid];
+      if (tid < t.b_rows) cscale = p.b_scales[t.col0 + tid];
+    }
     contract<MODE, F16>(c, lds, w, lane, stored, acc);
+    if constexpr (MODE == kInt8) {
+      scales[tid] = rscale;
+      scales[BM + tid] = cscale;
+    }
     // every copy has landed and no wave still reads a buffer before the next
     // tile's first copies
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -236,7 +302,8 @@ __global__ __launch_bounds__(kThreads) void large_kernel(Args p) {
     if (next.tile >= 0) {
       tn = find_tile<MODE, BM, BN>(p, sm, uni(next.tile));
       if (next.part >= 0) narrow_tile<MODE>(tn, uni(next.part), nsplit);
-      begin_tile(c, lds, tn, w, lane);
+      if (MODE == kInt8 && work.part < 0) aim_at_tile(c, tn, w, lane);
+      else begin_tile(c, lds, tn, w, lane);
     }
     if constexpr (MODE == kLora) {
       add_low_rank<F16, 8, 8>(p, t, ids, wrow, wcol, lane, uni(work.part), work.nparts, acc);
@@ -247,6 +314,12 @@ __global__ __launch_bounds__(kThreads) void large_kernel(Args p) {
       store_part<8, 8>(
           reinterpret_cast<float*>(p.ws + kWsHeader + (int64_t)work.slot * kPartBytes), acc, w,
           lane, wrow, t.a_rows);
+    } else if constexpr (MODE == kInt8) {
+      const bool more = next.tile >= 0;
+      if (p.out_f32)
+        store_int8<F16, true>(acc, out_tile<MODE>(p, t), scales, wrow, wcol, w, lane, c, lds, more);
+      else
+        store_int8<F16, false>(acc, out_tile<MODE>(p, t), scales, wrow, wcol, w, lane, c, lds, more);
     } else {
       store_blocks<MODE, F16, 8, 8>(acc, out_tile<MODE>(p, t), p.out_f32, wrow, wcol, lane);
     }

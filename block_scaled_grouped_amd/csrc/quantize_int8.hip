@@ -95,6 +95,8 @@ hipError_t launch(const Args& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// 256 threads a row from 2048 columns on: 114688 x 4096 227 us (6.2 TB/s), with 512 threads 279;
+// 32768 x 7168 121 us, with 512 threads 126, with 1024 166.
 template <bool F16>
 hipError_t launch_type(const Args& p, hipStream_t stream) {
   if (p.cols <= 512) return launch<F16, 64, 1, false>(p, stream);
