@@ -752,6 +752,15 @@ struct Addend {
 //   16-bit:  lanes trade halves of the two blocks (v_permlane16_swap), after which
 //            lane (r, q) holds columns 8 (q / 2) + [0, 8) of block q % 2: 16 bytes
 //            a lane, and again 64-byte runs of 16 rows.
+template <bool F16>
+__device__ __forceinline__ v4i swap_pair(const v4f& y0, const v4f& y1) {
+  const auto lo = __builtin_amdgcn_permlane16_swap((int)pack16<F16>(y0[0], y0[1]),
+                                                   (int)pack16<F16>(y1[0], y1[1]), false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap((int)pack16<F16>(y0[2], y0[3]),
+                                                   (int)pack16<F16>(y1[2], y1[3]), false, false);
+  return v4i{(int)lo[0], (int)hi[0], (int)lo[1], (int)hi[1]};
+}
+
 template <bool F32, bool F16>
 __device__ __forceinline__ void store_pair(const v4f& y0, const v4f& y1, __amdgpu_buffer_rsrc_t ro,
                                            int ldo, int row, int col0, int q, int out_cols) {
@@ -762,13 +771,9 @@ __device__ __forceinline__ void store_pair(const v4f& y0, const v4f& y1, __amdgp
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, y1), ro,
                                            block_off<4>(ldo, row, col + 16, out_cols), 0, 0);
   } else {
-    const auto lo = __builtin_amdgcn_permlane16_swap((int)pack16<F16>(y0[0], y0[1]),
-                                                     (int)pack16<F16>(y1[0], y1[1]), false, false);
-    const auto hi = __builtin_amdgcn_permlane16_swap((int)pack16<F16>(y0[2], y0[3]),
-                                                     (int)pack16<F16>(y1[2], y1[3]), false, false);
     const int col = col0 + 16 * (q & 1) + 8 * (q >> 1);
-    __builtin_amdgcn_raw_buffer_store_b128((v4i){(int)lo[0], (int)hi[0], (int)lo[1], (int)hi[1]},
-                                           ro, block_off<2>(ldo, row, col, out_cols), 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(swap_pair<F16>(y0, y1), ro,
+                                           block_off<2>(ldo, row, col, out_cols), 0, 0);
   }
 }
 

@@ -199,20 +199,23 @@ __device__ __forceinline__ void contract(Copies<MODE>& c, uint32_t lds, int w, i
   fence();
 }
 
-// INT8: a tile's output, with the 32 copies of the next tile's first two stages (`more`) between
+// INT8: a tile's output, with the 32 copies of the next tile's first two stages (MORE) between
 // its 32 pairs of blocks: copies and stores keep the memory path busy where the vector units
 // alone would (a contraction is half as long as a 16-bit one's, and the end of a tile, copies and
 // then stores, took 13 000 of its 87 000 cycles at k = 4096).  scales: of the tile's rows, then
 // of its columns, in LDS.
-template <bool F16, bool F32>
+// WHOLE: the tile has all its columns, so that a store's place is a lane's and a uniform offset.
+template <bool F16, bool F32, bool WHOLE, bool MORE>
 __device__ __forceinline__ void store_int8(const v4f (&acc)[8][8], const OutTile& o,
                                            const float* scales, int wrow, int wcol, int w,
-                                           int lane, Copies<kInt8>& c, uint32_t lds, bool more) {
+                                           int lane, Copies<kInt8>& c, uint32_t lds) {
   constexpr int esz = F32 ? 4 : 2;
+  static_assert(!(WHOLE && F32), "16-bit outputs");
   int ldo = o.ldo;
   asm volatile("" : "+s"(ldo));  // keeps all the store offsets from being hoisted
   const __amdgpu_buffer_rsrc_t ro = make_rsrc(o.out, (int64_t)o.rows * o.ldo * esz);
   const int q = lane >> 4, row = wrow + (lane & 15);
+  const int place = (row * ldo + wcol + 16 * (q & 1) + 8 * (q >> 1)) * 2;
   v4f cscale[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -224,7 +227,7 @@ __device__ __forceinline__ void store_int8(const v4f (&acc)[8][8], const OutTile
       constexpr int j = 2 * decltype(jc)::value, P = 4 * i + decltype(jc)::value;
       int voff = 0;
       fence();
-      if (more) {
+      if constexpr (MORE) {
         if constexpr (P % kCopies == 0) {
           constexpr int S = P / kCopies;
           c.lds = uni(lds + S * kBufBytes + w * 1024);
@@ -241,11 +244,29 @@ __device__ __forceinline__ void store_int8(const v4f (&acc)[8][8], const OutTile
         y0[e] = ((float)s0[e] * rscale) * cscale[j][e];
         y1[e] = ((float)s1[e] * rscale) * cscale[j + 1][e];
       }
-      if (more) c.template copy_end<P % kCopies>(voff);
-      store_pair<F32, F16>(y0, y1, ro, ldo, row + 16 * i, wcol + 16 * j, q, o.cols);
+      if constexpr (MORE) c.template copy_end<P % kCopies>(voff);
+      if constexpr (WHOLE) {
+        __builtin_amdgcn_raw_buffer_store_b128(swap_pair<F16>(y0, y1), ro, place + 32 * j,
+                                               32 * i * ldo, 0);
+      } else {
+        store_pair<F32, F16>(y0, y1, ro, ldo, row + 16 * i, wcol + 16 * j, q, o.cols);
+      }
       fence();
     });
   });
+}
+
+template <bool F16, bool MORE>
+__device__ __forceinline__ void store_tile_int8(const v4f (&acc)[8][8], const OutTile& o,
+                                                int out_f32, const float* scales, int wrow,
+                                                int wcol, int w, int lane, Copies<kInt8>& c,
+                                                uint32_t lds) {
+  if (out_f32)
+    store_int8<F16, true, false, MORE>(acc, o, scales, wrow, wcol, w, lane, c, lds);
+  else if (o.cols == BN)
+    store_int8<F16, false, true, MORE>(acc, o, scales, wrow, wcol, w, lane, c, lds);
+  else
+    store_int8<F16, false, false, MORE>(acc, o, scales, wrow, wcol, w, lane, c, lds);
 }
 
 // A tile's copies are begun before the epilogue of the one before it (INT8: in it), so that
@@ -315,11 +336,11 @@ __global__ __launch_bounds__(kThreads) void large_kernel(Args p) {
           reinterpret_cast<float*>(p.ws + kWsHeader + (int64_t)work.slot * kPartBytes), acc, w,
           lane, wrow, t.a_rows);
     } else if constexpr (MODE == kInt8) {
-      const bool more = next.tile >= 0;
-      if (p.out_f32)
-        store_int8<F16, true>(acc, out_tile<MODE>(p, t), scales, wrow, wcol, w, lane, c, lds, more);
+      const OutTile o = out_tile<MODE>(p, t);
+      if (next.tile >= 0)
+        store_tile_int8<F16, true>(acc, o, p.out_f32, scales, wrow, wcol, w, lane, c, lds);
       else
-        store_int8<F16, false>(acc, out_tile<MODE>(p, t), scales, wrow, wcol, w, lane, c, lds, more);
+        store_tile_int8<F16, false>(acc, o, p.out_f32, scales, wrow, wcol, w, lane, c, lds);
     } else {
       store_blocks<MODE, F16, 8, 8>(acc, out_tile<MODE>(p, t), p.out_f32, wrow, wcol, lane);
     }
