@@ -545,7 +545,7 @@ __global__ __launch_bounds__(kBwdThreads) void router_backward_kernel(Bwd p) {
   __shared__ __attribute__((aligned(16))) float slots[kBwdTokens][kLanes * EPL];
   __shared__ __attribute__((aligned(16))) float probs[kBwdTokens][kLanes * EPL];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int slot = lane & (kLanes - 1);
+  int slot = lane & (kLanes - 1);
   const int E = p.E, k = p.k;
   float* mine = slots[tid >> 4];
   float b[EPL];
@@ -557,23 +557,33 @@ __global__ __launch_bounds__(kBwdThreads) void router_backward_kernel(Bwd p) {
     mine[e] = 0.0f;
     b[j] = f != 0.0f && e < E ? f * (float)p.counts[e] : 0.0f;
   }
+  const int64_t stride = (int64_t)gridDim.x * kBwdTokens;
+  int64_t t = (int64_t)blockIdx.x * kBwdTokens + (tid >> 4);
+  float next[EPL], next_dw = 0.0f;
+  int next_e = -1;
+  const auto load = [&](int64_t token) {
+    const bool routed = token < p.tokens && (p.mask == nullptr || p.mask[token] != 0);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) next[j] = -INFINITY;
+    next_e = -1;
+    if (!routed) return;
+    load_row<DT, EPL, RUNS>(p.logits + token * p.ld, slot, E, next);
+    if (slot < k && p.d_weights != nullptr) {
+      next_e = p.experts[token * k + slot];
+      next_dw = p.d_weights[token * k + slot];
+    }
+  };
+  load(t);
   for (int64_t base = (int64_t)blockIdx.x * kBwdTokens; base < p.tokens;
-       base += (int64_t)gridDim.x * kBwdTokens) {
-    const int64_t t = base + (tid >> 4);
-    const bool here = t < p.tokens;
-    const char* row = p.logits + t * p.ld;
-    const bool routed = here && (p.mask == nullptr || p.mask[t] != 0);
+       base += stride, t += stride) {
+    // opaque: keeps what every expert's index gives from being held over the loop
+    asm volatile("" : "+v"(slot));
     float v[EPL], prob[EPL];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) v[j] = -INFINITY;
-    if (routed) load_row<DT, EPL, RUNS>(row, slot, E, v);
-    int e = -1;
-    float dw = 0.0f;
-    if (routed && slot < k && p.d_weights != nullptr) {
-      e = p.experts[t * k + slot];
-      if (e < 0 || e >= E) e = -1;
-      if (e >= 0) dw = p.d_weights[t * k + slot];
-    }
+    for (int j = 0; j < EPL; ++j) v[j] = next[j];
+    const int e = next_e >= 0 && next_e < E ? next_e : -1;
+    const float dw = e >= 0 ? next_dw : 0.0f;
+    if (base + stride < p.tokens) load(t + stride);
     const Softmax sm = softmax(v, prob);
 #pragma unroll
     for (int j = 0; j < EPL; ++j) prob[j] *= sm.inv;
@@ -606,7 +616,7 @@ __global__ __launch_bounds__(kBwdThreads) void router_backward_kernel(Bwd p) {
       const float d = prob[j] * (a[j] - dot) + (p.normalize ? given[j] : 0.0f);
       a[j] = sm.live ? d : 0.0f;
     }
-    if (here) store_row<DT, EPL, RUNS>(p.out + t * p.ldo, slot, E, a);
+    if (t < p.tokens) store_row<DT, EPL, RUNS>(p.out + t * p.ldo, slot, E, a);
   }
 }
 
@@ -693,7 +703,7 @@ hipError_t launch_router_backward(int dtype, const void* logits, int64_t ld, int
   p.out = static_cast<char*>(out);
   p.ldo = ldo * element_bytes(dtype);
   const int64_t want = (tokens + kBwdTokens - 1) / kBwdTokens;
-  const int64_t cap = 8 * (int64_t)device_cu_count();
+  const int64_t cap = 4 * (int64_t)device_cu_count();
   const unsigned blocks = (unsigned)(want < cap ? want : cap);
   return by_type(dtype, E, [&](auto dt, auto epl, auto runs) {
     hipLaunchKernelGGL((router_backward_kernel<decltype(dt)::value, decltype(epl)::value, decltype(runs)::value>),
