@@ -26,7 +26,7 @@ struct Args {
 template <bool F16, int TPR, int NC, bool LONG>
 __global__ __launch_bounds__(kThreads) void quantize_int8_kernel(Args p) {
   constexpr int kRows = kThreads / TPR;
-  __shared__ uint32_t peak[kThreads / 64];
+  __shared__ uint32_t peak[2][kThreads / 64];
   int64_t first = 0, last = p.rows_cap;
   if (p.offsets != nullptr) {
     first = p.offsets[0];
@@ -38,50 +38,53 @@ __global__ __launch_bounds__(kThreads) void quantize_int8_kernel(Args p) {
     if (last > p.rows_cap) last = p.rows_cap;
   }
   const int t = threadIdx.x % TPR;
-  const int64_t row = first + (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
-  if (row >= last) return;  // of a whole wave, and where rows share barriers of the workgroup
-  const uint16_t* src = p.x + row * p.ldx;
   const int cols = (int)p.cols;
-  v4i v[NC];
-  uint32_t m = 0;
-  for (int base = 0; base < (LONG ? cols : 1); base += 8 * TPR * NC) {
+  int turn = 0;
+  for (int64_t row = first + (int64_t)blockIdx.x * kRows + threadIdx.x / TPR; row < last;
+       row += (int64_t)gridDim.x * kRows) {  // the same for all threads that share a barrier
+    const uint16_t* src = p.x + row * p.ldx;
+    v4i v[NC];
+    uint32_t m = 0;
+    for (int base = 0; base < (LONG ? cols : 1); base += 8 * TPR * NC) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int e = base + 8 * (t + TPR * c);
-      v[c] = v4i{0, 0, 0, 0};
-      if (e < cols) {
-        const v4i* at = reinterpret_cast<const v4i*>(src + e);
-        v[c] = LONG ? *at : __builtin_nontemporal_load(at);
+      for (int c = 0; c < NC; ++c) {
+        const int e = base + 8 * (t + TPR * c);
+        v[c] = v4i{0, 0, 0, 0};
+        if (e < cols) {
+          const v4i* at = reinterpret_cast<const v4i*>(src + e);
+          v[c] = LONG ? *at : __builtin_nontemporal_load(at);
+        }
       }
+#pragma unroll
+      for (int c = 0; c < NC; ++c) m = max_magnitude(m, v[c]);
     }
+    m = max(m & 0xffffu, m >> 16);
 #pragma unroll
-    for (int c = 0; c < NC; ++c) m = max_magnitude(m, v[c]);
-  }
-  m = max(m & 0xffffu, m >> 16);
+    for (int d = 1; d < 64; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
+    if constexpr (TPR > 64) {
+      if ((threadIdx.x & 63) == 0) peak[turn][threadIdx.x >> 6] = m;
+      __syncthreads();
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
-  if constexpr (TPR > 64) {
-    if ((threadIdx.x & 63) == 0) peak[threadIdx.x >> 6] = m;
-    __syncthreads();
+      for (int w = 0; w < kThreads / 64; ++w) m = max(m, peak[turn][w]);
+      turn ^= 1;  // the next row's go elsewhere: one barrier a row
+    }
+    bool finite;
+    const RowScale r = row_scale<F16>(m, finite);
+    if (t == 0) {
+      p.scales[row] = r.s;
+      if (!finite) dev_status_or(p.status, kDevNonFinite);
+    }
+    int8_t* dst = p.data + row * p.cols;
+    for (int base = 0; base < (LONG ? cols : 1); base += 8 * TPR * NC) {
 #pragma unroll
-    for (int w = 0; w < kThreads / 64; ++w) m = max(m, peak[w]);
-  }
-  bool finite;
-  const RowScale r = row_scale<F16>(m, finite);
-  if (t == 0) {
-    p.scales[row] = r.s;
-    if (!finite) dev_status_or(p.status, kDevNonFinite);
-  }
-  int8_t* dst = p.data + row * p.cols;
-  for (int base = 0; base < (LONG ? cols : 1); base += 8 * TPR * NC) {
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int e = base + 8 * (t + TPR * c);
-      if constexpr (LONG) {
-        if (e < cols) v[c] = *reinterpret_cast<const v4i*>(src + e);
+      for (int c = 0; c < NC; ++c) {
+        const int e = base + 8 * (t + TPR * c);
+        if constexpr (LONG) {
+          if (e < cols) v[c] = *reinterpret_cast<const v4i*>(src + e);
+        }
+        const v2i q = quantize8<F16>(v[c], r, finite);
+        if (e < cols) *reinterpret_cast<v2i*>(dst + e) = q;
       }
-      const v2i q = quantize8<F16>(v[c], r, finite);
-      if (e < cols) *reinterpret_cast<v2i*>(dst + e) = q;
     }
   }
 }
@@ -89,8 +92,10 @@ __global__ __launch_bounds__(kThreads) void quantize_int8_kernel(Args p) {
 template <bool F16, int TPR, int NC, bool LONG>
 hipError_t launch(const Args& p, hipStream_t stream) {
   constexpr int kRows = kThreads / TPR;
-  const int64_t blocks = (p.rows_cap + kRows - 1) / kRows;
-  hipLaunchKernelGGL((quantize_int8_kernel<F16, TPR, NC, LONG>), dim3((unsigned)blocks),
+  // a launch has fewer than 2^32 threads
+  const int64_t blocks = (p.rows_cap + kRows - 1) / kRows, most = (int64_t)1 << 23;
+  hipLaunchKernelGGL((quantize_int8_kernel<F16, TPR, NC, LONG>),
+                     dim3((unsigned)(blocks < most ? blocks : most)),
                      dim3(kThreads), 0, stream, p);
   return hipGetLastError();
 }

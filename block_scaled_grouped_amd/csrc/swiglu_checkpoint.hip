@@ -102,13 +102,14 @@ struct Walk {
   int64_t row, last;
   int c, unit;             // chunk of the row, and of the workgroup's rows
   int chunks, waves, dr, dc;
-  __device__ __forceinline__ void init(const Rows& rows, int n, int rows_each) {
+  // block: the workgroup's rows are rows_each of them, from block * rows_each on.
+  __device__ __forceinline__ void init(const Rows& rows, int n, int rows_each, int64_t block) {
     unit = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     waves = (int)(blockDim.x >> 6);
     chunks = n;
     dr = waves / n;
     dc = waves - dr * n;
-    const int64_t first = rows.first + (int64_t)blockIdx.x * rows_each;
+    const int64_t first = rows.first + block * rows_each;
     last = first + rows_each < rows.last ? first + rows_each : rows.last;
     const int r = unit / n;
     row = first + r;
@@ -161,7 +162,6 @@ __global__ __launch_bounds__(kMaxThreads) void swiglu_kernel(Fwd p) {
   const int lane = threadIdx.x & 63;
   const int f = (int)p.f;
   Walk at;
-  at.init(rows, (f + kChunk - 1) / kChunk, p.rows_each);
   v4i next_g, next_u;
   float next_w = 1.0f;
   const auto load = [&]() {
@@ -175,39 +175,43 @@ __global__ __launch_bounds__(kMaxThreads) void swiglu_kernel(Fwd p) {
     }
     if (p.w != nullptr) next_w = p.w[at.row];
   };
-  load();
-  while (at.here()) {
-    const v4i g = next_g, u = next_u;
-    const float w = next_w;
-    const int64_t row = at.row;
-    const int col = at.c * kChunk + 8 * lane;
-    const bool here = col < f;
-    at.next();
+  for (int64_t block = blockIdx.x; block * p.rows_each < rows.last - rows.first;
+       block += gridDim.x) {
+    at.init(rows, (f + kChunk - 1) / kChunk, p.rows_each, block);
     load();
-    if constexpr (KEEP) {
-      const uint32_t ag = block_amax(g), au = block_amax(u);
-      const uint32_t bg = scale_byte<F16>(ag), bu = scale_byte<F16>(au);
-      const v2i qg = codes8<F16>(g, bg), qu = codes8<F16>(u, bu);
-      if (here) {
-        uint8_t* dst = p.data + row * 2 * p.f + col;
-        store<true>(dst, qg);  // not read before the backward pass
-        store<true>(dst + f, qu);
-        if ((lane & 3) == 0) {
-          uint8_t* sc = p.scales + row * (p.f / 16) + col / 32;
-          sc[0] = (uint8_t)bg;
-          sc[f / 32] = (uint8_t)bu;
+    while (at.here()) {
+      const v4i g = next_g, u = next_u;
+      const float w = next_w;
+      const int64_t row = at.row;
+      const int col = at.c * kChunk + 8 * lane;
+      const bool here = col < f;
+      at.next();
+      load();
+      if constexpr (KEEP) {
+        const uint32_t ag = block_amax(g), au = block_amax(u);
+        const uint32_t bg = scale_byte<F16>(ag), bu = scale_byte<F16>(au);
+        const v2i qg = codes8<F16>(g, bg), qu = codes8<F16>(u, bu);
+        if (here) {
+          uint8_t* dst = p.data + row * 2 * p.f + col;
+          store<true>(dst, qg);  // not read before the backward pass
+          store<true>(dst + f, qu);
+          if ((lane & 3) == 0) {
+            uint8_t* sc = p.scales + row * (p.f / 16) + col / 32;
+            sc[0] = (uint8_t)bg;
+            sc[f / 32] = (uint8_t)bu;
+          }
         }
+        if (__any(max(ag, au) >= (F16 ? 0x7c00u : 0x7f80u)) && lane == 0)
+          dev_status_or(p.status, kDevNonFinite);
       }
-      if (__any(max(ag, au) >= (F16 ? 0x7c00u : 0x7f80u)) && lane == 0)
-        dev_status_or(p.status, kDevNonFinite);
-    }
-    float y[8];
+      float y[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = elem<F16>(g, e);
-      y[e] = w * (x * sigmoid(x)) * elem<F16>(u, e);
+      for (int e = 0; e < 8; ++e) {
+        const float x = elem<F16>(g, e);
+        y[e] = w * (x * sigmoid(x)) * elem<F16>(u, e);
+      }
+      if (here) store8<F16, STREAM>(p.y + row * p.ldy + col, y);
     }
-    if (here) store8<F16, STREAM>(p.y + row * p.ldy + col, y);
   }
 }
 
@@ -253,7 +257,6 @@ __global__ __launch_bounds__(kMaxThreads) void swiglu_backward_kernel(Bwd p) {
   const int lane = threadIdx.x & 63;
   const int f = (int)p.f;
   Walk at;
-  at.init(rows, (f + kChunk - 1) / kChunk, p.rows_each);
   struct Kept {
     v2i g, u;
     v4i dy;
@@ -276,46 +279,51 @@ __global__ __launch_bounds__(kMaxThreads) void swiglu_backward_kernel(Bwd p) {
     }
     if (p.w != nullptr) next.w = p.w[at.row];
   };
-  load();
-  while (at.here()) {
-    const Kept k = next;
-    const int64_t row = at.row;
-    const int col = at.c * kChunk + 8 * lane, unit = at.unit;
-    at.next();
+  for (int64_t block = blockIdx.x; block * p.rows_each < rows.last - rows.first;
+       block += gridDim.x) {
+    at.init(rows, (f + kChunk - 1) / kChunk, p.rows_each, block);
     load();
-    float dw = 0.0f;
-    if (col < f) {
-      float g[8], u[8], dg[8], du[8], y[8];
-      decode8(k.g, k.bg, g);
-      decode8(k.u, k.bu, u);
+    while (at.here()) {
+      const Kept k = next;
+      const int64_t row = at.row;
+      const int col = at.c * kChunk + 8 * lane, unit = at.unit;
+      at.next();
+      load();
+      float dw = 0.0f;
+      if (col < f) {
+        float g[8], u[8], dg[8], du[8], y[8];
+        decode8(k.g, k.bg, g);
+        decode8(k.u, k.bu, u);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float s = sigmoid(g[e]), act = g[e] * s, dy = elem<F16>(k.dy, e);
-        if constexpr (ROWSUM) dw += dy * act * u[e];
-        const float dyw = dy * k.w;
-        du[e] = dyw * act;
-        dg[e] = dyw * u[e] * (s * fmaf(g[e], 1.0f - s, 1.0f));
-        y[e] = k.w * act * u[e];
+        for (int e = 0; e < 8; ++e) {
+          const float s = sigmoid(g[e]), act = g[e] * s, dy = elem<F16>(k.dy, e);
+          if constexpr (ROWSUM) dw += dy * act * u[e];
+          const float dyw = dy * k.w;
+          du[e] = dyw * act;
+          dg[e] = dyw * u[e] * (s * fmaf(g[e], 1.0f - s, 1.0f));
+          y[e] = k.w * act * u[e];
+        }
+        store8<F16, STREAM>(p.dh + row * p.lddh + col, dg);
+        store8<F16, STREAM>(p.dh + row * p.lddh + f + col, du);
+        if (p.y != nullptr) store8<F16, STREAM>(p.y + row * p.ldy + col, y);
       }
-      store8<F16, STREAM>(p.dh + row * p.lddh + col, dg);
-      store8<F16, STREAM>(p.dh + row * p.lddh + f + col, du);
-      if (p.y != nullptr) store8<F16, STREAM>(p.y + row * p.ldy + col, y);
+      if constexpr (ROWSUM) {
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) dw += __shfl_xor(dw, d, 64);
+        if (lane == 0) part[unit] = dw;
+      }
     }
     if constexpr (ROWSUM) {
+      __syncthreads();
+      const int64_t first = rows.first + block * p.rows_each;
+      for (int r = (int)(threadIdx.x >> 6); first + r < at.last; r += at.waves) {
+        float dw = 0.0f;
+        for (int c = lane; c < at.chunks; c += 64) dw += part[r * at.chunks + c];
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) dw += __shfl_xor(dw, d, 64);
-      if (lane == 0) part[unit] = dw;
-    }
-  }
-  if constexpr (ROWSUM) {
-    __syncthreads();
-    const int64_t first = rows.first + (int64_t)blockIdx.x * p.rows_each;
-    for (int r = (int)(threadIdx.x >> 6); first + r < at.last; r += at.waves) {
-      float dw = 0.0f;
-      for (int c = lane; c < at.chunks; c += 64) dw += part[r * at.chunks + c];
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) dw += __shfl_xor(dw, d, 64);
-      if (lane == 0) p.dw[first + r] = dw;
+        for (int d = 1; d < 64; d <<= 1) dw += __shfl_xor(dw, d, 64);
+        if (lane == 0) p.dw[first + r] = dw;
+      }
+      __syncthreads();  // the parts are read before the next rows'
     }
   }
 }
@@ -341,9 +349,8 @@ Shape shape_of(int64_t rows_cap, int64_t f) {
   if (each < 1) each = 1;
   if (each * chunks > kMaxUnits) each = kMaxUnits / chunks;
   // a launch has fewer than 2^32 threads
-  const int64_t least = (rows_cap + ((int64_t)1 << 20) - 1) >> 20;
-  if (each < least) each = least;
-  return {(int)each, (unsigned)((rows_cap + each - 1) / each), (unsigned)(64 * waves)};
+  const int64_t groups = (rows_cap + each - 1) / each, most = (int64_t)1 << 20;
+  return {(int)each, (unsigned)(groups < most ? groups : most), (unsigned)(64 * waves)};
 }
 
 constexpr int64_t kCacheBytes = (int64_t)256 << 20;  // of the last level

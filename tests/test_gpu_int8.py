@@ -295,3 +295,19 @@ def test_binding_refuses_what_does_not_fit():
         bsg.grouped_quantize_int8(x.t())
     with pytest.raises(ValueError, match="data"):
         bsg.grouped_quantize_int8(x, data=torch.zeros((8, 64), dtype=torch.int8, device=device()))
+
+
+def test_many_rows():
+    """More rows than one launch has workgroups for (2^23), and a capacity far beyond the live ones."""
+    rows = (1 << 23) + 5
+    for cols, lo in ((16, 0), (2064, rows - 40)):
+        x = torch.zeros((rows, cols), dtype=torch.bfloat16, device=device())
+        x[-40:] = torch.randn((40, cols), device=device()).to(torch.bfloat16)
+        x[:, 3] = 2.0
+        off = torch.tensor([lo, rows], device=device())
+        data, scales = bsg.grouped_quantize_int8(x, off)
+        _check_quantized(x[-40:], (data[-40:], scales[-40:]))
+        if lo == 0:
+            assert bool((scales[:-40] == torch.tensor(2.0) / torch.tensor(127.0)).all())
+            assert bool((data[:-40, 3] == 127).all()) and int(data[:-40].long().sum()) == 127 * (rows - 40)
+        del x, data, scales

@@ -301,3 +301,23 @@ def test_binding_refuses_what_does_not_fit():
     with pytest.raises(ValueError, match="d_h"):
         bsg.grouped_swiglu_checkpoint_mxfp8_backward(data, scales, y, off, d_h=y)
     assert np.prod(scales.shape) == 8 * 4
+
+
+def test_many_rows():
+    """More rows than one launch has workgroups for: workgroups take several blocks of rows."""
+    rows, f = (1 << 24) + 100, 32
+    h = torch.zeros((rows, 2 * f), dtype=torch.bfloat16, device=device())
+    h[:, 1], h[:, f + 1] = 2.0, 4.0
+    h[-9:] = _h(9, f, torch.bfloat16, 5).to(device())
+    w = torch.full((rows,), 0.5, device=device())
+    off = torch.tensor([0, rows], device=device())
+    y, data, scales = bsg.grouped_swiglu_checkpoint_mxfp8(h, off, row_weights=w)
+    one = float((0.5 * 2 * torch.sigmoid(torch.tensor(2.0)) * 4).to(torch.bfloat16))
+    assert bool((y[:-9, 1] == one).all()) and bool((y[:-9, 2:] == 0).all())
+    dy = torch.ones((rows, f), dtype=torch.bfloat16, device=device())
+    dh, dw, _ = bsg.grouped_swiglu_checkpoint_mxfp8_backward(data, scales, dy, off, row_weights=w)
+    r = _reference_backward(data[-9:], scales[-9:], dy[-9:], w[-9:], f)
+    mag = (r["d"] * r["g"] * r["s"] * r["u"]).abs()
+    assert bool(((dw[-9:].cpu().to(F64) - r["dw"]).abs() <= ((r["g"].abs() + 31) * STEP * mag).sum(1) + 1e-30).all())
+    assert bool((dw[:-9] == dw[0]).all()) and abs(float(dw[0]) - float(8 * torch.sigmoid(torch.tensor(2.0)))) < 1e-5
+    assert bool((dh[:-9] == dh[0]).all())
