@@ -246,11 +246,6 @@ def _i64():
     return torch.int64
 
 
-def _i8():
-    import torch
-    return torch.int8
-
-
 def _f32():
     import torch
     return torch.float32
@@ -1082,13 +1077,32 @@ def _maybe(t, name, nbytes, dtype, index):
     return None if t is None else _dense(t, name, nbytes, dtype, index)
 
 
+def _rows(t, name, dtype, index):
+    """(row stride, rows, columns) of a 2-D tensor on device `index` whose rows are contiguous."""
+    if t.dtype is dtype and t.get_device() == index and t.is_contiguous() and t.dim() == 2:
+        rows, cols = t.shape
+        return cols or 1, rows, cols
+    ld, _ = _strided(t, name, 2, dtype, index)
+    return ld, t.shape[0], t.shape[1]
+
+
 def _output(t, rows, cols, dtype, index, name="out"):
     """(tensor [rows, cols], row stride): a new one, or the given one after its checks."""
     if t is None:
         return _maker(index, dtype)(rows, cols), cols
-    if tuple(t.shape) != (rows, cols):
+    ld, r, c = _rows(t, name, dtype, index)
+    if r != rows or c != cols:
         raise ValueError("%s is %s; the call writes %s" % (name, tuple(t.shape), (rows, cols)))
-    return t, _strided(t, name, 2, dtype, index)[0]
+    return t, ld
+
+
+def _buffer(t, rows, cols, dtype, index, name):
+    """(tensor, address) of a dense output [rows, cols] or, without cols, [rows]."""
+    if t is None:
+        make = _maker(index, dtype)
+        t = make(rows) if cols is None else make(rows, cols)
+        return t, t.data_ptr()
+    return t, _dense(t, name, rows * (cols or 1) * t.element_size(), dtype, index)
 
 
 def _status(t, index):
@@ -1098,15 +1112,18 @@ def _status(t, index):
 def _router_args(logits, mask, index):
     """(in_dtype, row stride, tokens, experts, the mask's address)"""
     import torch
-    codes = {torch.bfloat16: BSG_IN_BF16, torch.float16: BSG_IN_F16, torch.float32: BSG_IN_F32}
-    if logits.dtype not in codes:
-        raise ValueError("logits must be bfloat16, float16 or float32, not %s" % _dtype_name(logits.dtype))
-    ld, _ = _strided(logits, "logits", 2, logits.dtype, index)
-    tokens, experts = logits.shape
-    if mask is not None and mask.dtype not in (torch.bool, torch.uint8):
-        raise ValueError("mask must be bool or uint8, not %s" % _dtype_name(mask.dtype))
-    m = None if mask is None else _dense(mask, "mask", tokens, mask.dtype, index)
-    return codes[logits.dtype], ld, tokens, experts, m
+    dtype = logits.dtype
+    code = (BSG_IN_F32 if dtype is torch.float32 else BSG_IN_BF16 if dtype is torch.bfloat16
+            else BSG_IN_F16 if dtype is torch.float16 else None)
+    if code is None:
+        raise ValueError("logits must be bfloat16, float16 or float32, not %s" % _dtype_name(dtype))
+    ld, tokens, experts = _rows(logits, "logits", dtype, index)
+    m = None
+    if mask is not None:
+        if mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("mask must be bool or uint8, not %s" % _dtype_name(mask.dtype))
+        m = _dense(mask, "mask", tokens, mask.dtype, index)
+    return code, ld, tokens, experts, m
 
 
 def moe_router_topk_workspace(tokens, experts, device=None):
@@ -1137,13 +1154,15 @@ def moe_router_topk(logits, top_k, mask=None, normalize=True, workspace=None, st
     if workspace is None:
         workspace = moe_router_topk_workspace(tokens, max(E, 1), logits.device)
     ints, floats = _maker(dev, torch.int32), _maker(dev, torch.float32)
-    out = {"experts": ints(tokens, top_k), "weights": floats(tokens, top_k), "counts": ints(E),
-           "prob_sums": floats(E), "live": ints(1), "loss": floats(1)}
+    experts, weights, counts = ints(tokens, top_k), floats(tokens, top_k), ints(E)
+    prob_sums, live, loss = floats(E), ints(1), floats(1)
     _launch(lib.moe_router_topk, dev, code, logits.data_ptr(), ld, tokens, E, top_k, m,
-            1 if normalize else 0, *(t.data_ptr() for t in out.values()),
+            1 if normalize else 0, experts.data_ptr(), weights.data_ptr(), counts.data_ptr(),
+            prob_sums.data_ptr(), live.data_ptr(), loss.data_ptr(),
             _dense(workspace, "workspace", 0, workspace.dtype, dev), workspace.nbytes,
             _status(status, dev))
-    return out
+    return {"experts": experts, "weights": weights, "counts": counts, "prob_sums": prob_sums,
+            "live": live, "loss": loss}
 
 
 def moe_router_topk_backward(logits, experts, counts, live, d_weights=None, d_loss=None, mask=None,
@@ -1173,9 +1192,9 @@ def moe_router_topk_backward(logits, experts, counts, live, d_weights=None, d_lo
 
 def _in_16bit(t, name):
     import torch
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return BSG_IN_BF16
-    if t.dtype == torch.float16:
+    if t.dtype is torch.float16:
         return BSG_IN_F16
     raise ValueError("%s must be bfloat16 or float16, not %s" % (name, _dtype_name(t.dtype)))
 
@@ -1187,51 +1206,42 @@ def grouped_quantize_int8(x, offsets=None, data=None, scales=None, status=None):
     import torch
     lib = load_library()
     code, dev = _in_16bit(x, "x"), _device_index(x, "x")
-    ld, _ = _strided(x, "x", 2, x.dtype, dev)
-    rows, cols = x.shape
-    if data is None:
-        data = _maker(dev, torch.int8)(rows, cols)
-    if scales is None:
-        scales = _maker(dev, torch.float32)(rows)
-    args = (_maybe(offsets, "offsets", 16, torch.int64, dev),
-            _dense(data, "data", rows * cols, torch.int8, dev),
-            _dense(scales, "scales", 4 * rows, torch.float32, dev), _status(status, dev))
+    ld, rows, cols = _rows(x, "x", x.dtype, dev)
+    data, dptr = _buffer(data, rows, cols, torch.int8, dev, "data")
+    scales, sptr = _buffer(scales, rows, None, torch.float32, dev, "scales")
+    off, G = None, 0
+    if offsets is not None:
+        off, G = _dense(offsets, "offsets", 16, torch.int64, dev), offsets.numel() - 1
+    st = _status(status, dev)
     if rows:
-        _launch(lib.grouped_quantize_int8, dev, code, x.data_ptr(), ld, rows, cols,
-                0 if offsets is None else offsets.numel() - 1, *args)
+        _launch(lib.grouped_quantize_int8, dev, code, x.data_ptr(), ld, rows, cols, G, off, dptr, sptr, st)
     return data, scales
 
 
-_out_type_of = {}
-
-
-def _out_types():
-    if not _out_type_of:
-        import torch
-        _out_type_of.update({BSG_OUT_BF16: torch.bfloat16, BSG_OUT_F16: torch.float16,
-                             BSG_OUT_F32: torch.float32})
-    return _out_type_of
-
-
-def _int8_product(rows, k, w, w_scales, offsets, out, out_dtype, default, dev):
-    """Checked arguments that the int8 products share: (out, G, arguments from b to out_dtype)."""
-    types = _out_types()
-    ldw, stride_w = _strided(w, "w", 3, _i8(), dev)
+def _int8_weights(w, w_scales, offsets, k, index):
+    """(groups, n, row stride, group stride, addresses of the scales and offsets) of an int8
+    product's checked weights."""
+    import torch
+    ldw, stride_w = _strided(w, "w", 3, torch.int8, index)
     G, n, wk = w.shape
     if offsets.numel() - 1 != G or wk != k:
         raise ValueError("w is %s; %d groups contracting %d are needed" % (
             tuple(w.shape), offsets.numel() - 1, k))
+    return (G, n, ldw, stride_w, _dense(w_scales, "w_scales", 4 * G * n, torch.float32, index),
+            _dense(offsets, "offsets", 16, torch.int64, index))
+
+
+def _int8_output(out, rows, n, out_dtype, default, index):
+    """(out, row stride, out_dtype): out_dtype None is that of `out` or, without one, the default."""
+    import torch
+    codes = {torch.bfloat16: BSG_OUT_BF16, torch.float16: BSG_OUT_F16, torch.float32: BSG_OUT_F32}
     if out_dtype is None:
-        out_dtype = default if out is None else next(
-            (c for c, d in types.items() if d == out.dtype), None)
-    odt = types.get(out_dtype)
+        out_dtype = default if out is None else codes.get(out.dtype)
+    odt = (torch.bfloat16 if out_dtype == BSG_OUT_BF16 else torch.float16 if out_dtype == BSG_OUT_F16
+           else torch.float32 if out_dtype == BSG_OUT_F32 else None)
     if odt is None:
         raise ValueError("out_dtype %r is not BSG_OUT_BF16, BSG_OUT_F16 or BSG_OUT_F32" % (out_dtype,))
-    out, ldo = _output(out, rows, n, odt, dev)
-    return out, G, (w.data_ptr(), ldw, stride_w,
-                    _dense(w_scales, "w_scales", 4 * G * n, _f32(), dev),
-                    _dense(offsets, "offsets", 16, _i64(), dev), rows, n, k, out.data_ptr(), ldo,
-                    out_dtype)
+    return _output(out, rows, n, odt, index) + (out_dtype,)
 
 
 def grouped_gemm_int8(a, a_scales, w, w_scales, offsets, out=None, out_dtype=None, workspace=None,
@@ -1243,15 +1253,17 @@ def grouped_gemm_int8(a, a_scales, w, w_scales, offsets, out=None, out_dtype=Non
     import torch
     lib = load_library()
     dev = _device_index(a, "a")
-    lda, _ = _strided(a, "a", 2, torch.int8, dev)
-    rows, k = a.shape
-    out, G, args = _int8_product(rows, k, w, w_scales, offsets, out, out_dtype, BSG_OUT_BF16, dev)
+    lda, rows, k = _rows(a, "a", torch.int8, dev)
+    G, n, ldw, stride_w, sptr, off = _int8_weights(w, w_scales, offsets, k, dev)
+    out, ldo, od = _int8_output(out, rows, n, out_dtype, BSG_OUT_BF16, dev)
     scales = _dense(a_scales, "a_scales", 4 * rows, torch.float32, dev)
-    ws = (None, 0) if workspace is None else (
-        _dense(workspace, "workspace", 0, workspace.dtype, dev), workspace.nbytes)
+    ws, nbytes = None, 0
+    if workspace is not None:
+        ws, nbytes = _dense(workspace, "workspace", 0, workspace.dtype, dev), workspace.nbytes
+    st = _status(status, dev)
     if rows:
-        _launch(lib.grouped_gemm_int8, dev, G, a.data_ptr(), lda, scales, *args, *ws,
-                _status(status, dev))
+        _launch(lib.grouped_gemm_int8, dev, G, a.data_ptr(), lda, scales, w.data_ptr(), ldw, stride_w,
+                sptr, off, rows, n, k, out.data_ptr(), ldo, od, ws, nbytes, st)
     return out
 
 
@@ -1282,16 +1294,16 @@ def grouped_gemm_int8_dynamic(x, w, w_scales, offsets, out=None, out_dtype=None,
     (some 67 MB and the tokens' integers a call)."""
     lib = load_library()
     code, dev = _in_16bit(x, "x"), _device_index(x, "x")
-    ldx, _ = _strided(x, "x", 2, x.dtype, dev)
-    rows, k = x.shape
-    out, G, args = _int8_product(rows, k, w, w_scales, offsets, out, out_dtype,
-                                 BSG_OUT_F16 if code == BSG_IN_F16 else BSG_OUT_BF16, dev)
+    ldx, rows, k = _rows(x, "x", x.dtype, dev)
+    G, n, ldw, stride_w, sptr, off = _int8_weights(w, w_scales, offsets, k, dev)
+    out, ldo, od = _int8_output(out, rows, n, out_dtype,
+                                BSG_OUT_F16 if code == BSG_IN_F16 else BSG_OUT_BF16, dev)
     if workspace is None:
         workspace = grouped_gemm_int8_dynamic_workspace(rows, k, x.device)
-    ws = _dense(workspace, "workspace", 0, workspace.dtype, dev)
+    ws, st = _dense(workspace, "workspace", 0, workspace.dtype, dev), _status(status, dev)
     if rows:
-        _launch(lib.grouped_gemm_int8_dynamic, dev, code, G, x.data_ptr(), ldx, *args, ws,
-                workspace.nbytes, _status(status, dev))
+        _launch(lib.grouped_gemm_int8_dynamic, dev, code, G, x.data_ptr(), ldx, w.data_ptr(), ldw,
+                stride_w, sptr, off, rows, n, k, out.data_ptr(), ldo, od, ws, workspace.nbytes, st)
     return out
 
 
@@ -1304,27 +1316,22 @@ def grouped_swiglu_checkpoint_mxfp8(h, offsets, row_weights=None, out=None, data
     import torch
     lib = load_library()
     code, dev = _in_16bit(h, "h"), _device_index(h, "h")
-    ldh, _ = _strided(h, "h", 2, h.dtype, dev)
-    rows, f2 = h.shape
+    ldh, rows, f2 = _rows(h, "h", h.dtype, dev)
     f = f2 // 2
     if f2 % 64 != 0 or f2 == 0:
         raise ValueError("h has %d columns, not two times a multiple of 32" % f2)
     out, ldo = _output(out, rows, f, h.dtype, dev)
-    kept = (None, None)
+    dptr = sptr = None
     if keep:
-        if data is None:
-            data = _maker(dev, torch.uint8)(rows, f2)
-        if scales is None:
-            scales = _maker(dev, torch.uint8)(rows, f // 16)
-        kept = (_dense(data, "data", rows * f2, torch.uint8, dev),
-                _dense(scales, "scales", rows * (f // 16), torch.uint8, dev))
+        data, dptr = _buffer(data, rows, f2, torch.uint8, dev, "data")
+        scales, sptr = _buffer(scales, rows, f // 16, torch.uint8, dev, "scales")
     else:
         data = scales = None
     w = _maybe(row_weights, "row_weights", 4 * rows, torch.float32, dev)
-    off = _dense(offsets, "offsets", 16, torch.int64, dev)
+    off, st = _dense(offsets, "offsets", 16, torch.int64, dev), _status(status, dev)
     if rows:
         _launch(lib.grouped_swiglu_checkpoint_mxfp8, dev, code, h.data_ptr(), ldh, w,
-                offsets.numel() - 1, off, rows, f, out.data_ptr(), ldo, *kept, _status(status, dev))
+                offsets.numel() - 1, off, rows, f, out.data_ptr(), ldo, dptr, sptr, st)
     return out, data, scales
 
 
@@ -1338,8 +1345,7 @@ def grouped_swiglu_checkpoint_mxfp8_backward(data, scales, d_out, offsets, row_w
     import torch
     lib = load_library()
     code, dev = _in_16bit(d_out, "d_out"), _device_index(d_out, "d_out")
-    ldd, _ = _strided(d_out, "d_out", 2, d_out.dtype, dev)
-    rows, f = d_out.shape
+    ldd, rows, f = _rows(d_out, "d_out", d_out.dtype, dev)
     if f % 32 != 0 or f == 0:
         raise ValueError("d_out has %d columns, not a multiple of 32" % f)
     d_h, ldh = _output(d_h, rows, 2 * f, d_out.dtype, dev, "d_h")
@@ -1347,16 +1353,16 @@ def grouped_swiglu_checkpoint_mxfp8_backward(data, scales, d_out, offsets, row_w
     if recompute or out is not None:
         out, ldo = _output(out, rows, f, d_out.dtype, dev)
         optr = out.data_ptr()
+    w = wptr = None
     if row_weights is None:
         d_row_weights = None
-    elif d_row_weights is None:
-        d_row_weights = _maker(dev, torch.float32)(rows)
-    args = (_dense(data, "data", rows * 2 * f, torch.uint8, dev),
-            _dense(scales, "scales", rows * (f // 16), torch.uint8, dev),
-            _maybe(row_weights, "row_weights", 4 * rows, torch.float32, dev), d_out.data_ptr(), ldd,
-            offsets.numel() - 1, _dense(offsets, "offsets", 16, torch.int64, dev), rows, f,
-            d_h.data_ptr(), ldh, optr, ldo,
-            _maybe(d_row_weights, "d_row_weights", 4 * rows, torch.float32, dev), _status(status, dev))
+    else:
+        w = _dense(row_weights, "row_weights", 4 * rows, torch.float32, dev)
+        d_row_weights, wptr = _buffer(d_row_weights, rows, None, torch.float32, dev, "d_row_weights")
+    dptr = _dense(data, "data", rows * 2 * f, torch.uint8, dev)
+    sptr = _dense(scales, "scales", rows * (f // 16), torch.uint8, dev)
+    off, st = _dense(offsets, "offsets", 16, torch.int64, dev), _status(status, dev)
     if rows:
-        _launch(lib.grouped_swiglu_checkpoint_mxfp8_backward, dev, code, *args)
+        _launch(lib.grouped_swiglu_checkpoint_mxfp8_backward, dev, code, dptr, sptr, w, d_out.data_ptr(),
+                ldd, offsets.numel() - 1, off, rows, f, d_h.data_ptr(), ldh, optr, ldo, wptr, st)
     return d_h, d_row_weights, out
