@@ -458,33 +458,41 @@ __global__ __launch_bounds__(kFwdThreads) void router_kernel(Fwd p) {
 
 // Adds up the workgroups' sums: 16 experts a workgroup, 16 threads an expert.  The last
 // workgroup to end adds up the loss.
-constexpr int kFinishThreads = 256;
+constexpr int kFinishThreads = 1024, kFinishParts = kFinishThreads / 16,
+              kFinishWaves = kFinishThreads / 64;
 
 __global__ __launch_bounds__(kFinishThreads) void router_finish_kernel(Fwd p, int parts) {
-  __shared__ double sums[16][17];
-  __shared__ int32_t counts[16][17];
+  __shared__ double sums[kFinishWaves][16];
+  __shared__ int32_t counts[kFinishWaves][16];
   __shared__ bool last;
-  __shared__ double waves[kFinishThreads / 64];
-  __shared__ int32_t lives[kFinishThreads / 64];
+  __shared__ double waves[kFinishWaves];
+  __shared__ int32_t lives[kFinishWaves];
   const int tid = threadIdx.x, e = tid & 15, i = tid >> 4;
   const int expert = (int)blockIdx.x * 16 + e;
   double s = 0.0;
   int32_t c = 0;
   if (expert < p.E) {
-#pragma unroll 8
-    for (int b = i; b < parts; b += 16) {
+#pragma unroll 4
+    for (int b = i; b < parts; b += kFinishParts) {
       const v2i v = p.parts[(int64_t)b * p.E + expert];
       const int bits = v[0];
       s += (double)__int_as_float(bits);
       c += v[1];
     }
   }
-  sums[i][e] = s;
-  counts[i][e] = c;
+#pragma unroll
+  for (int d = 16; d < 64; d <<= 1) {
+    s += __shfl_xor(s, d, 64);
+    c += __shfl_xor(c, d, 64);
+  }
+  if ((tid & 63) < 16) {
+    sums[tid >> 6][e] = s;
+    counts[tid >> 6][e] = c;
+  }
   __syncthreads();
   if (i == 0 && expert < p.E) {
 #pragma unroll
-    for (int j = 1; j < 16; ++j) {
+    for (int j = 1; j < kFinishWaves; ++j) {
       s += sums[j][e];
       c += counts[j][e];
     }
@@ -493,14 +501,14 @@ __global__ __launch_bounds__(kFinishThreads) void router_finish_kernel(Fwd p, in
     __hip_atomic_store(p.products + expert, (double)c * s, __ATOMIC_RELAXED,
                        __HIP_MEMORY_SCOPE_AGENT);
   }
-  __threadfence();
+  // thread 0 releases what its own wave stored, and the products are read past the caches: no
+  // other wave has to write a cache back (a fence of every thread: 5.6 instead of 4.7 us)
   __syncthreads();
   if (tid == 0)
     last = __hip_atomic_fetch_add(p.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
            gridDim.x - 1;
   __syncthreads();
   if (!last) return;
-  __threadfence();
   double all = tid < p.E ? __hip_atomic_load(p.products + tid, __ATOMIC_RELAXED,
                                              __HIP_MEMORY_SCOPE_AGENT)
                          : 0.0;
@@ -515,12 +523,16 @@ __global__ __launch_bounds__(kFinishThreads) void router_finish_kernel(Fwd p, in
   }
   __syncthreads();
   if (tid == 0) {
-    live = lives[0] + lives[1] + lives[2] + lives[3];
+#pragma unroll
+    for (int j = 1; j < kFinishWaves; ++j) {
+      live += lives[j];
+      all += waves[j];
+    }
     *p.live = live;
-    *p.loss = balance_loss(waves[0] + waves[1] + waves[2] + waves[3], p.E, p.k, live);
+    *p.loss = balance_loss(all, p.E, p.k, live);
   }
 }
-static_assert(kMaxExperts <= kFinishThreads, "a thread each");
+static_assert(kMaxExperts <= kFinishThreads && kFwdBlocks <= kFinishThreads, "a thread each");
 
 // ---------------------------------------------------------------- backward
 
