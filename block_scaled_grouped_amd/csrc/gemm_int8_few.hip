@@ -7,8 +7,9 @@
 // they go to the matrix instruction (v_mfma_i32_16x16x64: lane (r, q) = (l % 16, l / 16)
 // holds 16 bytes of column r).  Loaded straight into the registers, 16 neighbouring lanes ask
 // for 16 lines: 64 rows of 41 experts x 2048 x 7168 took 143 us, a tile at a time through the
-// ring 118, and now 107 (5.6 TB/s).  One row x 14336 x 4096 in 16-bit tokens takes 13.7 us
-// from call to call, 21.8 with a launch for the tokens and split 32-row tiles.
+// ring 118, and now 107 (5.6 TB/s).  One row x 14336 x 4096 in 16-bit tokens takes 11.9 us
+// from call to call (58.8 MB at 4.9 TB/s), 15.6 with a launch for the tokens, 20.5 with that
+// and split 32-row tiles.
 //
 // TOKENS: the rows are in 16 bits.  Every workgroup quantizes the rows itself, into LDS, while
 // its first weights are on their way: one launch instead of two, for calls of so few rows

@@ -22,6 +22,13 @@
 // A 16-bit logit has its bits above those eight.  A float32 one may share them with the
 // next in order: where that happens among a token's k + 1 largest the wave does it again,
 // on whole values.
+//
+// What bounds it: the forward pass the vector units (some 550 instructions for a wave's four
+// tokens of 256 experts), the backward pass HBM.  65536 float32 tokens of 256 experts, k 8:
+// forward 28.6 us (67 MB; 3.2 us of them from the first load to the first token), adding up
+// 4.7, backward 28.0 (139 MB at 5.0 TB/s).  4096 bf16 tokens of 64 experts 6.0, 4.6 and 5.9;
+// 64 of 8 3.5 in one launch, where two took 3.5 and 4.6.  Two workgroups a compute unit
+// (forward) are slower: 35.5 us.
 #include <type_traits>
 
 #include "bsg_internal.h"
@@ -35,7 +42,7 @@ constexpr int kMaxExperts = 256;
 constexpr int kFwdThreads = 1024;
 constexpr int kFwdTokens = kFwdThreads / kLanes;
 constexpr int kFwdWaves = kFwdThreads / 64;
-constexpr int kFwdBlocks = 256;      // at most
+constexpr int kFwdBlocks = 256;      // at most: one a compute unit
 constexpr int64_t kOneBlock = 256;   // tokens that one workgroup takes alone
 constexpr int kBwdThreads = 256;
 constexpr int kBwdTokens = kBwdThreads / kLanes;
@@ -110,7 +117,7 @@ typedef v2i v2i_any __attribute__((aligned(2)));
 typedef int int_any __attribute__((aligned(2)));
 #define BSG_GLOBAL __attribute__((address_space(1)))
 
-// A lane's logits; those past the last expert are -inf.  RUNS: the experts are whole runs;
+// A lane's logits; those past the last expert are anything.  RUNS: the experts are whole runs;
 // else they come one by one.
 template <int DT, int EPL, bool RUNS>
 __device__ __forceinline__ void load_row(const char* row, int slot, int E, float (&v)[EPL]) {
@@ -119,8 +126,7 @@ __device__ __forceinline__ void load_row(const char* row, int slot, int E, float
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
       const int e = expert_of<DT, EPL>(slot, j);
-      const float x = load_one<DT>(row, e < E ? e : E - 1);
-      v[j] = e < E ? x : -INFINITY;
+      v[j] = load_one<DT>(row, e < E ? e : E - 1);
     }
     return;
   }
@@ -145,12 +151,20 @@ __device__ __forceinline__ void load_row(const char* row, int slot, int E, float
     }
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-      float x;
-      if constexpr (DT == 2) x = __uint_as_float(w[j]);
-      else x = decode16<DT>((w[j >> 1] >> (16 * (j & 1))) & 0xffffu);
-      out[j] = e0 < E ? x : -INFINITY;
+      if constexpr (DT == 2) out[j] = __uint_as_float(w[j]);
+      else out[j] = decode16<DT>((w[j >> 1] >> (16 * (j & 1))) & 0xffffu);
     }
   }
+}
+
+// -inf for experts that are not there, and all of a token that is not to be routed.  Nothing to
+// do, for the whole wave, where its tokens are routed and the experts fill their lanes.
+template <int DT, int EPL>
+__device__ __forceinline__ void close_absent(float (&v)[EPL], bool routed, int slot, int E) {
+  if (E == kLanes * EPL && __all(routed)) return;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j)
+    v[j] = routed && expert_of<DT, EPL>(slot, j) < E ? v[j] : -INFINITY;
 }
 
 template <int DT, int EPL, bool RUNS>
@@ -191,12 +205,20 @@ __device__ __forceinline__ void store_row(char* row, int slot, int E, const floa
   }
 }
 
-// A logit's bits ordered as unsigned integers, -0 as 0 and a NaN as -inf.  What is below
-// kOpen is not to be chosen.
+// A logit's bits ordered as unsigned integers, -0 as 0; not a NaN's.  What is below kOpen is
+// not to be chosen.
 constexpr uint32_t kOpen = 0x00800000u;  // of the lowest finite number
 __device__ __forceinline__ uint32_t order(float v) {
-  const uint32_t u = __float_as_uint(fmaxf(v + 0.0f, -INFINITY));
+  const uint32_t u = __float_as_uint(v + 0.0f);
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float closed_if_nan(float v) { return fmaxf(v, -INFINITY); }
+
+// The middle one of a >= b and x: where x goes among them, b or what b makes room for.
+__device__ __forceinline__ uint32_t middle(uint32_t a, uint32_t b, uint32_t x) {
+  uint32_t m;
+  asm("v_med3_u32 %0, %1, %2, %3" : "=v"(m) : "v"(a), "v"(b), "v"(x));
+  return m;
 }
 
 template <int N>
@@ -216,15 +238,13 @@ __device__ __forceinline__ uint32_t max_of(const uint32_t (&v)[N]) {
 // they are at once where more than kFewRounds are asked for).
 constexpr int kHeads = 4, kFewRounds = 9, kRoundsAtOnce = 3;
 
-template <int DT, int EPL>
-__device__ __forceinline__ int choose(const float (&v)[EPL], int slot, int E, int k) {
+// key: of the lane's experts.  whole(key) gives them without the index, for float32.
+template <int DT, int EPL, typename F>
+__device__ __forceinline__ int choose(uint32_t (&key)[EPL], int slot, int E, int k, F whole) {
   constexpr int H = EPL < kHeads ? EPL : kHeads;
   // float32: one more than is chosen, which shows whether the last is next to another
   const int rounds = DT == 2 && k < E ? k + 1 : k;
-  uint32_t key[EPL], mine = 0, m = 0;
-#pragma unroll
-  for (int j = 0; j < EPL; ++j)
-    key[j] = (order(v[j]) & ~255u) | (uint32_t)(255 - expert_of<DT, EPL>(slot, j));
+  uint32_t mine = 0, m = 0;
   const auto below = [&](uint32_t top) {  // the largest key below `top`
     uint32_t d[EPL];
 #pragma unroll
@@ -235,9 +255,17 @@ __device__ __forceinline__ int choose(const float (&v)[EPL], int slot, int E, in
   if (!all) {
     uint32_t head[H];
     bool won = false;
-    head[0] = max_of(key);
+    // a key at a time into its place among the largest so far
+    head[0] = key[0];
 #pragma unroll
-    for (int i = 1; i < H; ++i) head[i] = below(head[i - 1]);
+    for (int j = 1; j < EPL; ++j) {
+      const uint32_t x = key[j];
+      if (j < H) head[j % H] = head[j - 1] < x ? head[j - 1] : x;
+#pragma unroll
+      for (int i = H - 1; i > 0; --i)
+        if (i < j) head[i] = middle(head[i - 1], head[i], x);
+      head[0] = head[0] > x ? head[0] : x;
+    }
     for (int r0 = 0; r0 < rounds; r0 += kRoundsAtOnce) {
 #pragma unroll
       for (int r = 0; r < kRoundsAtOnce; ++r) {
@@ -265,8 +293,7 @@ __device__ __forceinline__ int choose(const float (&v)[EPL], int slot, int E, in
     const uint32_t after = dpp<0x101>(mine);  // of lane + 1, which has to be active
     const uint32_t next = slot == k - 1 ? (rounds > k ? m : 0u) : after;
     if (__any(slot < k && next >= kOpen && (next ^ mine) < 256u)) {
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) key[j] = order(v[j]);
+      whole(key);
       chosen = -1;
       for (int r = 0; r < k; ++r) {
         m = max16u(max_of(key));
@@ -377,24 +404,34 @@ __global__ __launch_bounds__(kFwdThreads) void router_kernel(Fwd p) {
   float* mine = rows[tid >> 4];
   const int64_t stride = (int64_t)gridDim.x * kFwdTokens;
   int64_t t = (int64_t)blockIdx.x * kFwdTokens + (tid >> 4);
-  float next[EPL];
+  float v[EPL];
+  bool routed;
   const auto load = [&](int64_t token) {
-    const bool routed = token < p.tokens && (p.mask == nullptr || p.mask[token] != 0);
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) next[j] = -INFINITY;
-    if (routed) load_row<DT, EPL, RUNS>(p.logits + token * p.ld, slot, E, next);
+    routed = token < p.tokens && (p.mask == nullptr || p.mask[token] != 0);
+    if (routed) load_row<DT, EPL, RUNS>(p.logits + token * p.ld, slot, E, v);
   };
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) v[j] = -INFINITY;
   load(t);
   for (int64_t base = (int64_t)blockIdx.x * kFwdTokens; base < p.tokens;
        base += stride, t += stride) {
     // opaque: keeps what every expert's index gives from being held over the loop
     asm volatile("" : "+v"(slot));
-    float v[EPL], ex[EPL];
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) v[j] = next[j];
-    if (base + stride < p.tokens) load(t + stride);
+    float ex[EPL];
+    uint32_t key[EPL];
+    close_absent<DT, EPL>(v, routed, slot, E);
     const Softmax sm = softmax(v, ex);
-    bad |= sm.live && !(sm.sum < INFINITY);
+    const bool here = routed, nonfinite = !(sm.sum < INFINITY);
+    bad |= nonfinite;
+    if (__any(nonfinite)) {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) v[j] = closed_if_nan(v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      key[j] = (order(v[j]) & ~255u) | (uint32_t)(255 - expert_of<DT, EPL>(slot, j));
+    // the next tokens' logits, into the registers that are free now
+    if (base + stride < p.tokens) load(t + stride);
     wave_fence();
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
@@ -403,7 +440,15 @@ __global__ __launch_bounds__(kFwdThreads) void router_kernel(Fwd p) {
     }
     wave_fence();
     live_tokens += sm.live ? 1 : 0;
-    const int e = choose<DT, EPL>(v, slot, E, k);
+    const int e = choose<DT, EPL>(key, slot, E, k, [&](uint32_t (&whole)[EPL]) {
+      float x[EPL];
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) x[j] = -INFINITY;
+      if (here) load_row<DT, EPL, RUNS>(p.logits + t * p.ld, slot, E, x);
+      close_absent<DT, EPL>(x, here, slot, E);
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) whole[j] = order(closed_if_nan(x[j]));
+    });
     float weight = e >= 0 ? mine[e] * sm.inv : 0.0f;
     if (p.normalize) {
       const float all = sum16(weight);
@@ -571,32 +616,32 @@ __global__ __launch_bounds__(kBwdThreads) void router_backward_kernel(Bwd p) {
   }
   const int64_t stride = (int64_t)gridDim.x * kBwdTokens;
   int64_t t = (int64_t)blockIdx.x * kBwdTokens + (tid >> 4);
-  float next[EPL], next_dw = 0.0f;
+  float v[EPL], next_dw = 0.0f;
   int next_e = -1;
+  bool routed;
   const auto load = [&](int64_t token) {
-    const bool routed = token < p.tokens && (p.mask == nullptr || p.mask[token] != 0);
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) next[j] = -INFINITY;
+    routed = token < p.tokens && (p.mask == nullptr || p.mask[token] != 0);
     next_e = -1;
     if (!routed) return;
-    load_row<DT, EPL, RUNS>(p.logits + token * p.ld, slot, E, next);
+    load_row<DT, EPL, RUNS>(p.logits + token * p.ld, slot, E, v);
     if (slot < k && p.d_weights != nullptr) {
       next_e = p.experts[token * k + slot];
       next_dw = p.d_weights[token * k + slot];
     }
   };
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) v[j] = -INFINITY;
   load(t);
   for (int64_t base = (int64_t)blockIdx.x * kBwdTokens; base < p.tokens;
        base += stride, t += stride) {
     // opaque: keeps what every expert's index gives from being held over the loop
     asm volatile("" : "+v"(slot));
-    float v[EPL], prob[EPL];
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) v[j] = next[j];
+    float prob[EPL];
     const int e = next_e >= 0 && next_e < E ? next_e : -1;
     const float dw = e >= 0 ? next_dw : 0.0f;
-    if (base + stride < p.tokens) load(t + stride);
+    close_absent<DT, EPL>(v, routed, slot, E);
     const Softmax sm = softmax(v, prob);
+    if (base + stride < p.tokens) load(t + stride);
 #pragma unroll
     for (int j = 0; j < EPL; ++j) prob[j] *= sm.inv;
     float add = dw;

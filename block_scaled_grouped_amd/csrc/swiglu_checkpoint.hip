@@ -26,8 +26,8 @@ namespace {
 constexpr int kChunk = 512;  // columns of a wave
 constexpr int kMaxThreads = 1024;
 
-// g s(g) and s(g).  The exponential's error is under 2^-16 of an s below 2^-64, which
-// rounding to 16 bits hides, and 2^-22 around 1.
+// s(g).  The exponential's error is under 2^-16 of an s below 2^-64, which
+// rounding to 16 bits hides, and 2^-22 around 1.  An s below 2^-126 (g under -87.3) is 0.
 __device__ __forceinline__ float sigmoid(float g) {
   const float e = __builtin_amdgcn_exp2f(g * -1.44269502162933349609375f);
   return __builtin_amdgcn_rcpf(1.0f + e);

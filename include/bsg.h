@@ -768,9 +768,9 @@ int clip_grad_norm(const void* plan, int64_t num_chunks, float max_norm, const d
  *                j's expert
  * in float32, rounded once; 0 for tokens that are not live.  d_weights or d_loss may be
  * NULL (zeros).  experts is what the forward pass wrote (indexes outside [0, E) are
- * slots without one, whose d_weights are not read); counts and live may hold sums over several calls or
- * ranks: the loss is then that of all their tokens, E / (top_k live^2) * sum_e counts[e]
- * prob_sums[e] with prob_sums added up too.  Not in place.
+ * slots without one, whose d_weights are not read); counts and live may hold sums over
+ * several calls or ranks: the loss is then that of all their tokens, E / (top_k live^2) *
+ * sum_e counts[e] prob_sums[e] with prob_sums added up too.  Not in place.
  * Errors: BSG_ERR_NULL, BSG_ERR_SHAPE, BSG_ERR_UNSUPPORTED (type, normalize),
  * BSG_ERR_ALIGN (elements; workspace), BSG_ERR_WORKSPACE.
  */
@@ -866,7 +866,7 @@ int grouped_gemm_int8_dynamic(int in_dtype, int64_t G, const void* x, int64_t ld
  * The gated activation between an expert's two products, which keeps its input in 8 bits
  * for the backward pass.  With h = [g | u] (the first product's output, f columns each),
  * w the row's weight (row_weights, e.g. the router's, or 1) and s = 1 / (1 + exp(-g)):
- *   out = w g s u                          (float32, rounded once)
+ *   out = w g s u                          (float32, rounded once; an s below 2^-126 is 0)
  *   data, scales: h as grouped_quantize_mxfp8 quantizes rows (E4M3 elements, an E8M0 byte
  *                 for each 32; infinities and NaN saturate, and set BSG_DEV_NONFINITE)
  * and backwards, g and u being the kept values (element times 2^(byte - 127)):
