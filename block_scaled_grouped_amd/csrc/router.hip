@@ -312,6 +312,13 @@ __device__ __forceinline__ int choose(uint32_t (&key)[EPL], int slot, int E, int
   return chosen;
 }
 
+// The largest, of numbers.  A NaN may come out as one (it makes the sum NaN in any case).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float m;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(a), "v"(b), "v"(c));
+  return m;
+}
+
 // A token's softmax: exp(l - max) in ex, what they have to be multiplied by, and whether it is
 // live.  Without an open expert the sum of the exponentials is 0 (max stands for 0 then), with
 // a NaN or +inf it is NaN.
@@ -324,7 +331,9 @@ __device__ __forceinline__ Softmax softmax(const float (&v)[EPL], float (&ex)[EP
   Softmax r;
   float m = v[0];
 #pragma unroll
-  for (int j = 1; j < EPL; ++j) m = fmaxf(m, v[j]);
+  for (int j = 1; j < EPL; j += 2) m = max3(m, v[j], v[j + 1 < EPL ? j + 1 : j]);
+  // a lane move may not follow what it reads by less than two wait states
+  if constexpr (EPL > 1) asm volatile("s_nop 1" : "+v"(m));
   m = max16(m);
   r.max = m > -INFINITY ? m : 0.0f;
   r.sum = 0.0f;
@@ -408,11 +417,10 @@ __global__ __launch_bounds__(kFwdThreads) void router_kernel(Fwd p) {
   bool routed;
   const auto load = [&](int64_t token) {
     routed = token < p.tokens && (p.mask == nullptr || p.mask[token] != 0);
-    if (routed) load_row<DT, EPL, RUNS>(p.logits + token * p.ld, slot, E, v);
+    // one that is not stands for the first, so that the registers are loaded in every lane
+    load_row<DT, EPL, RUNS>(p.logits + (routed ? token * p.ld : 0), slot, E, v);
   };
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) v[j] = -INFINITY;
-  load(t);
+  if (p.tokens > 0) load(t);
   for (int64_t base = (int64_t)blockIdx.x * kFwdTokens; base < p.tokens;
        base += stride, t += stride) {
     // opaque: keeps what every expert's index gives from being held over the loop
@@ -423,15 +431,17 @@ __global__ __launch_bounds__(kFwdThreads) void router_kernel(Fwd p) {
     const Softmax sm = softmax(v, ex);
     const bool here = routed, nonfinite = !(sm.sum < INFINITY);
     bad |= nonfinite;
+    const auto key_of = [&](float x, int j) {
+      return (order(x) & ~255u) | (uint32_t)(255 - expert_of<DT, EPL>(slot, j));
+    };
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) key[j] = key_of(v[j], j);
     if (__any(nonfinite)) {
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) v[j] = closed_if_nan(v[j]);
+      for (int j = 0; j < EPL; ++j) key[j] = key_of(closed_if_nan(v[j]), j);
     }
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      key[j] = (order(v[j]) & ~255u) | (uint32_t)(255 - expert_of<DT, EPL>(slot, j));
     // the next tokens' logits, into the registers that are free now
-    if (base + stride < p.tokens) load(t + stride);
+    load(t + stride);
     wave_fence();
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
@@ -622,15 +632,12 @@ __global__ __launch_bounds__(kBwdThreads) void router_backward_kernel(Bwd p) {
   const auto load = [&](int64_t token) {
     routed = token < p.tokens && (p.mask == nullptr || p.mask[token] != 0);
     next_e = -1;
-    if (!routed) return;
-    load_row<DT, EPL, RUNS>(p.logits + token * p.ld, slot, E, v);
-    if (slot < k && p.d_weights != nullptr) {
+    load_row<DT, EPL, RUNS>(p.logits + (routed ? token * p.ld : 0), slot, E, v);
+    if (routed && slot < k && p.d_weights != nullptr) {
       next_e = p.experts[token * k + slot];
       next_dw = p.d_weights[token * k + slot];
     }
   };
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) v[j] = -INFINITY;
   load(t);
   for (int64_t base = (int64_t)blockIdx.x * kBwdTokens; base < p.tokens;
        base += stride, t += stride) {
@@ -641,7 +648,7 @@ __global__ __launch_bounds__(kBwdThreads) void router_backward_kernel(Bwd p) {
     const float dw = e >= 0 ? next_dw : 0.0f;
     close_absent<DT, EPL>(v, routed, slot, E);
     const Softmax sm = softmax(v, prob);
-    if (base + stride < p.tokens) load(t + stride);
+    load(t + stride);
 #pragma unroll
     for (int j = 0; j < EPL; ++j) prob[j] *= sm.inv;
     float add = dw;
