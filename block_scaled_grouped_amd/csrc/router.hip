@@ -23,12 +23,12 @@
 // next in order: where that happens among a token's k + 1 largest the wave does it again,
 // on whole values.
 //
-// What bounds it: the forward pass the vector units (some 550 instructions for a wave's four
-// tokens of 256 experts), the backward pass HBM.  65536 float32 tokens of 256 experts, k 8:
-// forward 28.6 us (67 MB; 3.2 us of them from the first load to the first token), adding up
-// 4.7, backward 28.0 (139 MB at 5.0 TB/s).  4096 bf16 tokens of 64 experts 6.0, 4.6 and 5.9;
-// 64 of 8 3.5 in one launch, where two took 3.5 and 4.6.  Two workgroups a compute unit
-// (forward) are slower: 35.5 us.
+// What bounds it: the forward pass the vector units (0.7 of their time busy before the last steps;
+// some 480 instructions for a wave's four tokens of 256 experts), the backward pass HBM.  65536
+// float32 tokens of 256 experts, k 8: forward 25.4 us (67 MB; some 3 of them until the first
+// tokens are there), adding up 4.8, backward 27.4 (139 MB at 5.1 TB/s).  16384 bf16 tokens of 64
+// experts 5.9, 4.6 and 5.7; 64 of 8 3.5 in one launch.  Two workgroups a compute unit (forward)
+// are slower: 35 us.
 #include <type_traits>
 
 #include "bsg_internal.h"
@@ -96,18 +96,15 @@ __device__ __forceinline__ float decode16(uint32_t bits) {
   if constexpr (DT == 1) return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
   return __uint_as_float(bits << 16);
 }
-template <int DT>
-__device__ __forceinline__ float load_one(const char* row, int e) {
-  const gchar* at = (const gchar*)(row) + (int64_t)e * kBytes<DT>;
-  if constexpr (DT == 2) return *reinterpret_cast<const __attribute__((address_space(1))) float*>(at);
-  return decode16<DT>(*reinterpret_cast<const __attribute__((address_space(1))) uint16_t*>(at));
-}
-
-// A lane's experts: runs of kRun, a run of the 16 lanes after the other.
-template <int DT, int EPL> constexpr int kRun = EPL < 16 / kBytes<DT> ? EPL : 16 / kBytes<DT>;
-template <int DT, int EPL>
+// A lane's experts: runs of kRun, a run of the 16 lanes after the other.  RUNS: the experts are
+// whole runs of 16 bytes (or what a lane has); else runs of one, which neighbouring lanes load and
+// store next to each other (65536 x 250 float32: forward 36 and backward 49 us with runs of four taken
+// one by one, now 26 and 27).
+template <int DT, int EPL, bool RUNS>
+constexpr int kRun = !RUNS ? 1 : EPL < 16 / kBytes<DT> ? EPL : 16 / kBytes<DT>;
+template <int DT, int EPL, bool RUNS>
 __device__ __forceinline__ int expert_of(int slot, int j) {
-  constexpr int R = kRun<DT, EPL>;
+  constexpr int R = kRun<DT, EPL, RUNS>;
   return R * (slot + kLanes * (j / R)) + j % R;
 }
 
@@ -117,19 +114,10 @@ typedef v2i v2i_any __attribute__((aligned(2)));
 typedef int int_any __attribute__((aligned(2)));
 #define BSG_GLOBAL __attribute__((address_space(1)))
 
-// A lane's logits; those past the last expert are anything.  RUNS: the experts are whole runs;
-// else they come one by one.
+// A lane's logits; those past the last expert are anything.
 template <int DT, int EPL, bool RUNS>
 __device__ __forceinline__ void load_row(const char* row, int slot, int E, float (&v)[EPL]) {
-  constexpr int R = kRun<DT, EPL>, bytes = R * kBytes<DT>;
-  if constexpr (!RUNS) {
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      const int e = expert_of<DT, EPL>(slot, j);
-      v[j] = load_one<DT>(row, e < E ? e : E - 1);
-    }
-    return;
-  }
+  constexpr int R = kRun<DT, EPL, RUNS>, bytes = R * kBytes<DT>;
 #pragma unroll
   for (int c = 0; c < EPL / R; ++c) {
     const int e0 = R * (slot + kLanes * c);
@@ -159,17 +147,17 @@ __device__ __forceinline__ void load_row(const char* row, int slot, int E, float
 
 // -inf for experts that are not there, and all of a token that is not to be routed.  Nothing to
 // do, for the whole wave, where its tokens are routed and the experts fill their lanes.
-template <int DT, int EPL>
+template <int DT, int EPL, bool RUNS>
 __device__ __forceinline__ void close_absent(float (&v)[EPL], bool routed, int slot, int E) {
   if (E == kLanes * EPL && __all(routed)) return;
 #pragma unroll
   for (int j = 0; j < EPL; ++j)
-    v[j] = routed && expert_of<DT, EPL>(slot, j) < E ? v[j] : -INFINITY;
+    v[j] = routed && expert_of<DT, EPL, RUNS>(slot, j) < E ? v[j] : -INFINITY;
 }
 
 template <int DT, int EPL, bool RUNS>
 __device__ __forceinline__ void store_row(char* row, int slot, int E, const float (&v)[EPL]) {
-  constexpr int R = kRun<DT, EPL>, bytes = R * kBytes<DT>, words = (bytes + 3) / 4;
+  constexpr int R = kRun<DT, EPL, RUNS>, bytes = R * kBytes<DT>, words = (bytes + 3) / 4;
 #pragma unroll
   for (int c = 0; c < EPL / R; ++c) {
     const int e0 = R * (slot + kLanes * c);
@@ -181,27 +169,15 @@ __device__ __forceinline__ void store_row(char* row, int slot, int E, const floa
       else w[j] = pack16<DT == 1>(in[2 * j], R > 1 ? in[(2 * j + 1) % R] : 0.0f);
     }
     BSG_GLOBAL char* at = (BSG_GLOBAL char*)(row) + (int64_t)e0 * kBytes<DT>;
-    if constexpr (RUNS) {
-      if (e0 >= E) continue;
-      if constexpr (bytes == 16)
-        *reinterpret_cast<BSG_GLOBAL v4i_any*>(at) = v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
-      else if constexpr (bytes == 8)
-        *reinterpret_cast<BSG_GLOBAL v2i_any*>(at) = v2i{(int)w[0], (int)w[1]};
-      else if constexpr (bytes == 4)
-        *reinterpret_cast<BSG_GLOBAL int_any*>(at) = (int)w[0];
-      else
-        *reinterpret_cast<BSG_GLOBAL uint16_t*>(at) = (uint16_t)w[0];
-    } else {
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        if (e0 + j >= E) continue;
-        if constexpr (DT == 2)
-          *reinterpret_cast<BSG_GLOBAL uint32_t*>(at + 4 * j) = w[j];
-        else
-          *reinterpret_cast<BSG_GLOBAL uint16_t*>(at + 2 * j) =
-              (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-      }
-    }
+    if (e0 >= E) continue;
+    if constexpr (bytes == 16)
+      *reinterpret_cast<BSG_GLOBAL v4i_any*>(at) = v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+    else if constexpr (bytes == 8)
+      *reinterpret_cast<BSG_GLOBAL v2i_any*>(at) = v2i{(int)w[0], (int)w[1]};
+    else if constexpr (bytes == 4)
+      *reinterpret_cast<BSG_GLOBAL int_any*>(at) = (int)w[0];
+    else
+      *reinterpret_cast<BSG_GLOBAL uint16_t*>(at) = (uint16_t)w[0];
   }
 }
 
@@ -239,7 +215,7 @@ __device__ __forceinline__ uint32_t max_of(const uint32_t (&v)[N]) {
 constexpr int kHeads = 4, kFewRounds = 9, kRoundsAtOnce = 3;
 
 // key: of the lane's experts.  whole(key) gives them without the index, for float32.
-template <int DT, int EPL, typename F>
+template <int DT, int EPL, bool RUNS, typename F>
 __device__ __forceinline__ int choose(uint32_t (&key)[EPL], int slot, int E, int k, F whole) {
   constexpr int H = EPL < kHeads ? EPL : kHeads;
   // float32: one more than is chosen, which shows whether the last is next to another
@@ -300,12 +276,12 @@ __device__ __forceinline__ int choose(uint32_t (&key)[EPL], int slot, int E, int
         uint32_t at = 0xffffu;
 #pragma unroll
         for (int j = EPL - 1; j >= 0; --j)
-          at = key[j] == m ? (uint32_t)expert_of<DT, EPL>(slot, j) : at;
+          at = key[j] == m ? (uint32_t)expert_of<DT, EPL, RUNS>(slot, j) : at;
         at = min16u(at);
         if (slot == r && m >= kOpen) chosen = (int)at;
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
-          key[j] = (uint32_t)expert_of<DT, EPL>(slot, j) == at ? 0u : key[j];
+          key[j] = (uint32_t)expert_of<DT, EPL, RUNS>(slot, j) == at ? 0u : key[j];
       }
     }
   }
@@ -427,12 +403,12 @@ __global__ __launch_bounds__(kFwdThreads) void router_kernel(Fwd p) {
     asm volatile("" : "+v"(slot));
     float ex[EPL];
     uint32_t key[EPL];
-    close_absent<DT, EPL>(v, routed, slot, E);
+    close_absent<DT, EPL, RUNS>(v, routed, slot, E);
     const Softmax sm = softmax(v, ex);
     const bool here = routed, nonfinite = !(sm.sum < INFINITY);
     bad |= nonfinite;
     const auto key_of = [&](float x, int j) {
-      return (order(x) & ~255u) | (uint32_t)(255 - expert_of<DT, EPL>(slot, j));
+      return (order(x) & ~255u) | (uint32_t)(255 - expert_of<DT, EPL, RUNS>(slot, j));
     };
 #pragma unroll
     for (int j = 0; j < EPL; ++j) key[j] = key_of(v[j], j);
@@ -446,16 +422,16 @@ __global__ __launch_bounds__(kFwdThreads) void router_kernel(Fwd p) {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
       acc[j] = fmaf(ex[j], sm.inv, acc[j]);
-      mine[expert_of<DT, EPL>(slot, j)] = ex[j];
+      mine[expert_of<DT, EPL, RUNS>(slot, j)] = ex[j];
     }
     wave_fence();
     live_tokens += sm.live ? 1 : 0;
-    const int e = choose<DT, EPL>(key, slot, E, k, [&](uint32_t (&whole)[EPL]) {
+    const int e = choose<DT, EPL, RUNS>(key, slot, E, k, [&](uint32_t (&whole)[EPL]) {
       float x[EPL];
 #pragma unroll
       for (int j = 0; j < EPL; ++j) x[j] = -INFINITY;
       if (here) load_row<DT, EPL, RUNS>(p.logits + t * p.ld, slot, E, x);
-      close_absent<DT, EPL>(x, here, slot, E);
+      close_absent<DT, EPL, RUNS>(x, here, slot, E);
 #pragma unroll
       for (int j = 0; j < EPL; ++j) whole[j] = order(closed_if_nan(x[j]));
     });
@@ -477,7 +453,7 @@ __global__ __launch_bounds__(kFwdThreads) void router_kernel(Fwd p) {
   for (int j = 0; j < EPL; ++j) {
     acc[j] += __shfl_xor(acc[j], 16, 64);
     acc[j] += __shfl_xor(acc[j], 32, 64);
-    if (lane < kLanes) sums[w][expert_of<DT, EPL>(slot, j)] = acc[j];
+    if (lane < kLanes) sums[w][expert_of<DT, EPL, RUNS>(slot, j)] = acc[j];
   }
   live_tokens += __shfl_xor(live_tokens, 16, 64);
   live_tokens += __shfl_xor(live_tokens, 32, 64);
@@ -620,7 +596,7 @@ __global__ __launch_bounds__(kBwdThreads) void router_backward_kernel(Bwd p) {
   const float f = n > 0 ? (float)((double)*p.d_loss * E / ((double)k * n * n)) : 0.0f;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
-    const int e = expert_of<DT, EPL>(slot, j);
+    const int e = expert_of<DT, EPL, RUNS>(slot, j);
     mine[e] = 0.0f;
     b[j] = f != 0.0f && e < E ? f * (float)p.counts[e] : 0.0f;
   }
@@ -646,7 +622,7 @@ __global__ __launch_bounds__(kBwdThreads) void router_backward_kernel(Bwd p) {
     float prob[EPL];
     const int e = next_e >= 0 && next_e < E ? next_e : -1;
     const float dw = e >= 0 ? next_dw : 0.0f;
-    close_absent<DT, EPL>(v, routed, slot, E);
+    close_absent<DT, EPL, RUNS>(v, routed, slot, E);
     const Softmax sm = softmax(v, prob);
     load(t + stride);
 #pragma unroll
@@ -654,7 +630,7 @@ __global__ __launch_bounds__(kBwdThreads) void router_backward_kernel(Bwd p) {
     float add = dw;
     if (p.normalize) {
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) probs[tid >> 4][expert_of<DT, EPL>(slot, j)] = prob[j];
+      for (int j = 0; j < EPL; ++j) probs[tid >> 4][expert_of<DT, EPL, RUNS>(slot, j)] = prob[j];
       wave_fence();
       float weight = e >= 0 ? probs[tid >> 4][e] : 0.0f;
       const float all = sum16(weight);
@@ -665,7 +641,7 @@ __global__ __launch_bounds__(kBwdThreads) void router_backward_kernel(Bwd p) {
     wave_fence();
     float a[EPL], dot = 0.0f, given[EPL];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) given[j] = mine[expert_of<DT, EPL>(slot, j)];
+    for (int j = 0; j < EPL; ++j) given[j] = mine[expert_of<DT, EPL, RUNS>(slot, j)];
     wave_fence();
     if (e >= 0) mine[e] = 0.0f;
     wave_fence();
@@ -690,7 +666,7 @@ hipError_t by_runs(int E, F f) {
   const std::integral_constant<int, DT> dt;
   const std::integral_constant<int, EPL> epl;
   if constexpr (EPL > 1)
-    if (E % kRun<DT, EPL> != 0) return f(dt, epl, std::false_type{});
+    if (E % kRun<DT, EPL, true> != 0) return f(dt, epl, std::false_type{});
   return f(dt, epl, std::true_type{});
 }
 template <int DT, typename F>
