@@ -127,9 +127,12 @@ struct Walk {
   }
 };
 
-// STREAM: past the caches, for outputs that the last-level cache cannot hold for the next
-// reader (16384 x 14336, forward and backward, with 16 waves a row: 332 -> 308 and 414 -> 396
-// us; 32000 x 2080, whose outputs it can hold, backward: 85 -> 92 us).
+// STREAM: past the caches, for outputs that would be written back from the last-level cache (256
+// MiB) while the next call's data comes in.  us without and with it, calls in a row into four
+// sets of outputs: 67 MB (16384 x 2048 forward) 46 and 50, 101 MB
+// (8192 x 2048 backward, all outputs) 34.3 and 33.0, 134 MB (16384 x 4096 forward) 98 and 94,
+// 266 MB (32000 x 2080 backward) 99 and 93, 470 MB (16384 x 14336 forward) 332 and 308.  (Into the
+// same outputs every time 266 MB take 82 without it: what the cache holds is written over.)
 template <bool STREAM, typename T>
 __device__ __forceinline__ void store(void* to, const T& v) {
   if constexpr (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<T*>(to));
@@ -330,7 +333,7 @@ __global__ __launch_bounds__(kMaxThreads) void swiglu_backward_kernel(Bwd p) {
 
 // Workgroups of 16 waves where there is work for the chip in them (4 where not), and as many
 // rows in each as give a wave some kRounds chunks.  16384 x 14336, forward and backward, and
-// 32000 x 2080 backward, us: 16 waves and 2 chunks each 306, 391 and 83, 3 chunks 307, 392 and
+// 32000 x 2080 backward (cached stores), us: 16 waves and 2 chunks each 306, 391 and 83, 3 chunks 307, 392 and
 // 82 (6.2, 6.0 and 6.5 TB/s), 5 chunks 323, 402 and 84, 8 chunks 344, 431 and 86; 4 waves 348,
 // 441 and 87.
 constexpr int64_t kRounds = 3;
@@ -353,7 +356,7 @@ Shape shape_of(int64_t rows_cap, int64_t f) {
   return {(int)each, (unsigned)(groups < most ? groups : most), (unsigned)(64 * waves)};
 }
 
-constexpr int64_t kCacheBytes = (int64_t)256 << 20;  // of the last level
+constexpr int64_t kStreamBytes = (int64_t)96 << 20;
 
 template <typename K, typename P>
 hipError_t run(K kernel, P p, hipStream_t stream) {
@@ -365,13 +368,13 @@ hipError_t run(K kernel, P p, hipStream_t stream) {
 
 template <bool F16, bool KEEP>
 hipError_t launch_forward(const Fwd& p, hipStream_t stream) {
-  if (2 * p.rows_cap * p.f > kCacheBytes) return run(swiglu_kernel<F16, KEEP, true>, p, stream);
+  if (2 * p.rows_cap * p.f >= kStreamBytes) return run(swiglu_kernel<F16, KEEP, true>, p, stream);
   return run(swiglu_kernel<F16, KEEP, false>, p, stream);
 }
 
 template <bool F16, bool ROWSUM>
 hipError_t launch_backward(const Bwd& p, hipStream_t stream) {
-  if ((p.y != nullptr ? 6 : 4) * p.rows_cap * p.f > 2 * kCacheBytes)
+  if ((p.y != nullptr ? 6 : 4) * p.rows_cap * p.f >= kStreamBytes)
     return run(swiglu_backward_kernel<F16, ROWSUM, true>, p, stream);
   return run(swiglu_backward_kernel<F16, ROWSUM, false>, p, stream);
 }
