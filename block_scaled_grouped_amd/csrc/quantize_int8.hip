@@ -22,8 +22,9 @@ struct Args {
 };
 
 // TPR threads take a row, NC runs of 8 elements each: a row of at most 8 TPR NC elements
-// is read once (LONG: any length, read again from the caches for its integers).
-template <bool F16, int TPR, int NC, bool LONG>
+// is read once (LONG: any length, read again from the caches for its integers).  STREAM: the integers go past
+// the caches.
+template <bool F16, int TPR, int NC, bool LONG, bool STREAM>
 __global__ __launch_bounds__(kThreads) void quantize_int8_kernel(Args p) {
   constexpr int kRows = kThreads / TPR;
   __shared__ uint32_t peak[2][kThreads / 64];
@@ -83,25 +84,38 @@ __global__ __launch_bounds__(kThreads) void quantize_int8_kernel(Args p) {
           if (e < cols) v[c] = *reinterpret_cast<const v4i*>(src + e);
         }
         const v2i q = quantize8<F16>(v[c], r, finite);
-        if (e < cols) *reinterpret_cast<v2i*>(dst + e) = q;
+        if (e < cols) {
+          v2i* at = reinterpret_cast<v2i*>(dst + e);
+          if constexpr (STREAM) __builtin_nontemporal_store(q, at);
+          else *at = q;
+        }
       }
     }
   }
 }
+
+// Integers of so many bytes go past the caches: 114688 x 4096 (470 MB) 224 us without and 216 with
+// it (6.5 TB/s), the tokens and the product of 32768 x 7168 (242 MB) 560 and 556, of 16384 x 4096
+// (67 MB) 795 both.  Fewer stay there for the product that reads them.
+constexpr int64_t kStreamBytes = (int64_t)96 << 20;
 
 template <bool F16, int TPR, int NC, bool LONG>
 hipError_t launch(const Args& p, hipStream_t stream) {
   constexpr int kRows = kThreads / TPR;
   // a launch has fewer than 2^32 threads
   const int64_t blocks = (p.rows_cap + kRows - 1) / kRows, most = (int64_t)1 << 23;
-  hipLaunchKernelGGL((quantize_int8_kernel<F16, TPR, NC, LONG>),
-                     dim3((unsigned)(blocks < most ? blocks : most)),
-                     dim3(kThreads), 0, stream, p);
-  return hipGetLastError();
+  const auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(kThreads), 0,
+                       stream, p);
+    return hipGetLastError();
+  };
+  return p.rows_cap * p.cols >= kStreamBytes
+             ? run(quantize_int8_kernel<F16, TPR, NC, LONG, true>)
+             : run(quantize_int8_kernel<F16, TPR, NC, LONG, false>);
 }
 
-// 256 threads a row from 2048 columns on: 114688 x 4096 227 us (6.2 TB/s), with 512 threads 279;
-// 32768 x 7168 121 us, with 512 threads 126, with 1024 166.
+// 256 threads a row from 2048 columns on: 114688 x 4096 227 us, with 512 threads 279;
+// 32768 x 7168 121 us, with 512 threads 126, with 1024 166 (cached stores).
 template <bool F16>
 hipError_t launch_type(const Args& p, hipStream_t stream) {
   if (p.cols <= 512) return launch<F16, 64, 1, false>(p, stream);
