@@ -538,8 +538,9 @@ def gemm_workspace(device=None):
     grouped_gemm_nvfp4_workspace_size(), grouped_gemm_16bit_workspace_size()) bytes
     (256-byte aligned: torch's caching allocator aligns blocks to 512), for the
     `workspace` argument of grouped_gemm_mxfp8, grouped_gemm_nvfp4_rowscaled,
-    grouped_gemm_nvfp4_pertensor and grouped_gemm_16bit.  Calls that may run at the
-    same time (on different streams) need a workspace each."""
+    grouped_gemm_nvfp4_pertensor, grouped_gemm_16bit and grouped_gemm_int8 (which needs
+    as much as grouped_gemm_16bit).  Calls that may run at the same time (on different
+    streams) need a workspace each."""
     import torch
     lib = load_library()
     n = max(int(lib.grouped_gemm_mxfp8_workspace_size()),

@@ -23,12 +23,11 @@
 // next in order: where that happens among a token's k + 1 largest the wave does it again,
 // on whole values.
 //
-// What bounds it: the forward pass the vector units (0.7 of their time busy before the last steps;
-// some 480 instructions for a wave's four tokens of 256 experts), the backward pass HBM.  65536
-// float32 tokens of 256 experts, k 8: forward 25.4 us (67 MB; some 3 of them until the first
-// tokens are there), adding up 4.8, backward 27.4 (139 MB at 5.1 TB/s).  16384 bf16 tokens of 64
-// experts 5.9, 4.6 and 5.7; 64 of 8 3.5 in one launch.  Two workgroups a compute unit (forward)
-// are slower: 35 us.
+// What bounds it: the forward pass the vector units (busy 0.77 of the time; 545 instructions for a
+// wave's four tokens of 256 experts), the backward pass HBM.  65536 float32 tokens of 256 experts,
+// k 8: forward 25 us (67 MB; some 3 of them until the first tokens are there), adding up 4.7,
+// backward 27.4 (139 MB at 5.1 TB/s).  16384 bf16 tokens of 64 experts 5.9, 4.6 and 5.7; 64 of 8
+// 3.5 in one launch.  Two workgroups a compute unit (forward) are slower: 35 us.
 #include <type_traits>
 
 #include "bsg_internal.h"

@@ -129,10 +129,10 @@ struct Walk {
 
 // STREAM: past the caches, for outputs that would be written back from the last-level cache (256
 // MiB) while the next call's data comes in.  us without and with it, calls in a row into four
-// sets of outputs: 67 MB (16384 x 2048 forward) 46 and 50, 101 MB
-// (8192 x 2048 backward, all outputs) 34.3 and 33.0, 134 MB (16384 x 4096 forward) 98 and 94,
-// 266 MB (32000 x 2080 backward) 99 and 93, 470 MB (16384 x 14336 forward) 332 and 308.  (Into the
-// same outputs every time 266 MB take 82 without it: what the cache holds is written over.)
+// sets of outputs: 67 MB (16384 x 2048 forward) 46 and 50, 101 MB (8192 x 2048 backward, all
+// outputs) 34.3 and 33.0, 134 MB (16384 x 4096 forward) 98 and 94, 266 MB (32000 x 2080
+// backward) 99 and 93, 470 MB (16384 x 14336 forward) 332 and 308.  (Into the same outputs every
+// time 266 MB take 82 without it: what the cache holds is written over.)
 template <bool STREAM, typename T>
 __device__ __forceinline__ void store(void* to, const T& v) {
   if constexpr (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<T*>(to));
@@ -333,9 +333,9 @@ __global__ __launch_bounds__(kMaxThreads) void swiglu_backward_kernel(Bwd p) {
 
 // Workgroups of 16 waves where there is work for the chip in them (4 where not), and as many
 // rows in each as give a wave some kRounds chunks.  16384 x 14336, forward and backward, and
-// 32000 x 2080 backward (cached stores), us: 16 waves and 2 chunks each 306, 391 and 83, 3 chunks 307, 392 and
-// 82 (6.2, 6.0 and 6.5 TB/s), 5 chunks 323, 402 and 84, 8 chunks 344, 431 and 86; 4 waves 348,
-// 441 and 87.
+// 32000 x 2080 backward (cached stores, the same outputs every time), us: 16 waves and 2 chunks
+// each 306, 391 and 83, 3 chunks 307, 392 and 82 (6.2, 6.0 and 6.5 TB/s), 5 chunks 323, 402 and
+// 84, 8 chunks 344, 431 and 86; 4 waves 348, 441 and 87.
 constexpr int64_t kRounds = 3;
 
 struct Shape {
