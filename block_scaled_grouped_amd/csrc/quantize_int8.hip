@@ -22,8 +22,8 @@ struct Args {
 };
 
 // TPR threads take a row, NC runs of 8 elements each: a row of at most 8 TPR NC elements
-// is read once (LONG: any length, read again from the caches for its integers).  STREAM: the integers go past
-// the caches.
+// is read once (LONG: any length, read again from the caches for its integers).  STREAM: the
+// integers go past the caches.
 template <bool F16, int TPR, int NC, bool LONG, bool STREAM>
 __global__ __launch_bounds__(kThreads) void quantize_int8_kernel(Args p) {
   constexpr int kRows = kThreads / TPR;

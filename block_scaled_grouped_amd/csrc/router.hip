@@ -97,8 +97,8 @@ __device__ __forceinline__ float decode16(uint32_t bits) {
 }
 // A lane's experts: runs of kRun, a run of the 16 lanes after the other.  RUNS: the experts are
 // whole runs of 16 bytes (or what a lane has); else runs of one, which neighbouring lanes load and
-// store next to each other (65536 x 250 float32: forward 36 and backward 49 us with runs of four taken
-// one by one, now 26 and 27).
+// store next to each other (65536 x 250 float32: forward 36 and backward 49 us with runs of four
+// taken one by one, now 26 and 27).
 template <int DT, int EPL, bool RUNS>
 constexpr int kRun = !RUNS ? 1 : EPL < 16 / kBytes<DT> ? EPL : 16 / kBytes<DT>;
 template <int DT, int EPL, bool RUNS>
@@ -715,7 +715,8 @@ hipError_t launch_router(int dtype, const void* logits, int64_t ld, int64_t toke
   const int64_t want = (tokens + kFwdTokens - 1) / kFwdTokens;
   const int blocks = tokens <= kOneBlock ? 1 : (int)(want < kFwdBlocks ? want : kFwdBlocks);
   const hipError_t e = by_type(dtype, E, [&](auto dt, auto epl, auto runs) {
-    hipLaunchKernelGGL((router_kernel<decltype(dt)::value, decltype(epl)::value, decltype(runs)::value>), dim3(blocks),
+    constexpr int DT = decltype(dt)::value, EPL = decltype(epl)::value;
+    hipLaunchKernelGGL((router_kernel<DT, EPL, decltype(runs)::value>), dim3(blocks),
                        dim3(kFwdThreads), 0, stream, p);
     return hipGetLastError();
   });
@@ -745,8 +746,9 @@ hipError_t launch_router_backward(int dtype, const void* logits, int64_t ld, int
   const int64_t cap = 4 * (int64_t)device_cu_count();
   const unsigned blocks = (unsigned)(want < cap ? want : cap);
   return by_type(dtype, E, [&](auto dt, auto epl, auto runs) {
-    hipLaunchKernelGGL((router_backward_kernel<decltype(dt)::value, decltype(epl)::value, decltype(runs)::value>),
-                       dim3(blocks), dim3(kBwdThreads), 0, stream, p);
+    constexpr int DT = decltype(dt)::value, EPL = decltype(epl)::value;
+    hipLaunchKernelGGL((router_backward_kernel<DT, EPL, decltype(runs)::value>), dim3(blocks),
+                       dim3(kBwdThreads), 0, stream, p);
     return hipGetLastError();
   });
 }
