@@ -19,6 +19,8 @@
 // lowest eight replaced by 255 - index.  Keys differ, so the next largest below M is the
 // one with the largest key - M (unsigned: those at or above M come out smallest), which
 // takes a subtraction and half a three-way maximum each, and no search for an index.
+// Only the differences compare so: M is added back after the maximum over the lanes, for
+// a lane with nothing below M would come out with a key at or above it.
 // A 16-bit logit has its bits above those eight.  A float32 one may share them with the
 // next in order: where that happens among a token's k + 1 largest the wave does it again,
 // on whole values.
@@ -220,11 +222,11 @@ __device__ __forceinline__ int choose(uint32_t (&key)[EPL], int slot, int E, int
   // float32: one more than is chosen, which shows whether the last is next to another
   const int rounds = DT == 2 && k < E ? k + 1 : k;
   uint32_t mine = 0, m = 0;
-  const auto below = [&](uint32_t top) {  // the largest key below `top`
+  const auto below = [&](uint32_t top) {  // the token's largest key below `top`
     uint32_t d[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) d[j] = key[j] - top;
-    return max_of(d) + top;
+    return max16u(max_of(d)) + top;
   };
   bool all = EPL > H && rounds > kFewRounds;
   if (!all) {
@@ -258,7 +260,7 @@ __device__ __forceinline__ int choose(uint32_t (&key)[EPL], int slot, int E, int
     m = max16u(max_of(key));
     mine = m;
     for (int r = 1; r < rounds; ++r) {
-      m = max16u(below(m));
+      m = below(m);
       mine = slot == r ? m : mine;
     }
   }
