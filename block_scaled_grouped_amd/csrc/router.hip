@@ -189,7 +189,8 @@ __device__ __forceinline__ uint32_t order(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ float closed_if_nan(float v) { return fmaxf(v, -INFINITY); }
+// by comparison: of a signalling NaN a maximum of three is a NaN
+__device__ __forceinline__ float closed_if_nan(float v) { return v == v ? v : -INFINITY; }
 
 // The middle one of a >= b and x: where x goes among them, b or what b makes room for.
 __device__ __forceinline__ uint32_t middle(uint32_t a, uint32_t b, uint32_t x) {
@@ -298,7 +299,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // A token's softmax: exp(l - max) in ex, what they have to be multiplied by, and whether it is
 // live.  Without an open expert the sum of the exponentials is 0 (max stands for 0 then), with
-// a NaN or +inf it is NaN.
+// a NaN or +inf it is NaN: close_if_all_nan has to follow where a wave has such a token.
 struct Softmax {
   float max, sum, inv;
   bool live;
@@ -323,6 +324,20 @@ __device__ __forceinline__ Softmax softmax(const float (&v)[EPL], float (&ex)[EP
   r.live = !(r.sum == 0.0f);
   r.inv = r.live ? 1.0f / r.sum : 0.0f;
   return r;
+}
+
+// A token with a NaN and no open expert is not live: ex is 0, and only the sum tells of the NaN.
+template <int EPL>
+__device__ __forceinline__ void close_if_all_nan(const float (&v)[EPL], float (&ex)[EPL],
+                                                 Softmax& r) {
+  float open = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) open = fmaxf(open, closed_if_nan(v[j]));
+  if (max16(open) > -INFINITY || r.sum == 0.0f) return;
+  r.live = false;
+  r.inv = 0.0f;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) ex[j] = 0.0f;
 }
 
 // ---------------------------------------------------------------- forward
@@ -405,7 +420,7 @@ __global__ __launch_bounds__(kFwdThreads) void router_kernel(Fwd p) {
     float ex[EPL];
     uint32_t key[EPL];
     close_absent<DT, EPL, RUNS>(v, routed, slot, E);
-    const Softmax sm = softmax(v, ex);
+    Softmax sm = softmax(v, ex);
     const bool here = routed, nonfinite = !(sm.sum < INFINITY);
     bad |= nonfinite;
     const auto key_of = [&](float x, int j) {
@@ -414,6 +429,7 @@ __global__ __launch_bounds__(kFwdThreads) void router_kernel(Fwd p) {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) key[j] = key_of(v[j], j);
     if (__any(nonfinite)) {
+      close_if_all_nan(v, ex, sm);
 #pragma unroll
       for (int j = 0; j < EPL; ++j) key[j] = key_of(closed_if_nan(v[j]), j);
     }
@@ -624,7 +640,8 @@ __global__ __launch_bounds__(kBwdThreads) void router_backward_kernel(Bwd p) {
     const int e = next_e >= 0 && next_e < E ? next_e : -1;
     const float dw = e >= 0 ? next_dw : 0.0f;
     close_absent<DT, EPL, RUNS>(v, routed, slot, E);
-    const Softmax sm = softmax(v, prob);
+    Softmax sm = softmax(v, prob);
+    if (__any(!(sm.sum < INFINITY))) close_if_all_nan(v, prob, sm);
     load(t + stride);
 #pragma unroll
     for (int j = 0; j < EPL; ++j) prob[j] *= sm.inv;

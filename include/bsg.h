@@ -742,9 +742,10 @@ int clip_grad_norm(const void* plan, int64_t num_chunks, float max_norm, const d
  *   loss = E / (top_k n^2) * sum_e counts[e] prob_sums[e]  (0 without a live token):
  *          E times the sum of an expert's share of the slots times its mean probability,
  *          1 where both are even.
- * Tokens that are not live get -1 and 0.  A live token with a NaN or +inf has p NaN (the
- * formula's), which reaches its weights, prob_sums and loss; *dev_status gets
- * BSG_DEV_NONFINITE.
+ * Tokens that are not live get -1 and 0, those whose logits are all NaN or -inf among them.
+ * A live token with a NaN or +inf has p NaN (the formula's), which reaches its weights,
+ * prob_sums and loss.  Either sets BSG_DEV_NONFINITE in *dev_status: a NaN in a token that
+ * the mask lets pass, or a +inf.
  *
  *   in_dtype    BSG_IN_BF16, BSG_IN_F16 or BSG_IN_F32.
  *   logits      [tokens, E], ld >= E elements between rows, aligned to its elements.
