@@ -204,7 +204,10 @@ __device__ __forceinline__ void contract(Copies<MODE>& c, uint32_t lds, int w, i
 // alone would (a contraction is half as long as a 16-bit one's, and the end of a tile, copies and
 // then stores, took 13 000 of its 87 000 cycles at k = 4096).  scales: of the tile's rows, then
 // of its columns, in LDS.
-// WHOLE: the tile has all its columns, so that a store's place is a lane's and a uniform offset.
+// WHOLE: the tile has all its columns, so that a store's place is the row of blocks' and a constant.
+// All of it is in the lane's offset: of the scalar one the compiler's description of these stores
+// says that the range check, which drops the rows past the tile's, leaves it out.  (Rows in the
+// scalar offset save an addition a row of blocks, and no time.)
 template <bool F16, bool F32, bool WHOLE, bool MORE>
 __device__ __forceinline__ void store_int8(const v4f (&acc)[8][8], const OutTile& o,
                                            const float* scales, int wrow, int wcol, int w,
@@ -215,7 +218,7 @@ __device__ __forceinline__ void store_int8(const v4f (&acc)[8][8], const OutTile
   asm volatile("" : "+s"(ldo));  // keeps all the store offsets from being hoisted
   const __amdgpu_buffer_rsrc_t ro = make_rsrc(o.out, (int64_t)o.rows * o.ldo * esz);
   const int q = lane >> 4, row = wrow + (lane & 15);
-  const int place = (row * ldo + wcol + 16 * (q & 1) + 8 * (q >> 1)) * 2;
+  int place = (row * ldo + wcol + 16 * (q & 1) + 8 * (q >> 1)) * 2;
   v4f cscale[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -246,13 +249,13 @@ __device__ __forceinline__ void store_int8(const v4f (&acc)[8][8], const OutTile
       }
       if constexpr (MORE) c.template copy_end<P % kCopies>(voff);
       if constexpr (WHOLE) {
-        __builtin_amdgcn_raw_buffer_store_b128(swap_pair<F16>(y0, y1), ro, place + 32 * j,
-                                               32 * i * ldo, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(swap_pair<F16>(y0, y1), ro, place + 32 * j, 0, 0);
       } else {
         store_pair<F32, F16>(y0, y1, ro, ldo, row + 16 * i, wcol + 16 * j, q, o.cols);
       }
       fence();
     });
+    if constexpr (WHOLE) place += 32 * ldo;
   });
 }
 
