@@ -45,3 +45,13 @@ def test_rows_outside_of_the_groups(case):
 @pytest.mark.gpu
 def test_the_cases_take_every_form():
     assert {f for case in CASES for f in _forms(case)} == {16, 32, 64, 128, 256}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,n,k,with_workspace,without", [
+    (2048, 4096, 2048, 256, 256), (1500, 4104, 2064, 128, 128), (700, 2056, 1040, 32, 32), (200, 2048, 4096, 32, 32),
+    (40, 2048, 4096, 32, 32)])
+def test_forms_of_uneven_groups(rows, n, k, with_workspace, without):
+    """Those of test_gpu_int8.test_forms, which runs them."""
+    assert [bsg.grouped_gemm_int8_tile_rows(3, rows + 3, n, k, workspace=w) for w in (True, False)] == [
+        with_workspace, without]
