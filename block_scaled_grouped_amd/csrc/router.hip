@@ -25,11 +25,13 @@
 // next in order: where that happens among a token's k + 1 largest the wave does it again,
 // on whole values.
 //
-// What bounds it: the forward pass the vector units (busy 0.77 of the time; 545 instructions for a
+// What bounds it: the forward pass the vector units (busy 0.76 of the time; 550 instructions for a
 // wave's four tokens of 256 experts), the backward pass HBM.  65536 float32 tokens of 256 experts,
 // k 8: forward 25 us (67 MB; some 3 of them until the first tokens are there), adding up 4.7,
-// backward 27.4 (139 MB at 5.1 TB/s).  16384 bf16 tokens of 64 experts 5.9, 4.6 and 5.7; 64 of 8
-// 3.5 in one launch.  Two workgroups a compute unit (forward) are slower: 35 us.
+// backward 27.7 (139 MB at 5.0 TB/s).  16384 bf16 tokens of 64 experts 5.9, 4.6 to 5.0 and 5.7; 64 of
+// 8 3.6 in one launch.  Two workgroups a compute unit (forward) are slower: 35 us.  Float32 tokens of
+// 129 to 256 experts in runs of one take all 128 registers and spill five more (forward, the only
+// form that does).
 #include <type_traits>
 
 #include "bsg_internal.h"

@@ -336,6 +336,11 @@ __global__ __launch_bounds__(kMaxThreads) void swiglu_backward_kernel(Bwd p) {
 // 32000 x 2080 backward (cached stores, the same outputs every time), us: 16 waves and 2 chunks
 // each 306, 391 and 83, 3 chunks 307, 392 and 82 (6.2, 6.0 and 6.5 TB/s), 5 chunks 323, 402 and
 // 84, 8 chunks 344, 431 and 86; 4 waves 348, 441 and 87.
+// Less work than the chip takes at once, rows of more than 4 chunks, us with 16 and with 4 waves,
+// forward and backward in a graph: 64 x 14336 5.1 and 5.7 against 7.7 and 8.0, 64 x 8192 4.1 and 4.7
+// against 5.2 and 5.7, 1 x 2560 2.8 and 3.4 against 3.2 and 3.7.  Up to 8 chunks 4 waves win from some
+// rows on (64 x 4096 3.6 and 4.2 against 3.9 and 4.6), and many rows' backward pass does at any
+// length (1024 x 2560 6.5 against 9.1, 400 x 8192 8.0 against 9.1).
 constexpr int64_t kRounds = 3;
 
 struct Shape {
